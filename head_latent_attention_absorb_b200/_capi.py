@@ -26,6 +26,12 @@ class MLADims(ctypes.Structure):
     _fields_ = [("n_h", c_i32), ("d_c", c_i32), ("d_r", c_i32), ("d_h", c_i32), ("d_v", c_i32)]
 
 
+class MLARows(ctypes.Structure):
+    _fields_ = [("base", c_vp), ("bstride", c_i64), ("rstride", c_i64), ("row_bytes", c_i32)]
+
+
+MAX_PLANES = 4
+
 # name -> (restype, argtypes), in the order of include/mla_api.h
 SIGNATURES = {
     "mla_abi_version": (c_i32, []),
@@ -62,6 +68,25 @@ SIGNATURES = {
                                   c_f32, c_i32, c_vp, c_vp, c_sz, c_vp]),
     "mla_cache_append": (c_i32, [MLADims, c_i32, c_i32, c_vp, c_i64, c_vp, c_f32, c_f32, c_vp, c_i32,
                                  c_vp, c_i64, c_i64, c_vp, c_i64, c_i64, c_vp, c_vp]),
+    "mla_cache_append_at": (c_i32, [MLADims, c_i32, c_i32, c_vp, c_i64, c_vp, c_f32, c_f32, c_vp, c_vp, c_i32,
+                                    c_vp, c_i64, c_i64, c_vp, c_i64, c_i64, c_vp, c_vp]),
+    "mla_cache_append_fp4": (c_i32, [MLADims, c_i32, c_i32, c_i32, c_vp, c_i64, c_i64, c_vp, c_f32, c_f32, c_f32,
+                                     c_vp, c_vp, c_vp, c_i32, c_vp, c_i64, c_i64, c_vp, c_i64, c_i64,
+                                     c_vp, c_i64, c_i64, c_vp, c_vp]),
+    "mla_cache_read_fp4": (c_i32, [MLADims, c_i32, c_i32, c_i32, c_vp, c_vp, c_i32, c_vp, c_i64, c_i64,
+                                   c_vp, c_i64, c_i64, c_f32, c_vp, c_i64, c_i64, c_vp, c_vp]),
+    "mla_decode_fp4kv_workspace_size": (c_sz, [MLADims, c_i32, c_i32, c_i32, c_i32]),
+    "mla_decode_absorb_fp4kv": (c_i32, [MLADims, c_i32, c_i32, c_i32, c_vp, c_i64, c_vp, c_i64,
+                                        c_vp, c_i64, c_i64, c_vp, c_i64, c_i64, c_vp, c_i64, c_i64, c_f32,
+                                        c_i32, c_vp, c_f32, c_vp, c_vp, c_vp, c_sz, c_vp, c_vp]),
+    "mla_cache_weights": (c_i32, [MLADims, c_i32, c_i32, c_i32, c_vp, c_i64, c_vp, c_i64,
+                                  c_vp, c_i64, c_i64, c_vp, c_i64, c_i64,
+                                  c_i32, c_vp, c_f32, c_vp, c_vp, c_i64, c_f32, c_vp, c_i64, c_vp, c_vp]),
+    "mla_cache_weights_fp4kv": (c_i32, [MLADims, c_i32, c_i32, c_i32, c_vp, c_i64, c_vp, c_i64,
+                                        c_vp, c_i64, c_i64, c_vp, c_i64, c_i64, c_vp, c_i64, c_i64, c_f32,
+                                        c_i32, c_vp, c_f32, c_vp, c_vp, c_i64, c_f32, c_vp, c_i64, c_vp, c_vp]),
+    "mla_cache_evict": (c_i32, [c_i32, c_i32, ctypes.POINTER(MLARows), c_i32, c_vp, c_i64, c_vp, c_i32, c_i32,
+                                c_i32, c_vp, c_vp, c_vp, c_vp]),
     "mla_check_topk": (c_i32, [c_i32, c_vp, c_i32, c_vp, c_i32, c_vp, c_vp]),
     "mla_prefill_sparse_workspace_size": (c_sz, [MLADims, c_i32, c_i32, c_i32]),
     "mla_prefill_sparse": (c_i32, [MLADims, c_i32, c_i32, c_i32, c_vp, c_vp, c_i64, c_vp, c_i64, c_vp,

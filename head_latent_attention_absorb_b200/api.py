@@ -7,6 +7,7 @@ All tensors are CUDA tensors.  Strides are read from the tensors, so a packed
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional, Sequence
 
@@ -60,6 +61,93 @@ def _headrows(t: torch.Tensor, name: str) -> int:
 
 def _dims(x: Sequence[int]) -> MLADims:
     return x if isinstance(x, MLADims) else MLADims(*x)
+
+
+def _i32(t: torch.Tensor, shape, name: str):
+    if t.dtype != torch.int32 or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise TypeError(f"{name} must be a contiguous int32 {list(shape)} tensor")
+
+
+def _shape(t: torch.Tensor, shape, dtype: torch.dtype, name: str):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    if t.shape[-1] > 1:
+        _rows(t, name)
+
+
+def _on_device(*tensors) -> torch.device:
+    """The one CUDA device that all the tensors (None: absent) live on."""
+    ts = [t for t in tensors if t is not None]
+    for t in ts:
+        if not t.is_cuda:
+            raise ValueError("expected a CUDA tensor")
+        if t.device != ts[0].device:
+            raise ValueError(f"tensors on two devices: {ts[0].device} and {t.device}")
+    return ts[0].device
+
+
+@contextlib.contextmanager
+def _entered(stream):
+    with torch.cuda.stream(stream):
+        yield
+
+
+def _launch_on(stream, device: torch.device):
+    """(context, handle) of a call: inside the context the tensors' device is current, and so is the
+    stream, so that what the call allocates belongs to the stream that uses it."""
+    cur = torch.cuda.current_stream(device)
+    if stream is None:
+        stream = cur
+    elif not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    if stream.cuda_stream == cur.cuda_stream and device.index == torch.cuda.current_device():
+        return contextlib.nullcontext(), cur.cuda_stream
+    return _entered(stream), stream.cuda_stream
+
+
+def _flag(dev_err: Optional[torch.Tensor]):
+    if dev_err is not None and (dev_err.dtype != torch.int32 or dev_err.numel() < 1):
+        raise TypeError("dev_err must be an int32 tensor")
+
+
+def _fp4_planes(d: MLADims, c4: torch.Tensor, kv_scale: torch.Tensor, k_r: Optional[torch.Tensor],
+                dtype: Optional[torch.dtype]):
+    """Shapes of a 4-bit cache; returns (B, n_max)."""
+    if c4.dim() != 3:
+        raise ValueError("c4 must be [B, n_max, d_c / 2]")
+    B, n_max = c4.shape[0], c4.shape[1]
+    _shape(c4, (B, n_max, d.d_c // 2), torch.uint8, "c4")
+    _shape(kv_scale, (B, n_max, d.d_c // 16), torch.uint8, "kv_scale")
+    if k_r is not None:
+        _shape(k_r, (B, n_max, d.d_r), dtype, "k_r")
+    return B, n_max
+
+
+def _token_rows(q: torch.Tensor, name: str) -> torch.Tensor:
+    """[B, T, n_h, w] as [B * T, n_h, w] without a copy."""
+    if q.dim() == 3:
+        return q
+    try:
+        return q.view(-1, q.shape[2], q.shape[3])
+    except RuntimeError:
+        raise ValueError(f"{name}: the tokens of consecutive sequences must be evenly strided") from None
+
+
+def _queries(d: MLADims, q_tilde: torch.Tensor, q_pe: torch.Tensor, B: int, n_max: int, lengths: torch.Tensor):
+    """Query tensors [B, n_h, .] or [B, T, n_h, .] as rows; returns (T, q_tilde, ldqt, q_pe, ldqp)."""
+    if q_tilde.dim() not in (3, 4):
+        raise ValueError("q_tilde must be [B, n_h, d_c] or [B, T, n_h, d_c]")
+    lead = tuple(q_tilde.shape[:-2])
+    T = 1 if len(lead) == 1 else lead[1]
+    _shape(q_tilde, (*lead, d.n_h, d.d_c), q_tilde.dtype, "q_tilde")
+    _shape(q_pe, (*lead, d.n_h, d.d_r), q_tilde.dtype, "q_pe")
+    if lead[0] != B:
+        raise ValueError(f"q_tilde holds {lead[0]} sequences, the cache {B}")
+    _i32(lengths, (B,), "lengths")
+    qt, qp = _token_rows(q_tilde, "q_tilde"), _token_rows(q_pe, "q_pe")
+    return T, qt, _headrows(qt, "q_tilde"), qp, _headrows(qp, "q_pe")
 
 
 def mla_absorb_q(dims, q_nope: torch.Tensor, w_kv_b: torch.Tensor, q_tilde: Optional[torch.Tensor] = None,
@@ -311,11 +399,13 @@ def mla_prefill_naive(dims, q: torch.Tensor, c_kv: torch.Tensor, k_r: torch.Tens
 
 def mla_cache_append(dims, kv_a: torch.Tensor, positions: torch.Tensor, c_kv: torch.Tensor, k_r: torch.Tensor,
                      gain: Optional[torch.Tensor] = None, eps: float = 1e-6, rope_base: float = 10000.0,
-                     dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
+                     dev_err: Optional[torch.Tensor] = None, stream=None,
+                     rows: Optional[torch.Tensor] = None) -> None:
     """Write each sequence's new token into the caches in place: RMSNorm(kv_a[b, :d_c]) * gain into
     c_kv[b, positions[b]] and the rotary key kv_a[b, d_c:] rotated by positions[b] into
     k_r[b, positions[b]].  kv_a [B, d_c + d_r] (rows may be strided); positions int32 [B];
-    c_kv [B, n_max, d_c] and k_r [B, n_max, d_r] may be views of one packed cache; gain fp32 [d_c]."""
+    c_kv [B, n_max, d_c] and k_r [B, n_max, d_r] may be views of one packed cache; gain fp32 [d_c].
+    rows int32 [B] gives the cache rows apart from the positions (a cache whose rows were evicted)."""
     d = _dims(dims)
     B, n_max = c_kv.shape[0], c_kv.shape[1]
     _rows(kv_a, "kv_a")
@@ -327,10 +417,17 @@ def mla_cache_append(dims, kv_a: torch.Tensor, positions: torch.Tensor, c_kv: to
         raise TypeError("positions must be a contiguous int32 tensor")
     if gain is not None and (gain.dtype != torch.float32 or not gain.is_contiguous()):
         raise TypeError("gain must be a contiguous float32 tensor")
-    check(lib().mla_cache_append(d, _dt(kv_a), B, _ptr(kv_a), kv_a.stride(0), _ptr(gain), float(eps),
-                                 float(rope_base), _ptr(positions), n_max,
-                                 _ptr(c_kv), c_kv.stride(0), c_kv.stride(1), _ptr(k_r), k_r.stride(0),
-                                 k_r.stride(1), _ptr(dev_err), _stream(stream)), "mla_cache_append")
+    if rows is None:
+        check(lib().mla_cache_append(d, _dt(kv_a), B, _ptr(kv_a), kv_a.stride(0), _ptr(gain), float(eps),
+                                     float(rope_base), _ptr(positions), n_max,
+                                     _ptr(c_kv), c_kv.stride(0), c_kv.stride(1), _ptr(k_r), k_r.stride(0),
+                                     k_r.stride(1), _ptr(dev_err), _stream(stream)), "mla_cache_append")
+        return
+    _i32(rows, (B,), "rows")
+    check(lib().mla_cache_append_at(d, _dt(kv_a), B, _ptr(kv_a), kv_a.stride(0), _ptr(gain), float(eps),
+                                    float(rope_base), _ptr(positions), _ptr(rows), n_max,
+                                    _ptr(c_kv), c_kv.stride(0), c_kv.stride(1), _ptr(k_r), k_r.stride(0),
+                                    k_r.stride(1), _ptr(dev_err), _stream(stream)), "mla_cache_append_at")
 
 
 def mla_check_topk(topk_idx: torch.Tensor, n_max: int, lengths: Optional[torch.Tensor] = None,
@@ -375,6 +472,225 @@ def mla_prefill_sparse(dims, q: torch.Tensor, c_kv: torch.Tensor, k_r: torch.Ten
                                    _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_err),
                                    _stream(stream)), "mla_prefill_sparse")
     return out
+
+
+def mla_cache_append_fp4(dims, kv_a: torch.Tensor, positions: torch.Tensor, c4: torch.Tensor, kv_scale: torch.Tensor,
+                         k_r: torch.Tensor, rows: Optional[torch.Tensor] = None,
+                         counts: Optional[torch.Tensor] = None, gain: Optional[torch.Tensor] = None,
+                         eps: float = 1e-6, rope_base: float = 10000.0, latent_scale: float = 1.0,
+                         dev_err: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Write new tokens into a 4-bit latent cache in place: E2M1 codes of RMSNorm(latent) * gain with an
+    E4M3 scale per 16 features, and the rotary key.  kv_a [B, d_c + d_r] or [B, T, d_c + d_r];
+    positions int32 [B], the position of each sequence's first token; rows int32 [B], its cache row
+    (None: the position); counts int32 [B], tokens of each sequence (None: all T).  c4 uint8
+    [B, n_max, d_c / 2], kv_scale uint8 [B, n_max, d_c / 16] and k_r [B, n_max, d_r] may be views of one
+    packed row.  latent_scale: a power of two, the same for every call on the cache."""
+    d = _dims(dims)
+    B, n_max = _fp4_planes(d, c4, kv_scale, k_r, kv_a.dtype)
+    if kv_a.dim() not in (2, 3):
+        raise ValueError("kv_a must be [B, d_c + d_r] or [B, T, d_c + d_r]")
+    T = kv_a.shape[1] if kv_a.dim() == 3 else 1
+    x = kv_a if kv_a.dim() == 3 else kv_a.unsqueeze(1)
+    _shape(x, (B, T, d.d_c + d.d_r), kv_a.dtype, "kv_a")
+    _i32(positions, (B,), "positions")
+    if rows is not None:
+        _i32(rows, (B,), "rows")
+    if counts is not None:
+        _i32(counts, (B,), "counts")
+    if gain is not None:
+        _shape(gain, (d.d_c,), torch.float32, "gain")
+    _flag(dev_err)
+    dev = _on_device(kv_a, positions, c4, kv_scale, k_r, rows, counts, gain, dev_err)
+    on, st = _launch_on(stream, dev)
+    with on:
+        check(lib().mla_cache_append_fp4(
+            d, _dt(kv_a), B, T, _ptr(x), x.stride(0), x.stride(1) if T > 1 else d.d_c + d.d_r, _ptr(gain), float(eps),
+            float(rope_base), float(latent_scale), _ptr(positions), _ptr(rows), _ptr(counts), n_max,
+            _ptr(c4), c4.stride(0), c4.stride(1), _ptr(kv_scale), kv_scale.stride(0), kv_scale.stride(1),
+            _ptr(k_r), k_r.stride(0), k_r.stride(1), _ptr(dev_err), st), "mla_cache_append_fp4")
+
+
+def mla_cache_read_fp4(dims, c4: torch.Tensor, kv_scale: torch.Tensor, n: int, first: Optional[torch.Tensor] = None,
+                       counts: Optional[torch.Tensor] = None, latent_scale: float = 1.0,
+                       dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                       dev_err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The values of n latent rows per sequence of a 4-bit cache, from row first[b] on (int32 [B]; None: 0):
+    out [B, n, d_c], zeros from counts[b] on (int32 [B]; None: n)."""
+    d = _dims(dims)
+    B, n_max = _fp4_planes(d, c4, kv_scale, None, None)
+    if out is not None:
+        _shape(out, (B, n, d.d_c), out.dtype, "out")
+    code = _dtc(dtype if out is None else out.dtype)
+    if first is not None:
+        _i32(first, (B,), "first")
+    if counts is not None:
+        _i32(counts, (B,), "counts")
+    _flag(dev_err)
+    dev = _on_device(c4, kv_scale, out, first, counts, dev_err)
+    on, st = _launch_on(stream, dev)
+    with on:
+        if out is None:
+            out = torch.empty((B, n, d.d_c), dtype=dtype, device=dev)
+        check(lib().mla_cache_read_fp4(
+            d, code, B, n, _ptr(first), _ptr(counts), n_max, _ptr(c4), c4.stride(0), c4.stride(1),
+            _ptr(kv_scale), kv_scale.stride(0), kv_scale.stride(1), float(latent_scale), _ptr(out), out.stride(0),
+            out.stride(1) if n > 1 else d.d_c, _ptr(dev_err), st), "mla_cache_read_fp4")
+    return out
+
+
+def mla_decode_fp4kv_workspace_size(dims, dtype: torch.dtype, B: int, T: int, n_max: int) -> int:
+    return int(lib().mla_decode_fp4kv_workspace_size(_dims(dims), _dtc(dtype), B, T, n_max))
+
+
+def mla_decode_absorb_fp4kv(dims, q_tilde: torch.Tensor, q_pe: torch.Tensor, c4: torch.Tensor, kv_scale: torch.Tensor,
+                            k_r: torch.Tensor, lengths: torch.Tensor, scale: float, latent_scale: float = 1.0,
+                            ctx: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None, dev_err: Optional[torch.Tensor] = None,
+                            stream=None) -> torch.Tensor:
+    """The absorbed decode over a 4-bit latent cache (planes as in mla_cache_append_fp4), one token per
+    sequence (q_tilde [B, n_h, d_c], q_pe [B, n_h, d_r]) or T ([B, T, n_h, .], the last T cached rows of each
+    sequence being those tokens).  Any n_h <= 128 in bf16.  Returns ctx of q_tilde's shape; lse float32
+    [B, n_h] or [B, T, n_h]."""
+    d = _dims(dims)
+    B, n_max = _fp4_planes(d, c4, kv_scale, k_r, q_tilde.dtype)
+    T, qt, ldqt, qp, ldqp = _queries(d, q_tilde, q_pe, B, n_max, lengths)
+    if ctx is not None:
+        _shape(ctx, q_tilde.shape, q_tilde.dtype, "ctx")
+    if lse is not None:
+        _shape(lse, q_tilde.shape[:-1], torch.float32, "lse")
+    if (ctx is not None and not ctx.is_contiguous()) or (lse is not None and not lse.is_contiguous()):
+        raise ValueError("ctx and lse must be contiguous")
+    _flag(dev_err)
+    dev = _on_device(q_tilde, q_pe, c4, kv_scale, k_r, lengths, ctx, lse, workspace, dev_err)
+    on, st = _launch_on(stream, dev)
+    with on:
+        if ctx is None:
+            ctx = torch.empty(q_tilde.shape, dtype=q_tilde.dtype, device=dev)
+        if workspace is None:
+            nbytes = mla_decode_fp4kv_workspace_size(d, q_tilde.dtype, B, T, n_max)
+            workspace = torch.empty((max(nbytes, 16),), dtype=torch.uint8, device=dev)
+        check(lib().mla_decode_absorb_fp4kv(
+            d, _dt(q_tilde), B, T, _ptr(qt), ldqt, _ptr(qp), ldqp, _ptr(c4), c4.stride(0), c4.stride(1),
+            _ptr(kv_scale), kv_scale.stride(0), kv_scale.stride(1), _ptr(k_r), k_r.stride(0), k_r.stride(1),
+            float(latent_scale), n_max, _ptr(lengths), float(scale), _ptr(ctx), _ptr(lse), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _ptr(dev_err), st),
+            "mla_decode_absorb_fp4kv")
+    return ctx
+
+
+def _weight_arrays(acc: Optional[torch.Tensor], out: Optional[torch.Tensor], B: int, n_max: int):
+    for t, name in ((acc, "acc"), (out, "out")):
+        if t is not None:
+            _shape(t, (B, n_max), torch.float32, name)
+
+
+def _bstride(t: Optional[torch.Tensor], n_max: int) -> int:
+    return n_max if t is None or t.shape[0] == 1 else t.stride(0)
+
+
+def mla_cache_weights(dims, q_tilde: torch.Tensor, q_pe: torch.Tensor, c_kv: torch.Tensor, k_r: torch.Tensor,
+                      lengths: torch.Tensor, scale: float, lse: torch.Tensor, acc: Optional[torch.Tensor] = None,
+                      decay: float = 1.0, out: Optional[torch.Tensor] = None,
+                      dev_err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The attention weight that each cached row received in a decode step, summed over heads and new
+    tokens, added to decay * acc (float32 [B, n_max]; the step's own T rows start from nothing).  Queries
+    [B, n_h, .] or [B, T, n_h, .]; lse is the decode's.  Returns out [B, n_max], which may be acc; entries
+    at and behind lengths[b] are left as they were (zeros when out is allocated here)."""
+    d = _dims(dims)
+    if c_kv.dim() != 3:
+        raise ValueError("c_kv must be [B, n_max, d_c]")
+    B, n_max = c_kv.shape[0], c_kv.shape[1]
+    _shape(c_kv, (B, n_max, d.d_c), q_tilde.dtype, "c_kv")
+    _shape(k_r, (B, n_max, d.d_r), q_tilde.dtype, "k_r")
+    T, qt, ldqt, qp, ldqp = _queries(d, q_tilde, q_pe, B, n_max, lengths)
+    _shape(lse, q_tilde.shape[:-1], torch.float32, "lse")
+    if not lse.is_contiguous():
+        raise ValueError("lse must be contiguous")
+    _weight_arrays(acc, out, B, n_max)
+    _flag(dev_err)
+    dev = _on_device(q_tilde, q_pe, c_kv, k_r, lengths, lse, acc, out, dev_err)
+    on, st = _launch_on(stream, dev)
+    with on:
+        if out is None:
+            out = torch.zeros((B, n_max), dtype=torch.float32, device=dev)
+        check(lib().mla_cache_weights(
+            d, _dt(q_tilde), B, T, _ptr(qt), ldqt, _ptr(qp), ldqp, _ptr(c_kv), c_kv.stride(0), c_kv.stride(1),
+            _ptr(k_r), k_r.stride(0), k_r.stride(1), n_max, _ptr(lengths), float(scale), _ptr(lse), _ptr(acc),
+            _bstride(acc, n_max), float(decay), _ptr(out), _bstride(out, n_max), _ptr(dev_err),
+            st), "mla_cache_weights")
+    return out
+
+
+def mla_cache_weights_fp4kv(dims, q_tilde: torch.Tensor, q_pe: torch.Tensor, c4: torch.Tensor, kv_scale: torch.Tensor,
+                            k_r: torch.Tensor, lengths: torch.Tensor, scale: float, lse: torch.Tensor,
+                            latent_scale: float = 1.0, acc: Optional[torch.Tensor] = None, decay: float = 1.0,
+                            out: Optional[torch.Tensor] = None, dev_err: Optional[torch.Tensor] = None,
+                            stream=None) -> torch.Tensor:
+    """mla_cache_weights over a 4-bit latent cache (planes as in mla_cache_append_fp4)."""
+    d = _dims(dims)
+    B, n_max = _fp4_planes(d, c4, kv_scale, k_r, q_tilde.dtype)
+    T, qt, ldqt, qp, ldqp = _queries(d, q_tilde, q_pe, B, n_max, lengths)
+    _shape(lse, q_tilde.shape[:-1], torch.float32, "lse")
+    if not lse.is_contiguous():
+        raise ValueError("lse must be contiguous")
+    _weight_arrays(acc, out, B, n_max)
+    _flag(dev_err)
+    dev = _on_device(q_tilde, q_pe, c4, kv_scale, k_r, lengths, lse, acc, out, dev_err)
+    on, st = _launch_on(stream, dev)
+    with on:
+        if out is None:
+            out = torch.zeros((B, n_max), dtype=torch.float32, device=dev)
+        check(lib().mla_cache_weights_fp4kv(
+            d, _dt(q_tilde), B, T, _ptr(qt), ldqt, _ptr(qp), ldqp, _ptr(c4), c4.stride(0), c4.stride(1),
+            _ptr(kv_scale), kv_scale.stride(0), kv_scale.stride(1), _ptr(k_r), k_r.stride(0), k_r.stride(1),
+            float(latent_scale), n_max, _ptr(lengths), float(scale), _ptr(lse), _ptr(acc), _bstride(acc, n_max),
+            float(decay), _ptr(out), _bstride(out, n_max), _ptr(dev_err), st),
+            "mla_cache_weights_fp4kv")
+    return out
+
+
+def mla_cache_evict(planes: Sequence[torch.Tensor], acc: torch.Tensor, lengths: torch.Tensor, keep: int,
+                    sink: int = 0, recent: int = 0, new_lengths: Optional[torch.Tensor] = None,
+                    row_map: Optional[torch.Tensor] = None, dev_err: Optional[torch.Tensor] = None, stream=None):
+    """Keep `keep` rows of every sequence that holds more: the first `sink`, the last `recent`, and the
+    heaviest of the rest by acc (float32 [B, n_max]); kept rows behind `keep` move, in place, into the rows
+    before it that go.  planes: 1 to 4 tensors [B, n_max, width] of any type whose rows move together
+    (e.g. [c_kv, k_r], [c4, kv_scale, k_r]; add acc.unsqueeze(-1) to keep it in step).  Returns
+    (new_lengths int32 [B], which may be given as lengths itself, and row_map int32 [B, keep]: the row
+    that row i held before, -1 from new_lengths[b] on)."""
+    planes = list(planes)
+    if not 1 <= len(planes) <= _capi.MAX_PLANES:
+        raise ValueError(f"need 1 to {_capi.MAX_PLANES} planes")
+    if acc.dim() != 2:
+        raise ValueError("acc must be [B, n_max]")
+    B, n_max = acc.shape
+    _shape(acc, (B, n_max), torch.float32, "acc")
+    _i32(lengths, (B,), "lengths")
+    rows = (_capi.MLARows * _capi.MAX_PLANES)()
+    for i, p in enumerate(planes):
+        if p.dim() != 3 or tuple(p.shape[:2]) != (B, n_max):
+            raise ValueError(f"plane {i} must be [B, n_max, width] = [{B}, {n_max}, .], got {list(p.shape)}")
+        if p.shape[2] > 1:
+            _rows(p, f"plane {i}")
+        es = p.element_size()
+        width = p.shape[2] * es
+        rows[i] = _capi.MLARows(p.data_ptr(), p.stride(0) * es, p.stride(1) * es if n_max > 1 else width, width)
+    if new_lengths is not None:
+        _i32(new_lengths, (B,), "new_lengths")
+    if row_map is not None:
+        _i32(row_map, (B, keep), "row_map")
+    _flag(dev_err)
+    dev = _on_device(acc, lengths, new_lengths, row_map, dev_err, *planes)
+    on, st = _launch_on(stream, dev)
+    with on:
+        if new_lengths is None:
+            new_lengths = torch.empty((B,), dtype=torch.int32, device=dev)
+        if row_map is None:
+            row_map = torch.empty((B, max(keep, 0)), dtype=torch.int32, device=dev)
+        check(lib().mla_cache_evict(B, n_max, rows, len(planes), _ptr(acc), _bstride(acc, n_max), _ptr(lengths),
+                                    int(keep), int(sink), int(recent), _ptr(new_lengths), _ptr(row_map),
+                                    _ptr(dev_err), st), "mla_cache_evict")
+    return new_lengths, row_map
 
 
 def mla_clear_device_error(dev_err: torch.Tensor, stream=None) -> None:

@@ -23,7 +23,8 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendArgs
   __shared__ float part[kAppendThreads / 32];
   const int b = blockIdx.x;
   const int pos = a.positions[b];
-  if (pos < 0 || pos >= a.n_max) {  // the row would land outside the cache: report, write nothing
+  const int dst = a.rows != nullptr ? a.rows[b] : pos;
+  if (pos < 0 || dst < 0 || dst >= a.n_max) {  // the row would land outside the cache: report, write nothing
     if (threadIdx.x == 0) raise_error(a.err, MLA_ERR_INDEX);
     return;
   }
@@ -42,7 +43,7 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendArgs
 #pragma unroll
   for (int w = 0; w < kAppendThreads / 32; ++w) tot += part[w];
   const float inv_rms = rsqrtf(tot / (float)a.d_c + a.eps);
-  T* c_dst = static_cast<T*>(a.c_kv) + (int64_t)b * a.ckv_b + (int64_t)pos * a.ckv_r;
+  T* c_dst = static_cast<T*>(a.c_kv) + (int64_t)b * a.ckv_b + (int64_t)dst * a.ckv_r;
   for (int i = threadIdx.x; i < a.d_c; i += kAppendThreads) {
     const float g = a.gain != nullptr ? a.gain[i] : 1.f;
     c_dst[i] = from_f32<T>(g * (to_f32(row[i]) * inv_rms));
@@ -50,7 +51,7 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendArgs
 
   // rotary key: pair (x[2i], x[2i+1]) rotated by pos * base^(-2i/d_r), i.e. multiplied as the
   // complex number x[2i] + j x[2i+1] by exp(j angle)
-  T* k_dst = static_cast<T*>(a.k_r) + (int64_t)b * a.kr_b + (int64_t)pos * a.kr_r;
+  T* k_dst = static_cast<T*>(a.k_r) + (int64_t)b * a.kr_b + (int64_t)dst * a.kr_r;
   const T* k_src = row + a.d_c;
   const double log_base = log((double)a.rope_base);
   for (int i = threadIdx.x; i < a.d_r / 2; i += kAppendThreads) {

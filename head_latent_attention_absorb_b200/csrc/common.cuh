@@ -86,9 +86,75 @@ struct AppendArgs {
   const void* kv_a; int64_t lda;  // [B, d_c + d_r] rows: latent first, rotary key last
   const float* gain;              // [d_c] RMSNorm gain, or nullptr for ones
   float eps, rope_base;
-  const int32_t* positions;       // [B] cache row (= position) of each new token
+  const int32_t* positions;       // [B] position of each new token
+  const int32_t* rows = nullptr;  // [B] cache row of each new token, or nullptr: row = position
   void* c_kv; int64_t ckv_b, ckv_r;
   void* k_r;  int64_t kr_b, kr_r;
+  int32_t* err;
+};
+
+// The caches an operator reads: latent rows in the element type (c_kv, strides in elements) or in
+// 4 bits (c4 codes and sc scales, strides in bytes), and the rotary rows.
+struct CacheView {
+  const void* c_kv = nullptr;  int64_t ckv_b = 0, ckv_r = 0;
+  const uint8_t* c4 = nullptr; int64_t c4_b = 0, c4_r = 0;
+  const uint8_t* sc = nullptr; int64_t sc_b = 0, sc_r = 0;
+  const void* k_r = nullptr;   int64_t kr_b = 0, kr_r = 0;
+  float latent_scale = 1.f;    // 4-bit rows: value = code * scale * latent_scale (a power of two)
+};
+
+// Validated arguments of the 4-bit decode and of the attention-weight pass: T new tokens for each of
+// B sequences, query rows ((b * T + s) * n_h + h).
+struct QueryArgs {
+  int n_h, d_c, d_r, B, T, n_max;
+  const void* q_tilde; int64_t ldqt;
+  const void* q_pe;    int64_t ldqp;
+  CacheView kv;
+  const int32_t* lengths;
+  float scale;
+  int32_t* err;
+};
+struct Fp4DecodeArgs : QueryArgs {
+  void* ctx;
+  float* lse;
+};
+struct WeightsArgs : QueryArgs {
+  const float* lse;
+  const float* acc; int64_t acc_b;  // nullptr: nothing accumulated so far
+  float decay;
+  float* out; int64_t out_b;
+};
+
+// Validated arguments of the 4-bit append (T tokens per sequence) and of the read-back.
+struct AppendFp4Args {
+  int d_c, d_r, B, T, n_max;
+  const void* kv_a; int64_t lda_b, lda;
+  const float* gain;
+  float eps, rope_base, latent_scale;
+  const int32_t* positions; const int32_t* rows; const int32_t* counts;
+  uint8_t* c4; int64_t c4_b, c4_r;
+  uint8_t* sc; int64_t sc_b, sc_r;
+  void* k_r;   int64_t kr_b, kr_r;
+  int32_t* err;
+};
+struct ReadFp4Args {
+  int d_c, B, n, n_max;
+  const int32_t* first; const int32_t* counts;
+  const uint8_t* c4; int64_t c4_b, c4_r;
+  const uint8_t* sc; int64_t sc_b, sc_r;
+  float latent_scale;
+  void* out; int64_t out_b, out_r;
+  int32_t* err;
+};
+
+// Validated arguments of the eviction: row planes with strides in bytes.
+struct EvictArgs {
+  int B, n_max, n_planes, keep, sink, recent;
+  mla_rows planes[MLA_MAX_PLANES];
+  const float* acc; int64_t acc_b;
+  const int32_t* lengths;
+  int32_t* new_lengths;
+  int32_t* row_map;
   int32_t* err;
 };
 

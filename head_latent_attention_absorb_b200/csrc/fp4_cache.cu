@@ -1,0 +1,316 @@
+// Append to and read-back from the 4-bit latent cache (the format is in fp4.cuh).
+//
+// Append ("Key-value down-projection", mla-kv excerpt; "Key-value latent RMSNorm"): for token i of
+// sequence b, x = kv_a[b, i, 0:d_c],
+//   y = g x / sqrt(mean(x^2) + eps) / latent_scale,
+//   per block of 16: s = e4m3(max|y| / 6), code = e2m1(y / s)   (nearest, ties to even, saturating)
+// and the rotary key y[2j] + j y[2j+1] turned by position * base^(-2j/d_r).
+//
+// One warp per token: lane l owns blocks l and l + 32, so the block maximum never leaves the lane, and
+// only the sum of squares crosses the warp (five shuffles).  A prompt is bound by its bytes (1152 read
+// and 416 written per bf16 token), a single token by latency.
+//
+// A 4-bit code is a step of up to a third of its value, so a value next to a rounding border has to
+// fall on the side that the formula puts it on.  The fp32 pass carries a relative error below
+// 32 * 2^-24 = 2^-19 (sum of up to 32 squares per lane and five exchanges, halved by the square root:
+// 19; reciprocal root 4; two products, the scale's reciprocal and the product with it 5).  It rounds
+// each quotient twice, moved down and up by 2^-19; where the two disagree (about one row in 150), or
+// where the sum of squares leaves fp32's safe range, the warp redoes the row in fp64.  fp64 results
+// reach the fp32 converters through round-to-odd, so the second rounding cannot undo the first.
+#include <math.h>
+
+#include "common.cuh"
+#include "fp4.cuh"
+#include "kernels.h"
+#include "sm100_ptx.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr float kDelta = 1.f / 524288.f;  // 2^-19
+
+__device__ __forceinline__ double warp_sum_f64(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// fp64 to fp32 by round-to-odd: a later rounding to few bits then equals the direct one.
+__device__ __forceinline__ float to_odd(double v) {
+  const float f = __double2float_rz(v);
+  if (f == f && (double)f != v) return __uint_as_float(__float_as_uint(f) | 1u);
+  return f;
+}
+
+// 16 consecutive elements as fp32 (bf16 rows are 16-byte aligned, fp32 rows element-aligned).
+__device__ __forceinline__ void load16(const float* p, float (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = p[i];
+}
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&x)[16]) {
+  const uint4* v = reinterpret_cast<const uint4*>(p);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint4 u = v[k];
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[8 * k + 2 * i] = __uint_as_float(w[i] << 16);
+      x[8 * k + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+}
+
+// NaN-keeping maximum of magnitudes.
+__device__ __forceinline__ float max_abs(float m, float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+  return r;
+}
+
+// One block in fp32; returns false when a rounding is too close to call.
+__device__ __forceinline__ bool quantise_fast(const float (&x)[16], const float* g, float mul, uint32_t (&code)[2],
+                                              uint32_t& s8) {
+  float y[16], m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    y[i] = x[i] * mul;
+    if (g != nullptr) y[i] *= __ldg(g + i);
+    m = max_abs(m, y[i]);
+  }
+  const float q = m * (1.f / 6.f);
+  const uint32_t s2 = fp4::to_scales(q - q * kDelta, q + q * kDelta);
+  s8 = s2 & 0xffu;
+  bool ok = s8 == (s2 >> 8);
+  const float s = fp4::scale_value(s8);
+  const float inv = s > 0.f ? 1.f / s : 0.f;  // a zero or NaN scale: all codes zero
+  code[0] = code[1] = 0u;
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {
+    const float a = y[i] * inv, b = y[i + 1] * inv;
+    const uint32_t lo = fp4::to_codes(a - a * kDelta, b - b * kDelta);
+    ok &= lo == fp4::to_codes(a + a * kDelta, b + b * kDelta);
+    code[i >> 3] |= lo << (4 * (i & 7));
+  }
+  return ok;
+}
+
+// One block in fp64.
+__device__ __noinline__ void quantise_exact(const float (&x)[16], const float* g, double mul, double unscale,
+                                            uint32_t (&code)[2], uint32_t& s8) {
+  double m = 0.0;
+  bool nan = false;
+  for (int i = 0; i < 16; ++i) {
+    double y = (double)x[i] * mul;
+    if (g != nullptr) y *= (double)g[i];
+    y *= unscale;
+    nan |= y != y;
+    m = fmax(m, fabs(y));
+  }
+  const float q = nan ? nanf("") : to_odd(m / 6.0);
+  s8 = fp4::to_scales(q, q) & 0xffu;
+  const double s = (double)fp4::scale_value(s8);
+  code[0] = code[1] = 0u;
+  if (!(s > 0.0)) return;
+  for (int i = 0; i < 16; i += 2) {
+    float r[2];
+    for (int k = 0; k < 2; ++k) {
+      double y = (double)x[i + k] * mul;
+      if (g != nullptr) y *= (double)g[i + k];
+      r[k] = to_odd(y * unscale / s);
+    }
+    code[i >> 3] |= fp4::to_codes(r[0], r[1]) << (4 * (i & 7));
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) append_fp4_kernel(AppendFp4Args a) {
+  sm100::griddep_launch_dependents();
+  sm100::griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t n_rows = (int64_t)a.B * a.T;
+  const int64_t stride = (int64_t)gridDim.x * (kThreads / 32);
+  const int blocks = a.d_c / fp4::kBlock;
+  // turns per position of the lane's rotary pairs (lane, lane + 32)
+  double turn[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    turn[k] = exp(-(2.0 * (lane + 32 * k) / a.d_r) * log((double)a.rope_base)) * 0.15915494309189533577;  // 1 / (2 pi)
+  for (int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); w < n_rows; w += stride) {
+    const int b = (int)(w / a.T), i = (int)(w % a.T);
+    if (a.counts != nullptr) {
+      const int n = a.counts[b];
+      if (n < 0 || n > a.T) {
+        if (lane == 0 && i == 0) raise_error(a.err, MLA_ERR_LENGTH);
+        continue;
+      }
+      if (i >= n) continue;
+    }
+    const int p0 = a.positions[b];
+    const int64_t pos = (int64_t)p0 + i;
+    const int64_t dst = (a.rows != nullptr ? (int64_t)a.rows[b] : (int64_t)p0) + i;
+    if (p0 < 0 || dst < 0 || dst >= a.n_max) {  // would land outside the cache: report, write nothing
+      if (lane == 0) raise_error(a.err, MLA_ERR_INDEX);
+      continue;
+    }
+    const T* row = static_cast<const T*>(a.kv_a) + b * a.lda_b + i * a.lda;
+    float x[2][16];
+    float ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int blk = lane + 32 * k;
+      if (blk < blocks) {
+        load16(row + blk * fp4::kBlock, x[k]);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) ss = fmaf(x[k][j], x[k][j], ss);
+      }
+    }
+    // the rotary key's loads overlap the norm
+    const T* key = row + a.d_c;
+    float k0[2], k1[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int j = lane + 32 * k;
+      if (j < a.d_r / 2) {
+        k0[k] = to_f32(key[2 * j]);
+        k1[k] = to_f32(key[2 * j + 1]);
+      }
+    }
+    ss = warp_sum(ss);
+    const float inv = rsqrtf(ss / (float)a.d_c + a.eps) * (1.f / a.latent_scale);
+    uint32_t code[2][2], s8[2];
+    bool ok = ss > 1e-30f && ss < 1e36f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int blk = lane + 32 * k;
+      if (blk < blocks)
+        ok &= quantise_fast(x[k], a.gain != nullptr ? a.gain + blk * fp4::kBlock : nullptr, inv, code[k], s8[k]);
+    }
+    if (!__all_sync(0xffffffffu, ok)) {
+      double s64 = 0.0;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (lane + 32 * k < blocks)
+          for (int j = 0; j < 16; ++j) s64 = fma((double)x[k][j], (double)x[k][j], s64);
+      s64 = warp_sum_f64(s64);
+      const double mul = 1.0 / sqrt(s64 / a.d_c + (double)a.eps);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int blk = lane + 32 * k;
+        if (blk < blocks)
+          quantise_exact(x[k], a.gain != nullptr ? a.gain + blk * fp4::kBlock : nullptr, mul,
+                         1.0 / (double)a.latent_scale, code[k], s8[k]);
+      }
+    }
+    uint8_t* c_dst = a.c4 + b * a.c4_b + dst * a.c4_r;
+    uint8_t* s_dst = a.sc + b * a.sc_b + dst * a.sc_r;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int blk = lane + 32 * k;
+      if (blk >= blocks) continue;
+      if constexpr (sizeof(T) == 2) {  // bf16 caches are 16-byte aligned
+        *reinterpret_cast<uint2*>(c_dst + 8 * blk) = make_uint2(code[k][0], code[k][1]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) c_dst[8 * blk + j] = (uint8_t)(code[k][j >> 2] >> (8 * (j & 3)));
+      }
+      s_dst[blk] = (uint8_t)s8[k];
+    }
+    // rotary key: the angle in turns, reduced in fp64 (at position 65535 an fp32 product is off by
+    // 4e-3 rad), then sin and cos of at most half a turn in fp32
+    T* k_dst = static_cast<T*>(a.k_r) + b * a.kr_b + dst * a.kr_r;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int j = lane + 32 * k;
+      if (j >= a.d_r / 2) continue;
+      const double t = (double)pos * turn[k];
+      float s, c;
+      sincospif(2.f * (float)(t - rint(t)), &s, &c);
+      k_dst[2 * j] = from_f32<T>(k0[k] * c - k1[k] * s);
+      k_dst[2 * j + 1] = from_f32<T>(k0[k] * s + k1[k] * c);
+    }
+  }
+}
+
+// Read-back: one thread per block of 16 features; rows past counts[b] come back as zeros.
+template <typename T>
+__global__ void __launch_bounds__(256) read_fp4_kernel(ReadFp4Args a) {
+  sm100::griddep_launch_dependents();
+  sm100::griddep_wait();
+  const int blocks = a.d_c / fp4::kBlock;
+  const int64_t total = (int64_t)a.B * a.n * blocks;
+  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < total; u += (int64_t)gridDim.x * 256) {
+    const int blk = (int)(u % blocks);
+    const int64_t r = u / blocks;
+    const int b = (int)(r / a.n), i = (int)(r % a.n);
+    const int n = a.counts != nullptr ? a.counts[b] : a.n;
+    const int64_t src = (a.first != nullptr ? a.first[b] : 0) + (int64_t)i;
+    bool live = i < n;
+    if (n < 0 || n > a.n) {
+      if (blk == 0 && i == 0) raise_error(a.err, MLA_ERR_LENGTH);
+      live = false;
+    } else if (live && (src < 0 || src >= a.n_max)) {
+      if (blk == 0) raise_error(a.err, MLA_ERR_INDEX);
+      live = false;
+    }
+    uint32_t w[2] = {0u, 0u};
+    float s = 0.f;
+    if (live) {
+      const uint8_t* c = a.c4 + b * a.c4_b + src * a.c4_r + 8 * blk;
+      if constexpr (sizeof(T) == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(c);
+        w[0] = v.x;
+        w[1] = v.y;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j >> 2] |= (uint32_t)c[j] << (8 * (j & 3));
+      }
+      s = fp4::scale_value(a.sc[b * a.sc_b + src * a.sc_r + blk]) * a.latent_scale;
+    }
+    float v[16];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint32_t h[4];
+      fp4::codes_to_f16(w[k], h);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = sm100::unpack_f16x2(h[j]);
+        v[8 * k + 2 * j] = f.x * s;
+        v[8 * k + 2 * j + 1] = f.y * s;
+      }
+    }
+    T* o = static_cast<T*>(a.out) + b * a.out_b + i * a.out_r + blk * fp4::kBlock;
+    if constexpr (sizeof(T) == 2) {
+      uint32_t p[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) p[j] = sm100::pack_bf16x2(v[2 * j], v[2 * j + 1]);
+      reinterpret_cast<uint4*>(o)[0] = make_uint4(p[0], p[1], p[2], p[3]);
+      reinterpret_cast<uint4*>(o)[1] = make_uint4(p[4], p[5], p[6], p[7]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) o[j] = v[j];
+    }
+  }
+}
+
+}  // namespace
+
+template <typename T>
+cudaError_t cache_append_fp4_launch(const AppendFp4Args& a, cudaStream_t st) {
+  const int64_t ctas = ((int64_t)a.B * a.T + kThreads / 32 - 1) / (kThreads / 32);
+  return launch_pdl(append_fp4_kernel<T>, dim3((unsigned)(ctas < 148 * 16 ? ctas : 148 * 16)), dim3(kThreads), 0, st, a);
+}
+
+template <typename T>
+cudaError_t cache_read_fp4_launch(const ReadFp4Args& a, cudaStream_t st) {
+  const int64_t ctas = ((int64_t)a.B * a.n * (a.d_c / fp4::kBlock) + 255) / 256;
+  return launch_pdl(read_fp4_kernel<T>, dim3((unsigned)(ctas < 148 * 8 ? ctas : 148 * 8)), dim3(256), 0, st, a);
+}
+
+template cudaError_t cache_append_fp4_launch<float>(const AppendFp4Args&, cudaStream_t);
+template cudaError_t cache_append_fp4_launch<__nv_bfloat16>(const AppendFp4Args&, cudaStream_t);
+template cudaError_t cache_read_fp4_launch<float>(const ReadFp4Args&, cudaStream_t);
+template cudaError_t cache_read_fp4_launch<__nv_bfloat16>(const ReadFp4Args&, cudaStream_t);
+
+}  // namespace mla

@@ -1,0 +1,227 @@
+// CUDA-core kernels of the 4-bit decode and of the attention-weight pass, generic in the dimensions.
+//
+//   decode   z[h,t] = scale (q~_h . c_t + q_pe,h . k^R_t), softmax over t <= length - T + s,
+//            ctx_h = sum_t p c_t, lse = log sum exp z      (split over the rows, merged by a second pass)
+//   weights  out[t] = [t < length - T] decay acc[t] + sum over tokens s and heads h of exp(z - lse)
+//
+// One warp per (head, query, split) in the decode and per cached row in the weights; lane l owns the
+// 16-feature blocks l and l + 32 of a latent row, so a 4-bit row costs a lane one 8-byte load and
+// one scale per block.  They carry the fp32 element type for any dimensions.
+#include <math.h>
+
+#include "common.cuh"
+#include "fp4.cuh"
+#include "kernels.h"
+#include "sm100_ptx.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kWarps = 4;
+
+// The lane's blocks of latent row t of sequence b (kFp4: decoded; otherwise in the element type).
+template <typename T, int NB, bool kFp4>
+__device__ __forceinline__ void load_row(const QueryArgs& a, int b, int t, int lane, float (&c)[NB][16]) {
+  const int blocks = (a.d_c + fp4::kBlock - 1) / fp4::kBlock;
+#pragma unroll
+  for (int k = 0; k < NB; ++k) {
+    const int blk = lane + 32 * k;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) c[k][i] = 0.f;
+    if (blk >= blocks) continue;
+    if constexpr (kFp4) {
+      const uint8_t* src = a.kv.c4 + b * a.kv.c4_b + t * a.kv.c4_r + 8 * blk;
+      const float s = fp4::scale_value(a.kv.sc[b * a.kv.sc_b + t * a.kv.sc_r + blk]) * a.kv.latent_scale;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        uint32_t word = 0u, h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) word |= (uint32_t)src[4 * w + j] << (8 * j);
+        fp4::codes_to_f16(word, h);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = sm100::unpack_f16x2(h[j]);
+          c[k][8 * w + 2 * j] = f.x * s;
+          c[k][8 * w + 2 * j + 1] = f.y * s;
+        }
+      }
+    } else {
+      const T* src = static_cast<const T*>(a.kv.c_kv) + b * a.kv.ckv_b + t * a.kv.ckv_r + 16 * blk;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (16 * blk + i < a.d_c) c[k][i] = to_f32(src[i]);
+    }
+  }
+}
+
+// The lane's share of q~ . c_t + q_pe . k^R_t of query row r, summed over the warp.
+template <typename T, int NB>
+__device__ __forceinline__ float score(const QueryArgs& a, int64_t r, const T* k_row, int lane,
+                                       const float (&c)[NB][16]) {
+  const T* q = static_cast<const T*>(a.q_tilde) + r * a.ldqt;
+  const T* qp = static_cast<const T*>(a.q_pe) + r * a.ldqp;
+  float dot = 0.f;
+#pragma unroll
+  for (int k = 0; k < NB; ++k)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int f = 16 * (lane + 32 * k) + i;
+      if (f < a.d_c) dot = fmaf(to_f32(q[f]), c[k][i], dot);
+    }
+  for (int f = lane; f < a.d_r; f += 32) dot = fmaf(to_f32(qp[f]), to_f32(k_row[f]), dot);
+  return warp_sum(dot) * a.scale;
+}
+
+template <typename T, int NB>
+__global__ void __launch_bounds__(32 * kWarps) decode_fp4_simt(Fp4DecodeArgs a, int n_splits, float* __restrict__ ws_o,
+                                                               float2* __restrict__ ws_ml) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = blockIdx.x * kWarps + warp;
+  const int q = blockIdx.y, split = blockIdx.z;
+  if (h >= a.n_h) return;
+  const int b = q / a.T, s = q % a.T;
+  const int len = a.lengths[b];
+  const bool bad = len < a.T || len > a.n_max;
+  if (bad && lane == 0 && h == 0 && split == 0) raise_error(a.err, MLA_ERR_LENGTH);
+  const int n = bad ? 0 : len - a.T + s + 1;  // rows this token sees
+  const int chunk = (a.n_max + n_splits - 1) / n_splits;
+  const int t0 = split * chunk, t1 = min(t0 + chunk, n);
+  const int64_t r = (int64_t)q * a.n_h + h;
+  float acc[NB][16];
+#pragma unroll
+  for (int k = 0; k < NB; ++k)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[k][i] = 0.f;
+  float m = -INFINITY, l = 0.f;
+  for (int t = t0; t < t1; ++t) {
+    float c[NB][16];
+    load_row<T, NB, true>(a, b, t, lane, c);
+    const float z = score<T, NB>(a, r, static_cast<const T*>(a.kv.k_r) + b * a.kv.kr_b + t * a.kv.kr_r, lane, c);
+    const float m_new = fmaxf(m, z);
+    const float corr = m_new > -INFINITY ? expf(m - m_new) : 1.f;
+    const float p = m_new > -INFINITY ? expf(z - m_new) : (z != z ? z : 0.f);
+    l = fmaf(l, corr, p);
+#pragma unroll
+    for (int k = 0; k < NB; ++k)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[k][i] = fmaf(acc[k][i], corr, p * c[k][i]);
+    m = m_new;
+  }
+  const bool whole = n_splits == 1;
+  const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+  const int64_t row = whole ? r : ((int64_t)split * a.B * a.T + q) * a.n_h + h;
+#pragma unroll
+  for (int k = 0; k < NB; ++k)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int f = 16 * (lane + 32 * k) + i;
+      if (f >= a.d_c) continue;
+      if (whole)
+        static_cast<T*>(a.ctx)[row * a.d_c + f] = from_f32<T>(acc[k][i] * inv);
+      else
+        ws_o[row * a.d_c + f] = acc[k][i];
+    }
+  if (lane != 0) return;
+  if (!whole)
+    ws_ml[row] = make_float2(m, l);
+  else if (a.lse != nullptr)
+    a.lse[row] = l == 0.f ? -INFINITY : m + logf(l);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(128) combine_fp4_simt(Fp4DecodeArgs a, int n_splits, const float* __restrict__ ws_o,
+                                                        const float2* __restrict__ ws_ml) {
+  const int64_t r = (int64_t)blockIdx.y * a.n_h + blockIdx.x, rows = (int64_t)a.B * a.T * a.n_h;
+  float M = -INFINITY, L = 0.f;
+  for (int s = 0; s < n_splits; ++s) M = fmaxf(M, ws_ml[s * rows + r].x);
+  for (int s = 0; s < n_splits; ++s) {
+    const float2 ml = ws_ml[s * rows + r];
+    if (ml.y != 0.f) L += ml.y * expf(ml.x - M);
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  for (int c = threadIdx.x; c < a.d_c; c += blockDim.x) {
+    float acc = 0.f;
+    for (int s = 0; s < n_splits; ++s) {
+      const float2 ml = ws_ml[s * rows + r];
+      if (ml.y != 0.f) acc = fmaf(expf(ml.x - M), ws_o[(s * rows + r) * a.d_c + c], acc);
+    }
+    static_cast<T*>(a.ctx)[r * a.d_c + c] = from_f32<T>(acc * inv);
+  }
+  if (a.lse != nullptr && threadIdx.x == 0) a.lse[r] = L == 0.f ? -INFINITY : M + logf(L);
+}
+
+template <typename T, int NB, bool kFp4>
+__global__ void __launch_bounds__(32 * kWarps) weights_simt(WeightsArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5), b = blockIdx.y;
+  const int len = a.lengths[b];
+  if (len < a.T || len > a.n_max) {
+    if (t == 0 && lane == 0) raise_error(a.err, MLA_ERR_LENGTH);
+    return;
+  }
+  if (t >= len) return;
+  float c[NB][16];
+  load_row<T, NB, kFp4>(a, b, t, lane, c);
+  const T* k_row = static_cast<const T*>(a.kv.k_r) + b * a.kv.kr_b + t * a.kv.kr_r;
+  float w = 0.f;
+  // new token s sees rows t <= len - T + s
+  for (int s = max(0, t - (len - a.T)); s < a.T; ++s)
+    for (int h = 0; h < a.n_h; ++h) {
+      const int64_t r = ((int64_t)b * a.T + s) * a.n_h + h;
+      const float lse = a.lse[r];
+      const float z = score<T, NB>(a, r, k_row, lane, c);
+      if (lse != -INFINITY) w += expf(z - lse);  // a row without a softmax gave no weight
+    }
+  if (lane != 0) return;
+  // a new token's row starts from nothing, whatever an evicted row left in its place
+  if (a.acc != nullptr && t < len - a.T) w = fmaf(a.decay, a.acc[b * a.acc_b + t], w);
+  a.out[b * a.out_b + t] = w;
+}
+
+}  // namespace
+
+int decode_fp4_simt_splits(int B, int n_max) {
+  // enough (head group, query, split) blocks to cover the GPU a few times over
+  const int by_rows = (n_max + 255) / 256, want = (4 * 148 + B - 1) / B;
+  const int s = by_rows < want ? by_rows : want;
+  return s < 1 ? 1 : s > 64 ? 64 : s;
+}
+
+size_t decode_fp4_simt_workspace(int n_h, int d_c, int B, int n_max) {
+  const int s = decode_fp4_simt_splits(B, n_max);
+  return s == 1 ? 256 : (size_t)s * B * n_h * (d_c * sizeof(float) + sizeof(float2)) + 256;
+}
+
+template <typename T>
+cudaError_t decode_fp4_simt_launch(const Fp4DecodeArgs& a, void* ws, cudaStream_t st) {
+  const int q = a.B * a.T, splits = decode_fp4_simt_splits(q, a.n_max);
+  float* ws_o = static_cast<float*>(ws);
+  float2* ws_ml = reinterpret_cast<float2*>(ws_o + (size_t)splits * q * a.n_h * a.d_c);
+  const dim3 grid((a.n_h + kWarps - 1) / kWarps, q, splits);
+  if (a.d_c <= 512)
+    decode_fp4_simt<T, 1><<<grid, 32 * kWarps, 0, st>>>(a, splits, ws_o, ws_ml);
+  else
+    decode_fp4_simt<T, 2><<<grid, 32 * kWarps, 0, st>>>(a, splits, ws_o, ws_ml);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || splits == 1) return e;
+  combine_fp4_simt<T><<<dim3(a.n_h, q), 128, 0, st>>>(a, splits, ws_o, ws_ml);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t weights_simt_launch(const WeightsArgs& a, cudaStream_t st) {
+  const dim3 grid((a.n_max + kWarps - 1) / kWarps, a.B);
+  const bool fp4 = a.kv.c4 != nullptr;
+  if (a.d_c <= 512)
+    (fp4 ? weights_simt<T, 1, true> : weights_simt<T, 1, false>)<<<grid, 32 * kWarps, 0, st>>>(a);
+  else
+    (fp4 ? weights_simt<T, 2, true> : weights_simt<T, 2, false>)<<<grid, 32 * kWarps, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+template cudaError_t decode_fp4_simt_launch<float>(const Fp4DecodeArgs&, void*, cudaStream_t);
+template cudaError_t decode_fp4_simt_launch<__nv_bfloat16>(const Fp4DecodeArgs&, void*, cudaStream_t);
+template cudaError_t weights_simt_launch<float>(const WeightsArgs&, cudaStream_t);
+template cudaError_t weights_simt_launch<__nv_bfloat16>(const WeightsArgs&, cudaStream_t);
+
+}  // namespace mla

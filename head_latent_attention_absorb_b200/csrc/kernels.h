@@ -27,6 +27,22 @@ int decode_simt_splits(int B, int n_keys_cap);
 template <typename T>
 cudaError_t cache_append_launch(const AppendArgs& a, cudaStream_t st);
 
+// ---- 4-bit latent cache (any dimensions; float or __nv_bfloat16) -----------------------------
+template <typename T>
+cudaError_t cache_append_fp4_launch(const AppendFp4Args& a, cudaStream_t st);
+template <typename T>
+cudaError_t cache_read_fp4_launch(const ReadFp4Args& a, cudaStream_t st);
+int decode_fp4_simt_splits(int B, int n_max);
+size_t decode_fp4_simt_workspace(int n_h, int d_c, int B, int n_max);
+template <typename T>
+cudaError_t decode_fp4_simt_launch(const Fp4DecodeArgs& a, void* ws, cudaStream_t st);
+
+// ---- attention weights and eviction ------------------------------------------------------------
+template <typename T>
+cudaError_t weights_simt_launch(const WeightsArgs& a, cudaStream_t st);
+cudaError_t evict_launch(const EvictArgs& a, cudaStream_t st);
+int evict_max_rows();
+
 // ---- top-k index validation (range and distinctness per sequence) --------------------------
 size_t check_topk_smem_bytes(int n_max);
 cudaError_t wait_timeout_launch(uint64_t limit_ns, int32_t* err, cudaStream_t st);

@@ -1,5 +1,6 @@
 // C-ABI entry points of libmla_b200.so: host-side validation, then dispatch to the kernels.
 // Every check that can be made on the host is made here, before anything is launched.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
@@ -55,6 +56,72 @@ mla_status check_bf16_ptr(mla_dtype dt, const void* p, const char* name) {
 }
 mla_status check_bf16_stride(mla_dtype dt, int64_t s, const char* name) {
   if (dt == MLA_BF16 && (s % 8) != 0) return fail(MLA_ERR_INVALID_ARG, "%s must be a multiple of 8 elements", name);
+  return MLA_OK;
+}
+
+// Dimensions of the cache operators: any head count at the DeepSeek widths in bf16
+mla_status check_cache_dims(const mla_dims& d, mla_dtype dt, bool fp4) {
+  if (d.n_h <= 0 || d.d_c <= 0 || d.d_r <= 0)
+    return fail(MLA_ERR_INVALID_ARG, "dimensions must be positive (n_h=%d d_c=%d d_r=%d)", d.n_h, d.d_c, d.d_r);
+  if (dt == MLA_BF16) {
+    if (d.n_h > 128 || d.d_c != 512 || d.d_r != 64)
+      return fail(MLA_ERR_UNSUPPORTED, "bf16 kernels need n_h <= 128, d_c=512 and d_r=64");
+    return MLA_OK;
+  }
+  if (dt != MLA_F32) return fail(MLA_ERR_INVALID_ARG, "unknown dtype %d", (int)dt);
+  if (d.n_h > 1024 || d.d_c > 1024 || d.d_r > 128)
+    return fail(MLA_ERR_UNSUPPORTED, "fp32 kernels accept n_h, d_c <= 1024, d_r <= 128");
+  if (fp4 && d.d_c % 16 != 0) return fail(MLA_ERR_UNSUPPORTED, "a 4-bit cache needs d_c a multiple of 16");
+  return MLA_OK;
+}
+
+// The 4-bit planes: row strides that hold a row; bf16 kernels load 16 bytes at a time
+mla_status check_fp4(const mla_dims& d, mla_dtype dt, const void* c4, int64_t c4_b, int64_t c4_r, const void* sc,
+                     int64_t sc_b, int64_t sc_r, float latent_scale) {
+  if (!c4 || !sc) return fail(MLA_ERR_INVALID_ARG, "NULL pointer");
+  if (c4_r < d.d_c / 2 || sc_r < d.d_c / 16 || c4_b < 0 || sc_b < 0)
+    return fail(MLA_ERR_INVALID_ARG, "c4 or kv_scale stride too small");
+  if (dt == MLA_BF16 && (!aligned16(c4) || !aligned16(sc) || c4_r % 16 || c4_b % 16 || sc_r % 16 || sc_b % 16))
+    return fail(MLA_ERR_INVALID_ARG, "c4 and kv_scale must be 16-byte aligned with strides of 16 bytes");
+  int e = 0;
+  if (!(latent_scale >= 5.42101086e-20f && latent_scale <= 1.8446744e19f) || frexpf(latent_scale, &e) != 0.5f)
+    return fail(MLA_ERR_INVALID_ARG, "latent_scale must be a power of two in [2^-64, 2^64]");
+  return MLA_OK;
+}
+
+// Query rows and rotary rows of the 4-bit decode and of the attention weights
+mla_status check_queries(const mla_dims& d, mla_dtype dt, int32_t B, int32_t T, const void* q_tilde, int64_t ldqt,
+                         const void* q_pe, int64_t ldqp, const void* k_r, int64_t kr_b, int64_t kr_r, int32_t n_max,
+                         const int32_t* lengths, float scale) {
+  if (B <= 0 || T < 1 || n_max <= 0 || T > n_max) return fail(MLA_ERR_INVALID_ARG, "need B > 0 and 1 <= T <= n_max");
+  if ((int64_t)B * T > 65535) return fail(MLA_ERR_UNSUPPORTED, "B * T must not exceed 65535");
+  if (!q_tilde || !q_pe || !k_r || !lengths) return fail(MLA_ERR_INVALID_ARG, "NULL pointer");
+  if (ldqt < d.d_c || ldqp < d.d_r) return fail(MLA_ERR_INVALID_ARG, "query row stride too small");
+  if (kr_r < d.d_r || kr_b < 0) return fail(MLA_ERR_INVALID_ARG, "cache stride too small");
+  if (!(scale > 0.f) || !(scale < INFINITY)) return fail(MLA_ERR_INVALID_ARG, "scale must be positive and finite");
+  if (dt != MLA_BF16) return MLA_OK;
+  if (!aligned16(q_tilde) || !aligned16(q_pe) || !aligned16(k_r))
+    return fail(MLA_ERR_INVALID_ARG, "q_tilde, q_pe and k_r must be 16-byte aligned");
+  if (ldqt % 8 || ldqp % 8 || kr_b % 8 || kr_r % 8)
+    return fail(MLA_ERR_INVALID_ARG, "query and k_r strides must be multiples of 8 elements");
+  return MLA_OK;
+}
+
+void fill_queries(mla::QueryArgs& a, const mla_dims& d, int32_t B, int32_t T, const void* q_tilde, int64_t ldqt,
+                  const void* q_pe, int64_t ldqp, const void* k_r, int64_t kr_b, int64_t kr_r, int32_t n_max,
+                  const int32_t* lengths, float scale, int32_t* err) {
+  a.n_h = d.n_h; a.d_c = d.d_c; a.d_r = d.d_r; a.B = B; a.T = T; a.n_max = n_max;
+  a.q_tilde = q_tilde; a.ldqt = ldqt; a.q_pe = q_pe; a.ldqp = ldqp;
+  a.kv.k_r = k_r; a.kv.kr_b = kr_b; a.kv.kr_r = kr_r;
+  a.lengths = lengths; a.scale = scale; a.err = err;
+}
+
+mla_status check_weights(const float* lse, const float* acc, int64_t acc_b, float decay, const float* out,
+                         int64_t out_b, int32_t n_max) {
+  if (!lse || !out) return fail(MLA_ERR_INVALID_ARG, "NULL pointer");
+  if (out_b < n_max || (acc && acc_b < n_max)) return fail(MLA_ERR_INVALID_ARG, "batch stride smaller than n_max");
+  if (acc == out && acc_b != out_b) return fail(MLA_ERR_INVALID_ARG, "acc and out are one array with two strides");
+  if (!(decay >= 0.f) || !(decay < INFINITY)) return fail(MLA_ERR_INVALID_ARG, "decay must be finite and >= 0");
   return MLA_OK;
 }
 
@@ -443,12 +510,13 @@ mla_status mla_prefill_naive(mla_dims dims, mla_dtype dtype, int32_t B, int32_t 
   return cuda_status(e, "mla_prefill_naive launch");
 }
 
-mla_status mla_cache_append(mla_dims dims, mla_dtype dtype, int32_t B, const void* kv_a, int64_t lda,
-                            const float* gain, float eps, float rope_base, const int32_t* positions, int32_t n_max,
-                            void* c_kv, int64_t ckv_bstride, int64_t ckv_rstride, void* k_r, int64_t kr_bstride,
-                            int64_t kr_rstride, int32_t* dev_err, void* stream) {
+mla_status mla_cache_append_at(mla_dims dims, mla_dtype dtype, int32_t B, const void* kv_a, int64_t lda,
+                               const float* gain, float eps, float rope_base, const int32_t* positions,
+                               const int32_t* rows, int32_t n_max, void* c_kv, int64_t ckv_bstride,
+                               int64_t ckv_rstride, void* k_r, int64_t kr_bstride, int64_t kr_rstride,
+                               int32_t* dev_err, void* stream) {
   g_msg[0] = 0;
-  MLA_TRY(check_dims(dims, dtype));
+  MLA_TRY(check_cache_dims(dims, dtype, false));  // the heads do not enter
   if (B <= 0 || n_max <= 0) return fail(MLA_ERR_INVALID_ARG, "B and n_max must be positive");
   if (!kv_a || !positions || !c_kv || !k_r) return fail(MLA_ERR_INVALID_ARG, "NULL pointer");
   if (dims.d_r % 2 != 0) return fail(MLA_ERR_INVALID_ARG, "d_r must be even (rotary pairs)");
@@ -469,6 +537,7 @@ mla_status mla_cache_append(mla_dims dims, mla_dtype dtype, int32_t B, const voi
   mla::AppendArgs a;
   a.d_c = dims.d_c; a.d_r = dims.d_r; a.B = B; a.n_max = n_max;
   a.kv_a = kv_a; a.lda = lda; a.gain = gain; a.eps = eps; a.rope_base = rope_base; a.positions = positions;
+  a.rows = rows;
   a.c_kv = c_kv; a.ckv_b = ckv_bstride; a.ckv_r = ckv_rstride;
   a.k_r = k_r; a.kr_b = kr_bstride; a.kr_r = kr_rstride;
   a.err = dev_err;
@@ -476,6 +545,195 @@ mla_status mla_cache_append(mla_dims dims, mla_dtype dtype, int32_t B, const voi
   const cudaError_t e = dtype == MLA_BF16 ? mla::cache_append_launch<__nv_bfloat16>(a, st)
                                           : mla::cache_append_launch<float>(a, st);
   return cuda_status(e, "mla_cache_append launch");
+}
+
+mla_status mla_cache_append(mla_dims dims, mla_dtype dtype, int32_t B, const void* kv_a, int64_t lda,
+                            const float* gain, float eps, float rope_base, const int32_t* positions, int32_t n_max,
+                            void* c_kv, int64_t ckv_bstride, int64_t ckv_rstride, void* k_r, int64_t kr_bstride,
+                            int64_t kr_rstride, int32_t* dev_err, void* stream) {
+  return mla_cache_append_at(dims, dtype, B, kv_a, lda, gain, eps, rope_base, positions, nullptr, n_max, c_kv,
+                             ckv_bstride, ckv_rstride, k_r, kr_bstride, kr_rstride, dev_err, stream);
+}
+
+mla_status mla_cache_append_fp4(mla_dims dims, mla_dtype dtype, int32_t B, int32_t T, const void* kv_a,
+                                int64_t lda_b, int64_t lda, const float* gain, float eps, float rope_base,
+                                float latent_scale, const int32_t* positions, const int32_t* rows,
+                                const int32_t* counts, int32_t n_max, uint8_t* c4, int64_t c4_bstride,
+                                int64_t c4_rstride, uint8_t* kv_scale, int64_t sc_bstride, int64_t sc_rstride,
+                                void* k_r, int64_t kr_bstride, int64_t kr_rstride, int32_t* dev_err, void* stream) {
+  g_msg[0] = 0;
+  MLA_TRY(check_cache_dims(dims, dtype, true));
+  if (B <= 0 || T <= 0 || n_max <= 0) return fail(MLA_ERR_INVALID_ARG, "B, T and n_max must be positive");
+  if (!kv_a || !positions || !k_r) return fail(MLA_ERR_INVALID_ARG, "NULL pointer");
+  if (dims.d_r % 2 != 0) return fail(MLA_ERR_INVALID_ARG, "d_r must be even (rotary pairs)");
+  if (lda < (int64_t)dims.d_c + dims.d_r || lda_b < 0)
+    return fail(MLA_ERR_INVALID_ARG, "lda smaller than d_c + d_r");
+  MLA_TRY(check_fp4(dims, dtype, c4, c4_bstride, c4_rstride, kv_scale, sc_bstride, sc_rstride, latent_scale));
+  if (kr_rstride < dims.d_r) return fail(MLA_ERR_INVALID_ARG, "row stride too small");
+  if (B > 1 && (c4_bstride < (int64_t)n_max * c4_rstride || sc_bstride < (int64_t)n_max * sc_rstride ||
+                kr_bstride < (int64_t)n_max * kr_rstride))
+    return fail(MLA_ERR_INVALID_ARG, "batch stride smaller than n_max rows");
+  if (!(eps >= 0.f) || !(eps < 1e30f)) return fail(MLA_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (!(rope_base > 0.f) || !(rope_base < 1e30f)) return fail(MLA_ERR_INVALID_ARG, "rope_base must be finite and > 0");
+  MLA_TRY(check_bf16_ptr(dtype, kv_a, "kv_a"));
+  MLA_TRY(check_bf16_ptr(dtype, k_r, "k_r"));
+  MLA_TRY(check_bf16_stride(dtype, lda, "lda"));
+  MLA_TRY(check_bf16_stride(dtype, lda_b, "lda_b"));
+  MLA_TRY(check_bf16_stride(dtype, kr_rstride, "kr_rstride"));
+  MLA_TRY(check_bf16_stride(dtype, kr_bstride, "kr_bstride"));
+  mla::AppendFp4Args a;
+  a.d_c = dims.d_c; a.d_r = dims.d_r; a.B = B; a.T = T; a.n_max = n_max;
+  a.kv_a = kv_a; a.lda_b = lda_b; a.lda = lda; a.gain = gain; a.eps = eps; a.rope_base = rope_base;
+  a.latent_scale = latent_scale; a.positions = positions; a.rows = rows; a.counts = counts;
+  a.c4 = c4; a.c4_b = c4_bstride; a.c4_r = c4_rstride;
+  a.sc = kv_scale; a.sc_b = sc_bstride; a.sc_r = sc_rstride;
+  a.k_r = k_r; a.kr_b = kr_bstride; a.kr_r = kr_rstride;
+  a.err = dev_err;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == MLA_BF16 ? mla::cache_append_fp4_launch<__nv_bfloat16>(a, st)
+                                          : mla::cache_append_fp4_launch<float>(a, st);
+  return cuda_status(e, "mla_cache_append_fp4 launch");
+}
+
+mla_status mla_cache_read_fp4(mla_dims dims, mla_dtype dtype, int32_t B, int32_t n, const int32_t* first,
+                              const int32_t* counts, int32_t n_max, const uint8_t* c4, int64_t c4_bstride,
+                              int64_t c4_rstride, const uint8_t* kv_scale, int64_t sc_bstride, int64_t sc_rstride,
+                              float latent_scale, void* out, int64_t out_bstride, int64_t out_rstride,
+                              int32_t* dev_err, void* stream) {
+  g_msg[0] = 0;
+  MLA_TRY(check_cache_dims(dims, dtype, true));
+  if (B <= 0 || n <= 0 || n_max <= 0) return fail(MLA_ERR_INVALID_ARG, "B, n and n_max must be positive");
+  if (!out) return fail(MLA_ERR_INVALID_ARG, "NULL pointer");
+  MLA_TRY(check_fp4(dims, dtype, c4, c4_bstride, c4_rstride, kv_scale, sc_bstride, sc_rstride, latent_scale));
+  if (out_rstride < dims.d_c || (B > 1 && out_bstride < (int64_t)n * out_rstride))
+    return fail(MLA_ERR_INVALID_ARG, "out stride too small");
+  MLA_TRY(check_bf16_ptr(dtype, out, "out"));
+  MLA_TRY(check_bf16_stride(dtype, out_rstride, "out_rstride"));
+  MLA_TRY(check_bf16_stride(dtype, out_bstride, "out_bstride"));
+  mla::ReadFp4Args a;
+  a.d_c = dims.d_c; a.B = B; a.n = n; a.n_max = n_max; a.first = first; a.counts = counts;
+  a.c4 = c4; a.c4_b = c4_bstride; a.c4_r = c4_rstride;
+  a.sc = kv_scale; a.sc_b = sc_bstride; a.sc_r = sc_rstride;
+  a.latent_scale = latent_scale; a.out = out; a.out_b = out_bstride; a.out_r = out_rstride; a.err = dev_err;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == MLA_BF16 ? mla::cache_read_fp4_launch<__nv_bfloat16>(a, st)
+                                          : mla::cache_read_fp4_launch<float>(a, st);
+  return cuda_status(e, "mla_cache_read_fp4 launch");
+}
+
+size_t mla_decode_fp4kv_workspace_size(mla_dims dims, mla_dtype dtype, int32_t B, int32_t T, int32_t n_max) {
+  if (check_cache_dims(dims, dtype, true) != MLA_OK || B <= 0 || T < 1 || n_max < T || (int64_t)B * T > 65535) return 0;
+  return mla::decode_fp4_simt_workspace(dims.n_h, dims.d_c, B * T, n_max);
+}
+
+mla_status mla_decode_absorb_fp4kv(mla_dims dims, mla_dtype dtype, int32_t B, int32_t T, const void* q_tilde,
+                                   int64_t ldqt, const void* q_pe, int64_t ldqp, const uint8_t* c4,
+                                   int64_t c4_bstride, int64_t c4_rstride, const uint8_t* kv_scale,
+                                   int64_t sc_bstride, int64_t sc_rstride, const void* k_r, int64_t kr_bstride,
+                                   int64_t kr_rstride, float latent_scale, int32_t n_max, const int32_t* lengths,
+                                   float scale, void* ctx_out, float* lse_out, void* workspace, size_t ws_bytes,
+                                   int32_t* dev_err, void* stream) {
+  g_msg[0] = 0;
+  MLA_TRY(check_cache_dims(dims, dtype, true));
+  MLA_TRY(check_queries(dims, dtype, B, T, q_tilde, ldqt, q_pe, ldqp, k_r, kr_bstride, kr_rstride, n_max, lengths,
+                        scale));
+  MLA_TRY(check_fp4(dims, dtype, c4, c4_bstride, c4_rstride, kv_scale, sc_bstride, sc_rstride, latent_scale));
+  if (!ctx_out) return fail(MLA_ERR_INVALID_ARG, "NULL pointer");
+  MLA_TRY(check_bf16_ptr(dtype, ctx_out, "ctx_out"));
+  const size_t need = mla_decode_fp4kv_workspace_size(dims, dtype, B, T, n_max);
+  if (!workspace || ws_bytes < need)
+    return fail(MLA_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need, workspace ? ws_bytes : (size_t)0);
+  if (!aligned16(workspace)) return fail(MLA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  mla::Fp4DecodeArgs a;
+  fill_queries(a, dims, B, T, q_tilde, ldqt, q_pe, ldqp, k_r, kr_bstride, kr_rstride, n_max, lengths, scale, dev_err);
+  a.kv.c4 = c4; a.kv.c4_b = c4_bstride; a.kv.c4_r = c4_rstride;
+  a.kv.sc = kv_scale; a.kv.sc_b = sc_bstride; a.kv.sc_r = sc_rstride;
+  a.kv.latent_scale = latent_scale;
+  a.ctx = ctx_out; a.lse = lse_out;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == MLA_BF16 ? mla::decode_fp4_simt_launch<__nv_bfloat16>(a, workspace, st)
+                                          : mla::decode_fp4_simt_launch<float>(a, workspace, st);
+  return cuda_status(e, "mla_decode_absorb_fp4kv launch");
+}
+
+mla_status mla_cache_weights(mla_dims dims, mla_dtype dtype, int32_t B, int32_t T, const void* q_tilde, int64_t ldqt,
+                             const void* q_pe, int64_t ldqp, const void* c_kv, int64_t ckv_bstride,
+                             int64_t ckv_rstride, const void* k_r, int64_t kr_bstride, int64_t kr_rstride,
+                             int32_t n_max, const int32_t* lengths, float scale, const float* lse, const float* acc,
+                             int64_t acc_bstride, float decay, float* out, int64_t out_bstride, int32_t* dev_err,
+                             void* stream) {
+  g_msg[0] = 0;
+  MLA_TRY(check_cache_dims(dims, dtype, false));
+  MLA_TRY(check_queries(dims, dtype, B, T, q_tilde, ldqt, q_pe, ldqp, k_r, kr_bstride, kr_rstride, n_max, lengths,
+                        scale));
+  if (!c_kv) return fail(MLA_ERR_INVALID_ARG, "NULL pointer");
+  if (ckv_rstride < dims.d_c || ckv_bstride < 0) return fail(MLA_ERR_INVALID_ARG, "cache stride too small");
+  MLA_TRY(check_bf16_ptr(dtype, c_kv, "c_kv"));
+  MLA_TRY(check_bf16_stride(dtype, ckv_rstride, "ckv_rstride"));
+  MLA_TRY(check_bf16_stride(dtype, ckv_bstride, "ckv_bstride"));
+  MLA_TRY(check_weights(lse, acc, acc_bstride, decay, out, out_bstride, n_max));
+  mla::WeightsArgs a;
+  fill_queries(a, dims, B, T, q_tilde, ldqt, q_pe, ldqp, k_r, kr_bstride, kr_rstride, n_max, lengths, scale, dev_err);
+  a.kv.c_kv = c_kv; a.kv.ckv_b = ckv_bstride; a.kv.ckv_r = ckv_rstride;
+  a.lse = lse; a.acc = acc; a.acc_b = acc_bstride; a.decay = decay; a.out = out; a.out_b = out_bstride;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == MLA_BF16 ? mla::weights_simt_launch<__nv_bfloat16>(a, st)
+                                          : mla::weights_simt_launch<float>(a, st);
+  return cuda_status(e, "mla_cache_weights launch");
+}
+
+mla_status mla_cache_weights_fp4kv(mla_dims dims, mla_dtype dtype, int32_t B, int32_t T, const void* q_tilde,
+                                   int64_t ldqt, const void* q_pe, int64_t ldqp, const uint8_t* c4,
+                                   int64_t c4_bstride, int64_t c4_rstride, const uint8_t* kv_scale,
+                                   int64_t sc_bstride, int64_t sc_rstride, const void* k_r, int64_t kr_bstride,
+                                   int64_t kr_rstride, float latent_scale, int32_t n_max, const int32_t* lengths,
+                                   float scale, const float* lse, const float* acc, int64_t acc_bstride,
+                                   float decay, float* out, int64_t out_bstride, int32_t* dev_err, void* stream) {
+  g_msg[0] = 0;
+  MLA_TRY(check_cache_dims(dims, dtype, true));
+  MLA_TRY(check_queries(dims, dtype, B, T, q_tilde, ldqt, q_pe, ldqp, k_r, kr_bstride, kr_rstride, n_max, lengths,
+                        scale));
+  MLA_TRY(check_fp4(dims, dtype, c4, c4_bstride, c4_rstride, kv_scale, sc_bstride, sc_rstride, latent_scale));
+  MLA_TRY(check_weights(lse, acc, acc_bstride, decay, out, out_bstride, n_max));
+  mla::WeightsArgs a;
+  fill_queries(a, dims, B, T, q_tilde, ldqt, q_pe, ldqp, k_r, kr_bstride, kr_rstride, n_max, lengths, scale, dev_err);
+  a.kv.c4 = c4; a.kv.c4_b = c4_bstride; a.kv.c4_r = c4_rstride;
+  a.kv.sc = kv_scale; a.kv.sc_b = sc_bstride; a.kv.sc_r = sc_rstride;
+  a.kv.latent_scale = latent_scale;
+  a.lse = lse; a.acc = acc; a.acc_b = acc_bstride; a.decay = decay; a.out = out; a.out_b = out_bstride;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == MLA_BF16 ? mla::weights_simt_launch<__nv_bfloat16>(a, st)
+                                          : mla::weights_simt_launch<float>(a, st);
+  return cuda_status(e, "mla_cache_weights_fp4kv launch");
+}
+
+mla_status mla_cache_evict(int32_t B, int32_t n_max, const mla_rows* planes, int32_t n_planes, const float* acc,
+                           int64_t acc_bstride, const int32_t* lengths, int32_t keep, int32_t sink, int32_t recent,
+                           int32_t* new_lengths, int32_t* row_map, int32_t* dev_err, void* stream) {
+  g_msg[0] = 0;
+  if (B <= 0 || n_max <= 0) return fail(MLA_ERR_INVALID_ARG, "B and n_max must be positive");
+  if (B > 65535) return fail(MLA_ERR_UNSUPPORTED, "B must not exceed 65535");
+  if (n_max > mla::evict_max_rows())
+    return fail(MLA_ERR_UNSUPPORTED, "n_max must not exceed %d", mla::evict_max_rows());
+  if (!planes || n_planes < 1 || n_planes > MLA_MAX_PLANES)
+    return fail(MLA_ERR_INVALID_ARG, "need 1 to %d planes", MLA_MAX_PLANES);
+  if (!acc || !lengths || !new_lengths || !row_map) return fail(MLA_ERR_INVALID_ARG, "NULL pointer");
+  if (keep < 1 || keep > n_max) return fail(MLA_ERR_INVALID_ARG, "keep must lie in [1, n_max]");
+  if (sink < 0 || recent < 0 || (int64_t)sink + recent > keep)
+    return fail(MLA_ERR_INVALID_ARG, "sink and recent must be >= 0 with a sum of at most keep");
+  if (acc_bstride < n_max && B > 1) return fail(MLA_ERR_INVALID_ARG, "acc batch stride smaller than n_max");
+  mla::EvictArgs a;
+  for (int p = 0; p < n_planes; ++p) {
+    const mla_rows& r = planes[p];
+    if (!r.base) return fail(MLA_ERR_INVALID_ARG, "plane %d: NULL pointer", p);
+    if (r.row_bytes <= 0 || r.rstride < r.row_bytes || (B > 1 && r.bstride < (n_max - 1) * r.rstride + r.row_bytes))
+      return fail(MLA_ERR_INVALID_ARG, "plane %d: rows overlap (row_bytes, rstride or bstride too small)", p);
+    a.planes[p] = r;
+  }
+  a.B = B; a.n_max = n_max; a.n_planes = n_planes; a.keep = keep; a.sink = sink; a.recent = recent;
+  a.acc = acc; a.acc_b = acc_bstride; a.lengths = lengths; a.new_lengths = new_lengths; a.row_map = row_map;
+  a.err = dev_err;
+  return cuda_status(mla::evict_launch(a, static_cast<cudaStream_t>(stream)), "mla_cache_evict launch");
 }
 
 mla_status mla_check_topk(int32_t B, const int32_t* topk_idx, int32_t topk, const int32_t* lengths, int32_t n_max,

@@ -17,6 +17,10 @@
  *                                                                    ("Value up-projection", MHA-prefill excerpt)
  *   mla_absorb_q_fp8, mla_out_up_fp8  the projections with an FP8 wkv_b and its 128 x 128 block scales
  *                                                                    ("Key-value down-projection", linear excerpt)
+ *   mla_cache_append_fp4, mla_cache_read_fp4, mla_decode_absorb_fp4kv  a latent cache held in 4 bits:
+ *                      its append, its values, and the decode that reads it
+ *   mla_cache_weights, mla_cache_weights_fp4kv, mla_cache_evict  the attention weight that each cached
+ *                      row receives, and the eviction of the rows that receive least
  * plus one opt-in check of the sparse decode's precondition:
  *   mla_check_topk     top-k indices in range and distinct per sequence (the mask is a set)
  *
@@ -333,6 +337,168 @@ mla_status mla_cache_append(mla_dims dims, mla_dtype dtype, int32_t B,
                             void* c_kv, int64_t ckv_bstride, int64_t ckv_rstride,
                             void* k_r, int64_t kr_bstride, int64_t kr_rstride,
                             int32_t* dev_err, void* stream);
+
+/*
+ * mla_cache_append_at - mla_cache_append with the cache row of each new token given apart from its
+ * position, for a cache whose rows have been evicted (mla_cache_evict): the token of sequence b is
+ * written to row rows[b] and its rotary key is turned by positions[b].
+ *   rows       DEVICE int32 [B], or NULL: row = position (mla_cache_append)
+ *   Device flag: a row outside [0, n_max) or a negative position sets MLA_ERR_INDEX and that sequence
+ *   writes nothing.  Other arguments as in mla_cache_append.  Asynchronous on `stream`.
+ */
+mla_status mla_cache_append_at(mla_dims dims, mla_dtype dtype, int32_t B,
+                               const void* kv_a, int64_t lda, const float* gain, float eps, float rope_base,
+                               const int32_t* positions, const int32_t* rows, int32_t n_max,
+                               void* c_kv, int64_t ckv_bstride, int64_t ckv_rstride,
+                               void* k_r, int64_t kr_bstride, int64_t kr_rstride,
+                               int32_t* dev_err, void* stream);
+
+/*
+ * The 4-bit latent cache
+ * ----------------------
+ * A latent row is cut into blocks of 16 features; a block holds sixteen E2M1 codes (magnitudes 0, .5, 1,
+ * 1.5, 2, 3, 4, 6 and a sign) and one E4M3 scale:
+ *   c[t, f] = code[t, f] * scale[t, f / 16] * latent_scale
+ *   c4        row t of sequence b: d_c / 2 bytes at c4 + b*c4_bstride + t*c4_rstride, feature 2i in the
+ *             low half of byte i and feature 2i + 1 in the high half
+ *   kv_scale  row t of sequence b: d_c / 16 bytes at kv_scale + b*sc_bstride + t*sc_rstride
+ *   k_r       rotary rows in the element type, strides in ELEMENTS as in mla_decode_absorb
+ *   latent_scale  one power of two in [2^-64, 2^64] for the whole cache (1 for latents of unit size;
+ *             smaller where a small RMSNorm gain would push scales below E4M3's 2^-9)
+ * Strides of c4 and kv_scale are in BYTES.  A packed bf16 row at the DeepSeek widths is 416 bytes (256
+ * codes, 32 scales, 64 rotary features; bf16 needs 1152): c4 = base, kv_scale = base + 256,
+ * k_r = base + 288.  code * scale has at most six significant bits, so reading a row back rounds
+ * nothing, in bf16 as in fp32.
+ * Types and widths of the three calls below: MLA_BF16 with d_c = 512, d_r = 64 and 1 <= n_h <= 128
+ * (16-byte aligned pointers, c4 and kv_scale strides multiples of 16, other strides as everywhere);
+ * MLA_F32 with n_h, d_c <= 1024, d_r <= 128 even, d_c a multiple of 16.  d_h and d_v are not read.
+ *
+ * mla_cache_append_fp4 - the counterpart of mla_cache_append, for one or many tokens per sequence (a
+ * decode's new token, or a padded batch of prompts).  Token i of sequence b, i < counts[b]:
+ *   y = gain x / sqrt(mean(x^2) + eps) / latent_scale,   x = kv_a[b, i, 0:d_c]
+ *   scale = e4m3(max |y| / 6) and code = e2m1(y / scale) per block, both to nearest, ties to even,
+ *   saturating (a zero scale: zero codes; a block with a NaN: a NaN scale, so that it reads as NaN)
+ *   and the rotary key kv_a[b, i, d_c:] turned by positions[b] + i, into cache row rows[b] + i.
+ * Values next to a rounding border are decided in fp64: the codes are the formula's, not those of an
+ * fp32 evaluation of it.
+ *   kv_a       element (b, i, j) at kv_a[b*lda_b + i*lda + j]; j < d_c latent, then d_r rotary
+ *   positions  DEVICE int32 [B]: position of each sequence's first new token
+ *   rows       DEVICE int32 [B]: cache row of it, or NULL: rows = positions
+ *   counts     DEVICE int32 [B]: tokens of each sequence in [0, T], or NULL: T everywhere
+ *   Device flag: counts[b] outside [0, T] sets MLA_ERR_LENGTH (the sequence writes nothing); a row outside
+ *   [0, n_max) or a negative position sets MLA_ERR_INDEX (that token is not written).  Every other
+ *   cache row is left as it was.  Asynchronous on `stream`.
+ */
+mla_status mla_cache_append_fp4(mla_dims dims, mla_dtype dtype, int32_t B, int32_t T,
+                                const void* kv_a, int64_t lda_b, int64_t lda, const float* gain, float eps,
+                                float rope_base, float latent_scale,
+                                const int32_t* positions, const int32_t* rows, const int32_t* counts,
+                                int32_t n_max, uint8_t* c4, int64_t c4_bstride, int64_t c4_rstride,
+                                uint8_t* kv_scale, int64_t sc_bstride, int64_t sc_rstride,
+                                void* k_r, int64_t kr_bstride, int64_t kr_rstride,
+                                int32_t* dev_err, void* stream);
+
+/*
+ * mla_cache_read_fp4 - the latent rows of a 4-bit cache as values, e.g. for mla_prefill_naive:
+ *   out[b, i, :] = c[first[b] + i, :] for i < counts[b], zeros for counts[b] <= i < n
+ *   first   DEVICE int32 [B], or NULL: 0;   counts  DEVICE int32 [B] in [0, n], or NULL: n
+ *   out     element (b, i, f) at out[b*out_bstride + i*out_rstride + f], in `dtype`
+ *   Device flag: counts[b] outside [0, n] sets MLA_ERR_LENGTH, a row outside [0, n_max) MLA_ERR_INDEX; the
+ *   rows concerned come back as zeros.  Asynchronous on `stream`.
+ */
+mla_status mla_cache_read_fp4(mla_dims dims, mla_dtype dtype, int32_t B, int32_t n,
+                              const int32_t* first, const int32_t* counts, int32_t n_max,
+                              const uint8_t* c4, int64_t c4_bstride, int64_t c4_rstride,
+                              const uint8_t* kv_scale, int64_t sc_bstride, int64_t sc_rstride,
+                              float latent_scale, void* out, int64_t out_bstride, int64_t out_rstride,
+                              int32_t* dev_err, void* stream);
+
+/* Bytes of scratch mla_decode_absorb_fp4kv needs for this shape on the current device; 0 for arguments
+ * that it would reject. */
+size_t mla_decode_fp4kv_workspace_size(mla_dims dims, mla_dtype dtype, int32_t B, int32_t T, int32_t n_max);
+
+/*
+ * mla_decode_absorb_fp4kv - the absorbed decode over a 4-bit cache, T new tokens per sequence (the last T of
+ * its lengths[b] rows; token s sees rows t <= lengths[b] - T + s, as in mla_decode_absorb_multi):
+ *   ctx[b*T + s, h, :] = sum_t softmax(z)_t c[t, :],  lse = log sum_t exp(z_t),
+ *   z_t = scale * (q_tilde . c[t, :] + q_pe . k_r[t, :])
+ *   q_tilde, q_pe, ctx_out, lse_out  query rows (b * T + s) * n_h + h, as in mla_decode_absorb_multi
+ *   lengths  DEVICE int32 [B] in [T, n_max]; another length sets MLA_ERR_LENGTH and the sequence's tokens
+ *            get ctx = 0, lse = -inf.  Rows at and behind lengths[b] may hold anything.
+ *   workspace  at least mla_decode_fp4kv_workspace_size() bytes, 16-byte aligned, no initialisation;
+ *            calls that may overlap need one each
+ *   B * T <= 65535.  Asynchronous on `stream`.
+ */
+mla_status mla_decode_absorb_fp4kv(mla_dims dims, mla_dtype dtype, int32_t B, int32_t T,
+                                   const void* q_tilde, int64_t ldqt, const void* q_pe, int64_t ldqp,
+                                   const uint8_t* c4, int64_t c4_bstride, int64_t c4_rstride,
+                                   const uint8_t* kv_scale, int64_t sc_bstride, int64_t sc_rstride,
+                                   const void* k_r, int64_t kr_bstride, int64_t kr_rstride, float latent_scale,
+                                   int32_t n_max, const int32_t* lengths, float scale, void* ctx_out,
+                                   float* lse_out, void* workspace, size_t ws_bytes, int32_t* dev_err,
+                                   void* stream);
+
+/*
+ * mla_cache_weights - the attention weight that each cached row received in a decode step, summed over
+ * its heads and new tokens and added to what the row had received before:
+ *   out[b, t] = [t < lengths[b] - T] * decay * acc[b, t] + sum_{s, h} exp(z[s, h, t] - lse[b*T + s, h])
+ *   for t < lengths[b], z as in mla_decode_absorb_fp4kv and only over the rows that token s sees.  The T new rows
+ *   start from nothing, so a row that an eviction freed takes no weight over.  out[b, t] for
+ *   t >= lengths[b] is left as it was.
+ *   lse      float [B * T, n_h], the decode's lse_out; -inf (no softmax) adds nothing
+ *   acc      float, element (b, t) at acc[b*acc_bstride + t], or NULL: nothing accumulated so far
+ *   out      float, element (b, t) at out[b*out_bstride + t]; may be acc itself
+ *   decay    >= 0 and finite; 1 sums over all steps
+ *   lengths  DEVICE int32 [B] in [T, n_max]; another length sets MLA_ERR_LENGTH and writes nothing
+ *   Sums over heads and tokens are in fp32, in a fixed order.  Types and widths: MLA_BF16 with
+ *   d_c = 512, d_r = 64, 1 <= n_h <= 128; MLA_F32 with n_h, d_c <= 1024, d_r <= 128.  B <= 65535.
+ * mla_cache_weights_fp4kv reads the 4-bit cache instead.  Asynchronous on `stream`.
+ */
+mla_status mla_cache_weights(mla_dims dims, mla_dtype dtype, int32_t B, int32_t T,
+                             const void* q_tilde, int64_t ldqt, const void* q_pe, int64_t ldqp,
+                             const void* c_kv, int64_t ckv_bstride, int64_t ckv_rstride,
+                             const void* k_r, int64_t kr_bstride, int64_t kr_rstride,
+                             int32_t n_max, const int32_t* lengths, float scale, const float* lse,
+                             const float* acc, int64_t acc_bstride, float decay, float* out,
+                             int64_t out_bstride, int32_t* dev_err, void* stream);
+mla_status mla_cache_weights_fp4kv(mla_dims dims, mla_dtype dtype, int32_t B, int32_t T,
+                                   const void* q_tilde, int64_t ldqt, const void* q_pe, int64_t ldqp,
+                                   const uint8_t* c4, int64_t c4_bstride, int64_t c4_rstride,
+                                   const uint8_t* kv_scale, int64_t sc_bstride, int64_t sc_rstride,
+                                   const void* k_r, int64_t kr_bstride, int64_t kr_rstride, float latent_scale,
+                                   int32_t n_max, const int32_t* lengths, float scale, const float* lse,
+                                   const float* acc, int64_t acc_bstride, float decay, float* out,
+                                   int64_t out_bstride, int32_t* dev_err, void* stream);
+
+/* One row array of a cache, of any type: row t of sequence b is the row_bytes bytes at
+ * base + b*bstride + t*rstride (strides in BYTES). */
+#define MLA_MAX_PLANES 4
+typedef struct {
+  void* base;
+  int64_t bstride, rstride;
+  int32_t row_bytes;
+} mla_rows;
+
+/*
+ * mla_cache_evict - keep `keep` rows of every sequence that holds more: its first `sink` rows, its last
+ * `recent` rows, and of the rest the rows of largest acc (ties: the lower row; a NaN counts as the
+ * least).  The kept rows at and behind `keep` move into the rows before it that go, in ascending order each; all
+ * other rows stay where they are.  Attention does not depend on the order of the rows; the next token
+ * of the sequence goes to row new_lengths[b] (mla_cache_append_at, mla_cache_append_fp4).
+ *   planes      HOST array of 1 .. MLA_MAX_PLANES row arrays that move together (c_kv and k_r; c8, kv_scale
+ *               and k_r; c4, kv_scale and k_r; acc itself as 4-byte rows, to keep it in step)
+ *   acc         float, element (b, t) at acc[b*acc_bstride + t] (mla_cache_weights)
+ *   lengths     DEVICE int32 [B] in [0, n_max]; another length sets MLA_ERR_LENGTH, the sequence's new
+ *               length is 0 and none of its rows move
+ *   keep        1 <= keep <= n_max; sink, recent >= 0, sink + recent <= keep
+ *   new_lengths DEVICE int32 [B]: min(lengths[b], keep); may be lengths itself
+ *   row_map     DEVICE int32 [B, keep]: the row that row i held before, -1 for i >= new_lengths[b]
+ *   n_max <= 400000, B <= 65535.  Planes must not overlap.  Asynchronous on `stream`.
+ */
+mla_status mla_cache_evict(int32_t B, int32_t n_max, const mla_rows* planes, int32_t n_planes,
+                           const float* acc, int64_t acc_bstride, const int32_t* lengths,
+                           int32_t keep, int32_t sink, int32_t recent, int32_t* new_lengths, int32_t* row_map,
+                           int32_t* dev_err, void* stream);
 
 /*
  * mla_check_topk - opt-in validation of a top-k index array before a sparse decode.  The pages'

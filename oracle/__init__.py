@@ -10,9 +10,17 @@ the absorb/naive identity, closed forms (one cached row, zero query, two keys),
 library special cases (``scaled_dot_product_attention`` in fp64), brute-force
 top-k masking, the page's parameter counts and cache-size formulas, the RMSNorm and
 rotation invariants of the cache append, the FP8 codes and block scales of the FP8 latent
-cache (``tests/test_oracle_fp8kv.py``), and planted mistakes that must be caught.  Every function here has at least one such pin.
+cache (``tests/test_oracle_fp8kv.py``), the 4-bit codes, attention weights and evictions of
+``tests/test_oracle_cache.py``, and planted mistakes that must be caught.  Every function here has at least one such pin.
 """
 
+from .cache_oracle import (  # noqa: F401
+    cache_append_fp4,
+    evict_map,
+    fp4_quantise,
+    fp4_values,
+    token_weights,
+)
 from .mla_oracle import (  # noqa: F401
     absorb_q,
     absorbed_decode,
