@@ -21,6 +21,30 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t (&h)[4]) {
       : "r"(w));
 }
 
+// Eight codes (one word) to four bf16 pairs: the bytes of a magnitude are looked up by a byte
+// permutation (its selectors are the codes), the sign bits come from its sign-replicating mode.
+__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t (&h)[4]) {
+  const uint32_t mag = w & 0x77777777u, sgn = w & 0x88888888u;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t m = mag >> (16 * k), s = sgn >> (16 * k);
+    // bf16 of 0 .5 1 1.5 2 3 4 6: 0000 3f00 3f80 3fc0 4000 4040 4080 40c0
+    const uint32_t lo = __byte_perm(0xc0800000u, 0xc0804000u, m);
+    const uint32_t hi = __byte_perm(0x3f3f3f00u, 0x40404040u, m);
+    uint32_t neg;  // 0x80 (plus) or 0xff (minus) in each byte
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(neg) : "r"(0x80u), "r"(s));
+    const uint32_t top = hi | ((neg << 1) & 0x80808080u);
+    h[2 * k] = __byte_perm(lo, top, 0x5140);
+    h[2 * k + 1] = __byte_perm(lo, top, 0x7362);
+  }
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // Two E4M3 scales (low and high byte) to an fp16 pair.
 __device__ __forceinline__ uint32_t scales_to_f16(uint32_t two) {
   uint32_t h;

@@ -208,20 +208,17 @@ cudaError_t decode_fp4_simt_launch(const Fp4DecodeArgs& a, void* ws, cudaStream_
   return cudaGetLastError();
 }
 
-template <typename T>
 cudaError_t weights_simt_launch(const WeightsArgs& a, cudaStream_t st) {
   const dim3 grid((a.n_max + kWarps - 1) / kWarps, a.B);
   const bool fp4 = a.kv.c4 != nullptr;
   if (a.d_c <= 512)
-    (fp4 ? weights_simt<T, 1, true> : weights_simt<T, 1, false>)<<<grid, 32 * kWarps, 0, st>>>(a);
+    (fp4 ? weights_simt<float, 1, true> : weights_simt<float, 1, false>)<<<grid, 32 * kWarps, 0, st>>>(a);
   else
-    (fp4 ? weights_simt<T, 2, true> : weights_simt<T, 2, false>)<<<grid, 32 * kWarps, 0, st>>>(a);
+    (fp4 ? weights_simt<float, 2, true> : weights_simt<float, 2, false>)<<<grid, 32 * kWarps, 0, st>>>(a);
   return cudaGetLastError();
 }
 
 template cudaError_t decode_fp4_simt_launch<float>(const Fp4DecodeArgs&, void*, cudaStream_t);
 template cudaError_t decode_fp4_simt_launch<__nv_bfloat16>(const Fp4DecodeArgs&, void*, cudaStream_t);
-template cudaError_t weights_simt_launch<float>(const WeightsArgs&, cudaStream_t);
-template cudaError_t weights_simt_launch<__nv_bfloat16>(const WeightsArgs&, cudaStream_t);
 
 }  // namespace mla

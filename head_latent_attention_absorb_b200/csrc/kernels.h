@@ -38,8 +38,8 @@ template <typename T>
 cudaError_t decode_fp4_simt_launch(const Fp4DecodeArgs& a, void* ws, cudaStream_t st);
 
 // ---- attention weights and eviction ------------------------------------------------------------
-template <typename T>
-cudaError_t weights_simt_launch(const WeightsArgs& a, cudaStream_t st);
+cudaError_t weights_simt_launch(const WeightsArgs& a, cudaStream_t st);  // fp32
+cudaError_t weights_tc_launch(const WeightsArgs& a, cudaStream_t st);  // bf16
 cudaError_t evict_launch(const EvictArgs& a, cudaStream_t st);
 int evict_max_rows();
 

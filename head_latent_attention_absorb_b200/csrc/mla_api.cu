@@ -677,8 +677,8 @@ mla_status mla_cache_weights(mla_dims dims, mla_dtype dtype, int32_t B, int32_t 
   a.kv.c_kv = c_kv; a.kv.ckv_b = ckv_bstride; a.kv.ckv_r = ckv_rstride;
   a.lse = lse; a.acc = acc; a.acc_b = acc_bstride; a.decay = decay; a.out = out; a.out_b = out_bstride;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == MLA_BF16 ? mla::weights_simt_launch<__nv_bfloat16>(a, st)
-                                          : mla::weights_simt_launch<float>(a, st);
+  const cudaError_t e = dtype == MLA_BF16 ? mla::weights_tc_launch(a, st)
+                                          : mla::weights_simt_launch(a, st);
   return cuda_status(e, "mla_cache_weights launch");
 }
 
@@ -702,8 +702,8 @@ mla_status mla_cache_weights_fp4kv(mla_dims dims, mla_dtype dtype, int32_t B, in
   a.kv.latent_scale = latent_scale;
   a.lse = lse; a.acc = acc; a.acc_b = acc_bstride; a.decay = decay; a.out = out; a.out_b = out_bstride;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == MLA_BF16 ? mla::weights_simt_launch<__nv_bfloat16>(a, st)
-                                          : mla::weights_simt_launch<float>(a, st);
+  const cudaError_t e = dtype == MLA_BF16 ? mla::weights_tc_launch(a, st)
+                                          : mla::weights_simt_launch(a, st);
   return cuda_status(e, "mla_cache_weights_fp4kv launch");
 }
 

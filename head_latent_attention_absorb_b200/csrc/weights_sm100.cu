@@ -1,0 +1,393 @@
+// Attention weights of the cached rows on tcgen05 tensor cores (sm_100a):
+//   out[t] = [t < L - T] decay acc[t] + sum over query rows r of exp(scale (q_r . key_t) - lse_r)
+// with the R = T n_h query rows of a sequence, q_r = [q~ | q_pe] and key_t = [c_t | k^R_t] (576 features).
+//
+// The scores are computed transposed, S^T = K Q^T: the 128 keys of a tile are the rows (TMEM lanes) of the
+// accumulator and up to 128 query rows its columns, so the sum over query rows is a sum within a thread and
+// nothing is exchanged.  Since lse is known there is no running maximum and no second pass.
+//
+// Bound: a bf16 cache by its bytes (1152 a row against 1152 n_h T / 8192 cycles of the tensor pipe at 128
+// heads), a 4-bit cache (416 bytes a row) by shared memory: a tile's MMAs read A and B there, 8 KB per 64
+// cycles, and the decoded tile is written there as well.
+//
+// * One CTA per SM takes an equal share of the batch's 128-key tiles.  The query rows of its sequence (144 KB
+//   in nine 64-feature slabs) stay in shared memory; the keys pass through a ring of five 16 KB slabs.
+// * bf16 cache: TMA boxes fill the ring.  4-bit cache: eight warps load codes and scales into registers one
+//   tile ahead and write bf16 slabs (code * scale * latent_scale is exact in bf16) in the same layout.
+// * The accumulator is double-buffered, so the four warps that take exponentials and sums run beside the
+//   next tile's MMAs.
+// * More than 128 query rows: groups of 128, one after the other over pieces of four tiles, so that the
+//   repeated reads of the keys come from L2.
+// * Every wait is bounded; on expiry the kernel records MLA_ERR_TIMEOUT, lets its copies land and returns.
+#include <math.h>
+
+#include "common.cuh"
+#include "fp4.cuh"
+#include "kernels.h"
+#include "sm100_ptx.cuh"
+#include "tile_range.cuh"
+#include "tma_host.h"
+
+namespace mla {
+namespace weights_tc {
+
+using namespace sm100;
+
+constexpr int kDC = 512, kDR = 64;
+constexpr int kTile = 128;                   // keys per tile: the rows of an MMA
+constexpr int kRows = 128;                   // query rows per group: its columns
+constexpr int kSlabs = (kDC + kDR) / 64;     // 64-feature slabs of a row
+constexpr int kSlabBytes = kTile * 128;      // 128 rows of 64 bf16 features
+constexpr int kStages = 5;
+constexpr int kGroupPiece = 4;               // tiles per piece when several groups pass over them
+constexpr int kQWarp = 6, kKeyWarp = 5, kMmaWarp = 4, kDecodeWarp0 = 7, kDecodeWarps = 8;
+constexpr int kThreadsBf16 = 32 * kDecodeWarp0, kThreadsFp4 = 32 * (kDecodeWarp0 + kDecodeWarps);
+constexpr uint32_t kTmemCols = 256;          // two accumulators of 128 columns
+constexpr uint64_t kWaitLimitNs = 1000000000ull;
+
+struct Params {
+  CUtensorMap tm_ckv;  // bf16 cache: (d_c, n_max, B), box (64, 128, 1), 128-byte swizzle
+  CUtensorMap tm_kr;   // (d_r, n_max, B), same box
+  CUtensorMap tm_q;    // (d_c, R, B) query rows, same box: rows past R read as zeros
+  CUtensorMap tm_qp;   // (d_r, R, B)
+  CacheView kv;        // 4-bit cache
+  const int32_t* lengths;
+  int B, T, n_h, n_max, ckv_z, kr_z;  // z: 0 where all sequences share one cache (batch stride 0)
+  float scale_log2;
+  const float* lse;
+  const float* acc;
+  int64_t acc_b;
+  float decay;
+  float* out;
+  int64_t out_b;
+  int32_t* err;
+};
+
+struct Smem {
+  uint64_t full[kStages], empty[kStages], q_full, q_empty, s_full[2], s_empty[2], drain;
+  alignas(16) float neg_lse[kRows];  // -lse in log2 units, -inf for absent and dropped rows
+  int dropped[4];        // some present row of the quarter has no softmax
+  uint32_t tmem_base;
+  int abort, never;
+  TileRange range;
+};
+constexpr int kRingOff = kSlabs * kSlabBytes;
+constexpr int kSmemOff = kRingOff + kStages * kSlabBytes;
+constexpr int kSmemBytes = kSmemOff + (int)sizeof(Smem) + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory above 227 KB");
+
+// Bounded wait that records its own expiry.
+__device__ __forceinline__ bool wait(Smem& sm, uint64_t& bar, uint32_t parity, int32_t* err) {
+  if (mbar_wait(smem_u32(&bar), parity, &sm.abort, kWaitLimitNs)) return true;
+  raise_error(err, MLA_ERR_TIMEOUT);
+  sm.abort = 1;
+  return false;
+}
+
+// Calls f(b, length, group, first tile, end tile) for every pass of this CTA: all groups of query rows over
+// a piece of a sequence, then the next piece.
+template <typename F>
+__device__ __forceinline__ void for_each_pass(const Params& p, const Smem& sm, F f) {
+  const int groups = (p.T * p.n_h + kRows - 1) / kRows;
+  for_each_piece<kTile>(sm.range, p.lengths, p.B, p.T, p.n_max, [&](int b, int len, int begin, int end) {
+    const int step = groups > 1 ? kGroupPiece : end - begin;
+    for (int t0 = begin; t0 < end; t0 += step)
+      for (int g = 0; g < groups; ++g)
+        if (!f(b, len, g, t0, min(t0 + step, end))) return false;
+    return true;
+  });
+}
+
+// One lane's part of a tile of the 4-bit cache: key t, 32 features of every latent slab and half the rotary
+// row; and the tile's slabs written in the layout of the TMA boxes.
+struct KeyPart {
+  uint4 code[8], scale[2], rope[4];
+};
+__device__ __forceinline__ void load_part(const Params& p, int b, int t, int len, int half, KeyPart& k) {
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) k.code[j] = zero;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) k.rope[j] = zero;
+  k.scale[0] = k.scale[1] = zero;
+  if (t >= len) return;  // rows behind the sequence may hold anything, or not exist
+  const uint4* c = reinterpret_cast<const uint4*>(p.kv.c4 + b * p.kv.c4_b + t * p.kv.c4_r) + half;
+  const uint4* s = reinterpret_cast<const uint4*>(p.kv.sc + b * p.kv.sc_b + t * p.kv.sc_r);
+  const uint4* r = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.kv.k_r) + b * p.kv.kr_b +
+                                                  t * p.kv.kr_r) + 4 * half;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) k.code[j] = __ldg(c + 2 * j);
+  k.scale[0] = __ldg(s);
+  k.scale[1] = __ldg(s + 1);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) k.rope[j] = __ldg(r + j);
+}
+
+template <bool kFp4>
+__global__ void __launch_bounds__(kFp4 ? kThreadsFp4 : kThreadsBf16, 1) weights_kernel(const __grid_constant__ Params p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Smem& sm = *reinterpret_cast<Smem*>(smem + kSmemOff);
+  const uint32_t q_addr = smem_u32(smem), ring = smem_u32(smem + kRingOff);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int R = p.T * p.n_h;
+
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(smem_u32(&sm.full[s]), kFp4 ? kDecodeWarps : 1);
+      mbar_init(smem_u32(&sm.empty[s]), 1);
+    }
+    mbar_init(smem_u32(&sm.q_full), 1);
+    mbar_init(smem_u32(&sm.q_empty), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sm.s_full[i]), 1);
+      mbar_init(smem_u32(&sm.s_empty[i]), 4);
+    }
+    mbar_init(smem_u32(&sm.drain), 1);
+    sm.abort = sm.never = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&sm.tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  griddep_wait();
+  if (warp == 0) tile_range<kTile>(p.lengths, p.B, p.T, p.n_max, blockIdx.x, gridDim.x, p.err, &sm.range);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+
+  if (warp == kQWarp) {
+    // ---------------------------------------------------------------- the query rows of each pass
+    if (lane == 0) {
+      const uint64_t pol = policy_evict_last();
+      uint32_t pass = 0;
+      for_each_pass(p, sm, [&](int b, int, int g, int, int) {
+        if (!wait(sm, sm.q_empty, (pass & 1u) ^ 1u, p.err)) return false;
+        const uint32_t bar = smem_u32(&sm.q_full);
+        mbar_arrive_expect_tx(bar, kSlabs * kSlabBytes);
+        for (int j = 0; j < kSlabs - 1; ++j) tma_load_3d(q_addr + j * kSlabBytes, &p.tm_q, bar, 64 * j, kRows * g, b, pol);
+        tma_load_3d(q_addr + (kSlabs - 1) * kSlabBytes, &p.tm_qp, bar, 0, kRows * g, b, pol);
+        ++pass;
+        return true;
+      });
+      if (pass > 0) mbar_wait(smem_u32(&sm.q_full), (pass - 1) & 1u, &sm.never, kWaitLimitNs);
+    }
+    __syncwarp();
+  } else if (!kFp4 && warp == kKeyWarp) {
+    // ---------------------------------------------------------------- bf16 keys by TMA
+    if (lane == 0) {
+      const uint64_t pol = R > kRows ? policy_evict_last() : policy_evict_first();
+      uint32_t n = 0;
+      for_each_pass(p, sm, [&](int b, int, int, int t0, int t1) {
+        for (int t = t0; t < t1; ++t)
+          for (int j = 0; j < kSlabs; ++j, ++n) {
+            const uint32_t st = n % kStages;
+            if (!wait(sm, sm.empty[st], ((n / kStages) & 1u) ^ 1u, p.err)) return false;
+            const uint32_t bar = smem_u32(&sm.full[st]), dst = ring + st * kSlabBytes;
+            mbar_arrive_expect_tx(bar, kSlabBytes);
+            if (j < kSlabs - 1)
+              tma_load_3d(dst, &p.tm_ckv, bar, 64 * j, t * kTile, b * p.ckv_z, pol);
+            else
+              tma_load_3d(dst, &p.tm_kr, bar, 0, t * kTile, b * p.kr_z, pol);
+          }
+        return true;
+      });
+      for (uint32_t k = n > kStages ? n - kStages : 0; k < n; ++k)
+        mbar_wait(smem_u32(&sm.full[k % kStages]), (k / kStages) & 1u, &sm.never, kWaitLimitNs);
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ---------------------------------------------------------------- S^T = K Q^T
+    if (lane == 0) {
+      uint32_t n = 0, tile = 0, pass = 0;
+      for_each_pass(p, sm, [&](int, int, int g, int t0, int t1) {
+        const int cols = (min(R - kRows * g, kRows) + 31) & ~31;  // zero rows pad to the readers' 32 columns
+        const uint32_t idesc = idesc_bf16_f32(kTile, cols, 0, 0);
+        if (!wait(sm, sm.q_full, pass & 1u, p.err)) return false;
+        for (int t = t0; t < t1; ++t, ++tile) {
+          const uint32_t buf = tile & 1u;
+          if (!wait(sm, sm.s_empty[buf], ((tile >> 1) & 1u) ^ 1u, p.err)) return false;
+          tc_fence_after();
+          for (int j = 0; j < kSlabs; ++j, ++n) {
+            const uint32_t st = n % kStages;
+            if (!wait(sm, sm.full[st], (n / kStages) & 1u, p.err)) return false;
+            tc_fence_after();
+            const uint32_t a = ring + st * kSlabBytes, q = q_addr + j * kSlabBytes;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ss(tmem + buf * kRows, smem_desc(a + 32 * k, 16, 1024, kSwizzle128),
+                     smem_desc(q + 32 * k, 16, 1024, kSwizzle128), idesc, j > 0 || k > 0 ? 1u : 0u);
+            mma_commit(smem_u32(&sm.empty[st]));
+          }
+          mma_commit(smem_u32(&sm.s_full[buf]));
+        }
+        mma_commit(smem_u32(&sm.q_empty));
+        ++pass;
+        return true;
+      });
+      mma_commit(smem_u32(&sm.drain));
+      mbar_wait(smem_u32(&sm.drain), 0, &sm.never, kWaitLimitNs);
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    // ---------------------------------------------------------------- exponentials and sums, one key per thread
+    // After a failed wait the warp still walks its passes, without the tiles: the four warps meet there.
+    uint32_t tile = 0;
+    bool dead = false;
+    for_each_pass(p, sm, [&](int b, int len, int g, int t0, int t1) {
+      const int rows = min(R - kRows * g, kRows), cols = (rows + 31) & ~31;
+      named_bar_sync(1, 128);  // the previous pass has read its values
+      {
+        const int r = threadIdx.x;
+        const float lse = r < rows ? p.lse[(int64_t)b * R + kRows * g + r] : -INFINITY;
+        sm.neg_lse[r] = lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f;
+        const bool d = __any_sync(0xffffffffu, r < rows && lse == -INFINITY);
+        if (lane == 0) sm.dropped[warp] = d;
+      }
+      named_bar_sync(1, 128);
+      const bool dropped = sm.dropped[0] | sm.dropped[1] | sm.dropped[2] | sm.dropped[3];
+      const uint32_t nl = smem_u32(sm.neg_lse);
+      for (int t = t0; t < t1 && !dead; ++t, ++tile) {
+        const uint32_t buf = tile & 1u, src = tmem + ((uint32_t)(32 * warp) << 16) + buf * kRows;
+        dead = !__all_sync(0xffffffffu, wait(sm, sm.s_full[buf], (tile >> 1) & 1u, p.err));
+        if (dead) break;
+        tc_fence_after();
+        const int key = t * kTile + 32 * warp + lane;
+        // some row of this tile is not seen by every token, or a query row gave no weight: select
+        const bool select = dropped || (p.T > 1 && (t + 1) * kTile > len - p.T);
+        const int first = max(0, key - (len - p.T)) * p.n_h - kRows * g;  // first query row that sees the key
+        float w[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int c = 0; c < cols; c += 32) {
+          uint32_t s[32];
+          tmem_ld32(src + c, s);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 l4 = ld_shared_v4(nl + 4 * (c + i));
+            const float l[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float x = ex2f_approx(fmaf(__uint_as_float(s[i + e]), p.scale_log2, l[e]));
+              w[e] += select && (c + i + e < first || l[e] == -INFINITY) ? 0.f : x;
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.s_empty[buf]));
+        if (key < len) {
+          float* out = p.out + b * p.out_b + key;
+          float sum = (w[0] + w[1]) + (w[2] + w[3]);
+          if (g > 0)
+            sum += *out;
+          else if (p.acc != nullptr && key < len - p.T)
+            sum = fmaf(p.decay, p.acc[b * p.acc_b + key], sum);
+          *out = sum;
+        }
+      }
+      return true;
+    });
+  } else if (kFp4 && warp >= kDecodeWarp0) {
+    // ---------------------------------------------------------------- 4-bit keys to bf16 slabs
+    // Lane pairs own a key: each lane 32 of the 64 features of every slab, so a load instruction reads whole
+    // 32-byte sectors and the eight lanes of a store phase hit distinct banks.
+    const int row = 16 * (warp - kDecodeWarp0) + (lane >> 1), half = lane & 1;
+    const uint32_t dst_row = ring + row * 128;
+    uint32_t n = 0;
+    KeyPart k;
+    for_each_pass(p, sm, [&](int b, int len, int, int t0, int t1) {
+      load_part(p, b, t0 * kTile + row, len, half, k);
+      for (int t = t0; t < t1; ++t) {
+#pragma unroll
+        for (int j = 0; j < kSlabs; ++j, ++n) {
+          const uint32_t st = n % kStages;
+          if (!__all_sync(0xffffffffu, wait(sm, sm.empty[st], ((n / kStages) & 1u) ^ 1u, p.err))) return false;
+          const uint32_t dst = dst_row + st * kSlabBytes;
+          if (j < kSlabs - 1) {
+            const uint32_t sw[8] = {k.scale[0].x, k.scale[0].y, k.scale[0].z, k.scale[0].w,
+                                    k.scale[1].x, k.scale[1].y, k.scale[1].z, k.scale[1].w};
+            const float2 s2 = unpack_f16x2(fp4::scales_to_f16(sw[j] >> (16 * half)));
+            const float s0 = s2.x * p.kv.latent_scale, s1 = s2.y * p.kv.latent_scale;
+            const uint32_t scale[2] = {pack_bf16x2(s0, s0), pack_bf16x2(s1, s1)};
+            const uint32_t words[4] = {k.code[j].x, k.code[j].y, k.code[j].z, k.code[j].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t h[4];
+              fp4::codes_to_bf16(words[i], h);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) h[e] = fp4::mul_bf16x2(h[e], scale[i >> 1]);
+              st_shared_v4_b32(dst + (((4 * half + i) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              st_shared_v4_b32(dst + (((4 * half + i) ^ (row & 7)) << 4), k.rope[i].x, k.rope[i].y, k.rope[i].z,
+                               k.rope[i].w);
+            if (t + 1 < t1) load_part(p, b, (t + 1) * kTile + row, len, half, k);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm.full[st]));
+        }
+      }
+      return true;
+    });
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+bool make_map(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1_bytes,
+              uint64_t s2_bytes) {
+  const uint64_t dims[3] = {d0, d1, d2}, strides[2] = {s1_bytes, s2_bytes};
+  const uint32_t box[3] = {64, 128, 1};
+  return make_tensor_map_bf16(m, base, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// A cache map; sequences that share one cache (batch stride 0) become one.
+bool make_cache_map(CUtensorMap* m, const void* base, int width, int n_max, int B, int64_t row, int64_t batch, int* z) {
+  *z = B > 1 && batch != 0;
+  const uint64_t rb = (uint64_t)row * 2;
+  return make_map(m, base, width, n_max, *z ? B : 1, rb, *z ? (uint64_t)batch * 2 : rb * n_max);
+}
+
+template <bool kFp4>
+cudaError_t launch(const Params& p, int grid, cudaStream_t st) {
+  const cudaError_t e = cudaFuncSetAttribute(weights_kernel<kFp4>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(weights_kernel<kFp4>, dim3(grid), dim3(kFp4 ? kThreadsFp4 : kThreadsBf16), kSmemBytes, st, p);
+}
+
+}  // namespace weights_tc
+
+cudaError_t weights_tc_launch(const WeightsArgs& a, cudaStream_t st) {
+  using namespace weights_tc;
+  const bool fp4 = a.kv.c4 != nullptr;
+  const int R = a.T * a.n_h;
+  Params p{};
+  if (!make_map(&p.tm_q, a.q_tilde, kDC, R, a.B, (uint64_t)a.ldqt * 2, (uint64_t)a.ldqt * 2 * R) ||
+      !make_map(&p.tm_qp, a.q_pe, kDR, R, a.B, (uint64_t)a.ldqp * 2, (uint64_t)a.ldqp * 2 * R))
+    return cudaErrorInvalidValue;
+  if (!fp4 && (!make_cache_map(&p.tm_ckv, a.kv.c_kv, kDC, a.n_max, a.B, a.kv.ckv_r, a.kv.ckv_b, &p.ckv_z) ||
+               !make_cache_map(&p.tm_kr, a.kv.k_r, kDR, a.n_max, a.B, a.kv.kr_r, a.kv.kr_b, &p.kr_z)))
+    return cudaErrorInvalidValue;
+  p.kv = a.kv;
+  p.lengths = a.lengths;
+  p.B = a.B; p.T = a.T; p.n_h = a.n_h; p.n_max = a.n_max;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.lse = a.lse; p.acc = a.acc; p.acc_b = a.acc_b; p.decay = a.decay;
+  p.out = a.out; p.out_b = a.out_b; p.err = a.err;
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int64_t tiles = (int64_t)a.B * ((a.n_max + kTile - 1) / kTile);
+  const int grid = (int)(tiles < sms ? tiles : sms);
+  return fp4 ? launch<true>(p, grid, st) : launch<false>(p, grid, st);
+}
+
+}  // namespace mla
