@@ -1,0 +1,835 @@
+// Absorbed decode over the 4-bit latent cache on tcgen05 tensor cores (sm_100a):
+//   z[r, t] = scale (q~_r . c_t + q_pe,r . k^R_t),  ctx_r = sum_t softmax(z)_t c_t,  lse_r = log sum_t exp z
+// for the R = T n_h query rows r of a sequence (row r belongs to new token r / n_h and sees the rows
+// t <= L - T + r / n_h), c_t = code * scale decoded on chip.
+//
+// Bound: the tensor pipe.  A cached row costs 2 R (2 d_c + d_r) operations against 416 bytes: at R = 128
+// 669 a byte, far right of the GPU's ridge.
+//
+// Why this split.  The fp32 context of 128 rows x 512 features fills TMEM, so no SM can hold it beside
+// scores.  A CTA therefore keeps one half of the latent features of the context (256 columns) and computes
+// all 576 features of the scores itself: the score work is done twice, 27.3 instead of 17.8 MFLOP per 64
+// rows and two CTAs, and in return nothing is exchanged, no CTA waits for another one and the halves need
+// not even run at the same time.  (Exchanging partial scores between two CTAs through distributed shared
+// memory holds the bf16 decode at one third of the tensor peak.)
+//
+// * Operands are fp16: code * scale has at most six significant bits and lies in 2^-10 .. 2688, so the cache
+//   is exact; a query row is scaled by a power of two that puts its largest element into [2^14, 2^15), so that
+//   bf16 elements are exact down to 2^-31 of it, and the power goes into the row's softmax scale.  The rotary
+//   part stays in bf16 (separate MMAs into the same accumulator).  Probabilities are rounded to fp16.
+// * Tiles of 64 keys.  TMEM: context 256 columns, scores 64, query features [0, 384) 192 columns as the A
+//   operand; the other query features and the probabilities are A operands in shared memory.
+// * Nine warps decode: lane pairs own a key, 16-byte loads of codes two tiles ahead in registers, cvt to fp16,
+//   one product with the block's scale, stores in the 128-byte-swizzled layout.  The four slabs of the
+//   CTA's own half serve the scores (K-major) and the values (MN-major) and stay until the values are used: three
+//   buffers.  The other half's slabs and the rotary slab are free once the scores are done: a ring of eight.
+// * MMA order S(t + 1), O(t), S(t + 2), ...: the softmax of tile t runs under S(t + 1), and the tensor pipe
+//   works on O(t - 1) while S(t) is read from TMEM.
+// * Four softmax warps, one query row per thread; base-2 exponentials, their reference moved (and the context
+//   rescaled in TMEM) only when the running maximum grows by more than 8.
+// * Work: chunks of single sequences when each can have CTAs of its own and the chunks come out balanced, else
+//   equal ranges of all tiles.  A sequence that is cut leaves fp32 partials and a second kernel joins them in a
+//   fixed order.
+// * Every wait is bounded; on expiry the kernel records MLA_ERR_TIMEOUT and all warps run out their barriers.
+#include <math.h>
+
+#include "common.cuh"
+#include "fp4.cuh"
+#include "kernels.h"
+#include "sm100_ptx.cuh"
+
+namespace mla {
+namespace decode_fp4 {
+
+using namespace sm100;
+
+constexpr int kDC = 512;
+constexpr int kTile = 64;                        // keys per tile
+constexpr int kRows = 128;                       // query rows per group: the rows of every MMA
+constexpr int kSlabBytes = kTile * 128;          // 64 keys of 64 features
+constexpr int kKvStages = 3, kKvBytes = 4 * kSlabBytes;
+constexpr int kKSlots = 8, kKPerTile = 5;        // rotary slab and the other half's four slabs
+constexpr int kQSlabBytes = kRows * 128;         // 128 query rows of 64 features
+constexpr int kQTmemSlabs = 6;                   // query slabs in TMEM; the other two and the rotary one in shared memory
+constexpr int kKOff = kKvStages * kKvBytes;
+constexpr int kQOff = kKOff + kKSlots * kSlabBytes;
+constexpr int kPOff = kQOff + 3 * kQSlabBytes;
+constexpr int kSmemOff = kPOff + kRows * 128;
+static_assert(kQTmemSlabs * kQSlabBytes <= kQOff, "the query is staged in the key buffers");
+static_assert(kRows * 256 * 4 <= kQOff, "the partial context is staged in the key buffers");
+constexpr int kMmaWarp = 4, kKvWarp0 = 5, kKWarp0 = 9, kRopeWarp = 13;
+constexpr int kThreads = 32 * 14;
+constexpr int kQLoaders = 12;                    // softmax and latent decode warps load the query
+constexpr uint32_t kTmemCols = 512, kColO = 0, kColS = 256, kColQ = 320;
+// Probabilities are 2^(z - ref): ref is set kRaise below the largest score so far (log2 units) and moved up
+// only when a score passes it by kRescale.  So they reach 2^15 at most (fp16 ends at 2^16), the sum is at
+// least 2^kRaise, and a probability that fp16's subnormals round (2^-25) is off by 2^-32 of the sum.
+constexpr float kRaise = 7.f, kRescale = 15.f;
+constexpr int kPlanRegs = 8;                     // items per lane that the chunk search holds
+constexpr int kSwitchTiles = 5;                  // what a second piece costs a CTA, in tiles
+constexpr uint64_t kWaitLimitNs = 1000000000ull;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct Params {
+  CacheView kv;
+  const __nv_bfloat16* q_tilde;
+  const __nv_bfloat16* q_pe;
+  int64_t ldqt, ldqp;
+  const int32_t* lengths;
+  int B, T, n_h, n_max, R, groups, pairs;
+  float scale_log2;
+  __nv_bfloat16* ctx;
+  float* lse;
+  int4* table;    // [B * groups] partials of an item: first slot, first CTA pair, number
+  float2* ws_ml;  // [2 pairs slots][2 halves][128] (reference in log2 units, sum)
+  float* ws_o;    // [slots][2 halves][min(R, 128)][256], 16-byte chunk j of row r at (j + r) % 64
+  int32_t* err;
+};
+
+// An item is a group of up to 128 query rows of one sequence.  Keys its last row sees, 0 for a bad length.
+__device__ __forceinline__ int item_keys(const Params& p, int i) {
+  const int len = p.lengths[i / p.groups];
+  if (len < p.T || len > p.n_max) return 0;
+  const int last = min(p.R, kRows * (i % p.groups + 1)) - 1;
+  return len - p.T + last / p.n_h + 1;
+}
+__device__ __forceinline__ int item_tiles(const Params& p, int i) { return (item_keys(p, i) + kTile - 1) / kTile; }
+
+// A CTA pair's share: pieces of items.
+struct Plan {
+  long long lo, hi, tb, total;  // tiles [lo, hi) of all items' tiles laid end to end; first tile of `item`
+  int item, chunk, c0, n;       // chunk > 0: one piece, the (pair - c0)-th of item's n chunks
+  int nc;                       // pairs that have work
+};
+struct Piece {
+  int item, begin, end, tiles;  // item < 0: none left
+  int slot, c0, n;              // where its partial goes; first pair and number of the item's pieces
+};
+
+struct Smem {
+  uint64_t kv_full[kKvStages], kv_empty[kKvStages], k_full[kKSlots], k_empty[kKSlots];
+  uint64_t s_full, s_empty, p_full, pv_done, drain;
+  alignas(16) float row_scale[kRows];  // softmax scale of a query row, log2 units
+  Plan plan;
+  Piece piece;
+  uint32_t tmem_base;
+  int abort, never;
+};
+constexpr int kSmemBytes = kSmemOff + (int)sizeof(Smem) + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory above 227 KB");
+
+__device__ __forceinline__ bool wait(Smem& sm, uint64_t& bar, uint32_t parity, int32_t* err) {
+  if (mbar_wait(smem_u32(&bar), parity, &sm.abort, kWaitLimitNs)) return true;
+  raise_error(err, MLA_ERR_TIMEOUT);
+  sm.abort = 1;
+  return false;
+}
+// All lanes wait; the warp goes on only if all of them saw the phase complete.
+__device__ __forceinline__ bool wait_warp(Smem& sm, uint64_t& bar, uint32_t parity, int32_t* err) {
+  return __all_sync(0xffffffffu, wait(sm, bar, parity, err));
+}
+
+__device__ __forceinline__ int warp_sum_int(int v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ int warp_max_int(int v) { return __reduce_max_sync(0xffffffffu, v); }
+
+// One warp: the share of pair c.
+__device__ void make_plan(const Params& p, int c, Plan* out) {
+  const int lane = threadIdx.x & 31, items = p.B * p.groups;
+  long long total = 0;
+  int longest = 0, nonempty = 0, nt[kPlanRegs];
+  bool bad = false;
+#pragma unroll
+  for (int k = 0; k < kPlanRegs; ++k) nt[k] = 0;
+  for (int i0 = 0, k = 0; i0 < items; i0 += 32, ++k) {
+    const int n = i0 + lane < items ? item_tiles(p, i0 + lane) : 0;
+    bad |= i0 + lane < items && n == 0;
+#pragma unroll
+    for (int j = 0; j < kPlanRegs; ++j)
+      if (j == k) nt[j] = n;
+    total += n;
+    longest = max(longest, n);
+    nonempty += n > 0;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  longest = warp_max_int(longest);
+  nonempty = warp_sum_int(nonempty);
+  if (__any_sync(0xffffffffu, bad) && c == 0 && lane == 0) raise_error(p.err, MLA_ERR_LENGTH);
+  Plan r;
+  r.total = total;
+  r.nc = (int)(total < p.pairs ? total : p.pairs);
+  r.lo = r.hi = r.tb = 0;
+  r.item = items;
+  r.chunk = r.c0 = r.n = 0;
+  if (c >= r.nc) {
+    if (lane == 0) *out = r;
+    return;
+  }
+  auto chunks = [&](int size) {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < kPlanRegs; ++k) n += (nt[k] + size - 1) / size;
+    return warp_sum_int(n);
+  };
+  // the smallest chunk whose chunks fit the pairs
+  const int even = (int)((total + r.nc - 1) / r.nc);
+  if (items <= 32 * kPlanRegs && nonempty <= r.nc) {
+    int lo = even, hi = longest;
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (chunks(mid) <= r.nc)
+        hi = mid;
+      else
+        lo = mid + 1;
+    }
+    if (lo <= even + kSwitchTiles) r.chunk = lo;
+  }
+  if (r.chunk == 0) {
+    r.lo = total * c / r.nc;
+    r.hi = total * (c + 1) / r.nc;
+  }
+  long long base = 0;  // chunks or tiles before item i0
+  const long long at = r.chunk > 0 ? c : r.lo;
+  for (int i0 = 0; i0 < items; i0 += 32) {
+    const int tiles = i0 + lane < items ? item_tiles(p, i0 + lane) : 0;
+    const int n = r.chunk > 0 ? (tiles + r.chunk - 1) / r.chunk : tiles;
+    int sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, base + sum > at);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      r.item = i0 + l;
+      r.tb = base + __shfl_sync(0xffffffffu, sum - n, l);
+      r.n = __shfl_sync(0xffffffffu, n, l);
+      break;
+    }
+    base += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  r.c0 = (int)r.tb;  // chunk plan: the item's first chunk is its first pair's
+  if (lane == 0) *out = r;
+}
+
+// One thread: the next piece of pair c.
+__device__ void next_piece(const Params& p, int c, Plan& s, Piece* out) {
+  Piece r;
+  r.item = -1;
+  r.begin = r.end = r.tiles = r.slot = r.c0 = r.n = 0;
+  const int items = p.B * p.groups;
+  if (s.chunk > 0) {
+    if (s.item < items) {
+      r.item = s.item;
+      r.tiles = item_tiles(p, s.item);
+      r.begin = (c - s.c0) * s.chunk;
+      r.end = min(r.begin + s.chunk, r.tiles);
+      r.slot = 2 * c;
+      r.c0 = s.c0;
+      r.n = s.n;
+      s.item = items;
+    }
+    *out = r;
+    return;
+  }
+  for (; s.item < items && s.lo < s.hi; ++s.item) {
+    const int nt = item_tiles(p, s.item);
+    if (s.tb + nt > s.lo) {
+      const long long end = s.hi < s.tb + nt ? s.hi : s.tb + nt;
+      r.item = s.item;
+      r.tiles = nt;
+      r.begin = (int)(s.lo - s.tb);
+      r.end = (int)(end - s.tb);
+      // the pair that holds tile t is ((t + 1) nc - 1) / total
+      r.c0 = (int)(((s.tb + 1) * s.nc - 1) / s.total);
+      r.n = (int)(((s.tb + nt) * s.nc - 1) / s.total) - r.c0 + 1;
+      r.slot = 2 * c + (s.total * c / s.nc < s.tb ? 1 : 0);  // a pair's first and its later pieces
+      s.lo = end;
+      s.tb += nt;
+      ++s.item;
+      *out = r;
+      return;
+    }
+    s.tb += nt;
+  }
+  *out = r;
+}
+
+// A decode warp's lane: 32 features of one 64-feature slab for four keys of a tile.
+struct Part {
+  uint4 code[4];
+  uint32_t scale[4];
+};
+__device__ __forceinline__ void load_part(const Params& p, int b, int tile, int len, int slab, int lane, Part& k) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = tile * kTile + 16 * i + (lane >> 1);
+    k.code[i] = make_uint4(0u, 0u, 0u, 0u);
+    k.scale[i] = 0u;
+    if (t < len) {  // rows behind the sequence may hold anything, or not exist
+      k.code[i] = __ldg(reinterpret_cast<const uint4*>(p.kv.c4 + b * p.kv.c4_b + t * p.kv.c4_r + 32 * slab) + (lane & 1));
+      k.scale[i] = __ldg(reinterpret_cast<const uint16_t*>(p.kv.sc + b * p.kv.sc_b + t * p.kv.sc_r + 4 * slab) + (lane & 1));
+    }
+  }
+}
+__device__ __forceinline__ void store_part(const Part& k, uint32_t dst, int lane) {
+  const int half = lane & 1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = 16 * i + (lane >> 1);
+    const uint32_t s2 = fp4::scales_to_f16(k.scale[i]);
+    const uint32_t s[2] = {__byte_perm(s2, s2, 0x1010), __byte_perm(s2, s2, 0x3232)};
+    const uint32_t words[4] = {k.code[i].x, k.code[i].y, k.code[i].z, k.code[i].w};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      uint32_t h[4];
+      fp4::codes_to_f16(words[w], h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[e] = fp4::mul_f16x2(h[e], s[w >> 1]);
+      st_shared_v4_b32(dst + row * 128 + (((4 * half + w) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+__device__ __forceinline__ void load_rope(const Params& p, int b, int tile, int len, int lane, uint4 (&k)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = tile * kTile + 16 * i + (lane >> 1);
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.kv.k_r) + b * p.kv.kr_b +
+                                                      t * p.kv.kr_r) + 4 * (lane & 1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) k[4 * i + j] = t < len ? __ldg(src + j) : make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+__device__ __forceinline__ void store_rope(const uint4 (&k)[16], uint32_t dst, int lane) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = 16 * i + (lane >> 1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      st_shared_v4_b32(dst + row * 128 + (((4 * (lane & 1) + j) ^ (row & 7)) << 4), k[4 * i + j].x, k[4 * i + j].y,
+                       k[4 * i + j].z, k[4 * i + j].w);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ float max_abs4(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+  return m;
+}
+__device__ __forceinline__ uint4 scale_to_f16(const uint4& v, float a, float b) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = pack_f16x2_ieee(bf16_lo(w[i]) * a * b, bf16_hi(w[i]) * a * b);
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// The item's query rows: latent part as fp16 (slabs 0..5 into `stage`, 6 and 7 into the resident buffer),
+// rotary part as bf16, both times the row's power of two; rows past R as zeros.  Warp w of kQLoaders.
+__device__ __forceinline__ void load_query(const Params& p, Smem& sm, uint32_t stage, uint32_t resident, int b, int g,
+                                           int w, int lane) {
+  constexpr int kBatch = 4;
+  for (int r0 = w; r0 < kRows; r0 += kQLoaders * kBatch) {
+    uint4 lat[kBatch][2], rope[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int r = r0 + k * kQLoaders;
+      lat[k][0] = lat[k][1] = rope[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < kRows && kRows * g + r < p.R) {
+        const int64_t row = (int64_t)b * p.R + kRows * g + r;
+        const uint4* q = reinterpret_cast<const uint4*>(p.q_tilde + row * p.ldqt);
+        lat[k][0] = __ldg(q + lane);
+        lat[k][1] = __ldg(q + 32 + lane);
+        if (lane < 8) rope[k] = __ldg(reinterpret_cast<const uint4*>(p.q_pe + row * p.ldqp) + lane);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int r = r0 + k * kQLoaders;
+      if (r >= kRows) break;
+      float m = fmaxf(fmaxf(max_abs4(lat[k][0]), max_abs4(lat[k][1])) * p.kv.latent_scale, max_abs4(rope[k]));
+      m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+      // 2^e that puts the largest element into [2^14, 2^15)
+      const int e = m > 0.f ? max(-126, min(126, 14 + 127 - (int)(__float_as_uint(m) >> 23))) : 0;
+      const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int slab = (lane + 32 * h) >> 3, pos = lane & 7;
+        const uint4 v = scale_to_f16(lat[k][h], p.kv.latent_scale, mul);
+        const uint32_t base = slab < kQTmemSlabs ? stage + slab * kQSlabBytes : resident + (slab - kQTmemSlabs) * kQSlabBytes;
+        st_shared_v4_b32(base + r * 128 + ((pos ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
+      }
+      if (lane < 8) {
+        const uint32_t x[4] = {rope[k].x, rope[k].y, rope[k].z, rope[k].w};
+        uint32_t y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = pack_bf16x2(bf16_lo(x[i]) * mul, bf16_hi(x[i]) * mul);
+        st_shared_v4_b32(resident + 2 * kQSlabBytes + r * 128 + ((lane ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
+      }
+      if (lane == 0) sm.row_scale[r] = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23), 1.2e-38f);
+    }
+  }
+  fence_proxy_async_smem();
+}
+
+// One K-major 64-feature slab of the scores: query slab F (8: the rotary part) against the keys at `keys`.
+template <int F>
+__device__ __forceinline__ void slab_scores(uint32_t base, uint32_t tmem, uint32_t keys, bool first) {
+  constexpr uint32_t idesc = F < 8 ? idesc_f16_f32(kRows, kTile, 0, 0) : idesc_bf16_f32(kRows, kTile, 0, 0);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint64_t bd = smem_desc(keys + 32 * k, 16, 1024, kSwizzle128);
+    const uint32_t add = first && k == 0 ? 0u : 1u;
+    if constexpr (F < kQTmemSlabs)
+      mma_ts(tmem + kColS, tmem + kColQ + 32 * F + 8 * k, bd, idesc, add);
+    else
+      mma_ss(tmem + kColS, smem_desc(base + kQOff + (F - kQTmemSlabs) * kQSlabBytes + 32 * k, 16, 1024, kSwizzle128), bd,
+             idesc, add);
+  }
+}
+
+// The score MMAs of tile `it` for the CTA of half H: its own half's slabs, the rotary one, the other half's.
+template <int H>
+__device__ __forceinline__ bool issue_scores(Smem& sm, uint32_t base, uint32_t tmem, uint32_t it, int32_t* err) {
+  if (!wait(sm, sm.s_empty, (it & 1u) ^ 1u, err)) return false;
+  const uint32_t st = it % kKvStages, kv = base + st * kKvBytes;
+  if (!wait(sm, sm.kv_full[st], (it / kKvStages) & 1u, err)) return false;
+  tc_fence_after();
+  slab_scores<4 * H>(base, tmem, kv, true);
+  slab_scores<4 * H + 1>(base, tmem, kv + kSlabBytes, false);
+  slab_scores<4 * H + 2>(base, tmem, kv + 2 * kSlabBytes, false);
+  slab_scores<4 * H + 3>(base, tmem, kv + 3 * kSlabBytes, false);
+#pragma unroll
+  for (int j = 0; j < kKPerTile; ++j) {
+    const uint32_t k = kKPerTile * it + j, slot = k % kKSlots, keys = base + kKOff + slot * kSlabBytes;
+    if (!wait(sm, sm.k_full[slot], (k / kKSlots) & 1u, err)) return false;
+    tc_fence_after();
+    if (j == 0) slab_scores<8>(base, tmem, keys, false);
+    if (j == 1) slab_scores<4 - 4 * H>(base, tmem, keys, false);
+    if (j == 2) slab_scores<5 - 4 * H>(base, tmem, keys, false);
+    if (j == 3) slab_scores<6 - 4 * H>(base, tmem, keys, false);
+    if (j == 4) slab_scores<7 - 4 * H>(base, tmem, keys, false);
+    mma_commit(smem_u32(&sm.k_empty[slot]));
+  }
+  mma_commit(smem_u32(&sm.s_full));
+  return true;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ Params p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Smem& sm = *reinterpret_cast<Smem*>(smem + kSmemOff);
+  const uint32_t base = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int pair = blockIdx.x >> 1, hf = blockIdx.x & 1;
+
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kKvStages; ++s) {
+      mbar_init(smem_u32(&sm.kv_full[s]), 4);
+      mbar_init(smem_u32(&sm.kv_empty[s]), 1);
+    }
+    for (int s = 0; s < kKSlots; ++s) {
+      mbar_init(smem_u32(&sm.k_full[s]), 1);
+      mbar_init(smem_u32(&sm.k_empty[s]), 1);
+    }
+    mbar_init(smem_u32(&sm.s_full), 1);
+    mbar_init(smem_u32(&sm.s_empty), 4);
+    mbar_init(smem_u32(&sm.p_full), 4);
+    mbar_init(smem_u32(&sm.pv_done), 1);
+    mbar_init(smem_u32(&sm.drain), 1);
+    sm.abort = sm.never = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&sm.tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  griddep_wait();
+  if (warp == 0) {
+    make_plan(p, pair, &sm.plan);
+    __syncwarp();
+    if (lane == 0) next_piece(p, pair, sm.plan, &sm.piece);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+
+  // it0: tiles of the earlier pieces.  All warps take every barrier of every piece, also after a failed wait.
+  uint32_t it0 = 0;
+  bool dead = false;
+  while (true) {
+    const Piece pc = sm.piece;
+    if (pc.item < 0) break;
+    const int b = pc.item / p.groups, g = pc.item % p.groups, len = p.lengths[b];
+    const int rows = min(p.R - kRows * g, kRows);
+    const uint32_t n = (uint32_t)(pc.end - pc.begin);
+    const bool whole = pc.n == 1;
+
+    // ------------------------------------------------------------------ query into TMEM and shared memory
+    if (warp < kQLoaders + 1 && warp != kMmaWarp)
+      load_query(p, sm, base, base + kQOff, b, g, warp < kMmaWarp ? warp : warp - 1, lane);
+    __syncthreads();
+    if (warp < 4) {
+      const int r = threadIdx.x;
+#pragma unroll
+      for (int j = 0; j < kQTmemSlabs; ++j) {
+        uint32_t v[32];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint4 u = ld_shared_v4_b32(base + j * kQSlabBytes + r * 128 + ((c ^ (r & 7)) << 4));
+          v[4 * c] = u.x;
+          v[4 * c + 1] = u.y;
+          v[4 * c + 2] = u.z;
+          v[4 * c + 3] = u.w;
+        }
+        tmem_st32(tmem + ((uint32_t)(32 * warp) << 16) + kColQ + 32 * j, v);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+
+    if (warp == kMmaWarp) {
+      // ---------------------------------------------------------------- MMAs
+      if (lane == 0 && !dead) {
+        const uint32_t id_o = idesc_f16_f32(kRows, 256, 0, 1), tO = tmem + kColO;
+        auto scores = [&](uint32_t it) {
+          return hf == 0 ? issue_scores<0>(sm, base, tmem, it, p.err) : issue_scores<1>(sm, base, tmem, it, p.err);
+        };
+        auto values = [&](uint32_t it, bool first) {
+          if (!wait(sm, sm.p_full, it & 1u, p.err)) return false;
+          tc_fence_after();
+          const uint32_t st = it % kKvStages;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ss(tO, smem_desc(base + kPOff + 32 * k, 16, 1024, kSwizzle128),
+                   smem_desc(base + st * kKvBytes + 2048 * k, kSlabBytes, 1024, kSwizzle128), id_o,
+                   !first || k > 0 ? 1u : 0u);
+          mma_commit(smem_u32(&sm.kv_empty[st]));
+          mma_commit(smem_u32(&sm.pv_done));
+          return true;
+        };
+        bool ok = scores(it0);
+        for (uint32_t t = 0; t < n && ok; ++t) {
+          if (t + 1 < n) ok = scores(it0 + t + 1);
+          ok = ok && values(it0 + t, t == 0);
+        }
+        dead = !ok;
+      }
+      __syncwarp();
+    } else if (warp < 4) {
+      // ---------------------------------------------------------------- softmax, one query row per thread
+      const int r = threadIdx.x;
+      const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+      const uint32_t tS = tmem + lanes + kColS, tO = tmem + lanes + kColO;
+      const uint32_t p_row = base + kPOff + r * 128;
+      const float sl = sm.row_scale[r];
+      // keys that the row, and the group's first row, see
+      const int limit = len - p.T + (kRows * g + min(r, rows - 1)) / p.n_h + 1;
+      const int all_see = len - p.T + (kRows * g) / p.n_h + 1;
+      float ref = -INFINITY, l = 0.f;
+      for (uint32_t t = 0; t < n && !dead; ++t) {
+        const uint32_t it = it0 + t;
+        const int k0 = (pc.begin + (int)t) * kTile;
+        dead = !wait_warp(sm, sm.s_full, it & 1u, p.err);
+        if (dead) break;
+        tc_fence_after();
+        float s[64];
+        {
+          uint32_t v[32];
+          tmem_ld32(tS, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(v[i]);
+          tmem_ld32(tS + 32, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s[32 + i] = __uint_as_float(v[i]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.s_empty));
+        if (k0 + kTile > all_see) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i) s[i] = k0 + i < limit ? s[i] : -INFINITY;
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int i = 4; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+        const float z = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
+        float f = 1.f;
+        const bool raise = z > ref + kRescale;  // ref = -inf: any finite maximum
+        if (raise) {
+          f = ex2f_approx(ref - (z - kRaise));
+          l *= f;
+          ref = z - kRaise;
+        }
+        const float neg = ref == -INFINITY ? 0.f : -ref;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t h[32];
+#pragma unroll
+        for (int i = 0; i < 64; i += 2) {
+          const float a = ex2f_approx(fmaf(s[i], sl, neg)), c = ex2f_approx(fmaf(s[i + 1], sl, neg));
+          sum[i & 2] += a;
+          sum[(i & 2) + 1] += c;
+          h[i / 2] = pack_f16x2_ieee(a, c);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        if (t > 0) {  // the last tile's probabilities are used up, its context complete
+          dead = !wait_warp(sm, sm.pv_done, (it - 1) & 1u, p.err);
+          if (dead) break;
+          if (__any_sync(0xffffffffu, raise)) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 256; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(tO + c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st32(tO + c, o);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          st_shared_v4_b32(p_row + ((c ^ (r & 7)) << 4), h[4 * c], h[4 * c + 1], h[4 * c + 2], h[4 * c + 3]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.p_full));
+      }
+      if (!dead) dead = !wait_warp(sm, sm.pv_done, (it0 + n - 1) & 1u, p.err);
+      if (!dead) {
+        // -------------------------------------------------------------- the piece's result
+        // through the idle key buffers, 16-byte chunks rotated by the row so that neither the row-wise
+        // writes nor the copies out conflict
+        tc_fence_after();
+        const uint32_t out_row = (uint32_t)b * p.R + kRows * g;  // first query row of the group
+        if (whole) {
+          const float inv = (l == 0.f ? 0.f : 1.f / l) * p.kv.latent_scale;
+          const uint32_t dst = base + r * 512;
+#pragma unroll 1
+          for (int c = 0; c < 256; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(tO + c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t v[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                v[e] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
+              st_shared_v4_b32(dst + (((c / 8 + i + r) & 31) << 4), v[0], v[1], v[2], v[3]);
+            }
+          }
+          __syncwarp();
+          for (int k = 32 * warp; k < min(32 * warp + 32, rows); ++k) {
+            const uint4 v = ld_shared_v4_b32(base + k * 512 + (((lane + k) & 31) << 4));
+            reinterpret_cast<uint4*>(p.ctx + (int64_t)(out_row + k) * kDC + 256 * hf)[lane] = v;
+          }
+          if (hf == 0 && r < rows && p.lse != nullptr)
+            p.lse[out_row + r] = l == 0.f ? -INFINITY : ref * kLn2 + logf(l);
+        } else {
+          const uint32_t dst = base + r * 1024;
+#pragma unroll 1
+          for (int c = 0; c < 256; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(tO + c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              st_shared_v4_b32(dst + (((c / 4 + i + r) & 63) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          const int64_t part = 2 * (int64_t)pc.slot + hf;
+          const int mine = min(32, rows - 32 * warp);
+          if (lane == 0 && mine > 0) {
+            bulk_store_s2g(p.ws_o + (part * min(p.R, kRows) + 32 * warp) * 256, base + 32 * warp * 1024, mine * 1024);
+            bulk_group_commit();
+            bulk_group_wait_all();
+          }
+          if (r < rows) p.ws_ml[part * kRows + r] = make_float2(ref, l);
+        }
+        if (threadIdx.x == 0 && hf == 0 && pc.begin == 0) p.table[pc.item] = make_int4(pc.slot, pc.c0, pc.n, 0);
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (threadIdx.x == 0) next_piece(p, pair, sm.plan, &sm.piece);
+      __syncwarp();
+    } else if (warp < kRopeWarp) {
+      // ---------------------------------------------------------------- latent slabs
+      const bool own = warp < kKWarp0;  // a slab of this CTA's half
+      const int j = own ? warp - kKvWarp0 : warp - kKWarp0;
+      const int slab = 4 * (own ? hf : 1 - hf) + j;
+      Part k0, k1;
+      load_part(p, b, pc.begin, len, slab, lane, k0);
+      load_part(p, b, pc.begin + 1, len, slab, lane, k1);
+      for (uint32_t t = 0; t < n && !dead; ++t) {
+        const uint32_t it = it0 + t;
+        const Part cur = k0;
+        k0 = k1;
+        if (t + 2 < n) load_part(p, b, pc.begin + t + 2, len, slab, lane, k1);
+        if (own) {
+          const uint32_t st = it % kKvStages;
+          dead = !wait_warp(sm, sm.kv_empty[st], ((it / kKvStages) & 1u) ^ 1u, p.err);
+          if (dead) break;
+          store_part(cur, base + st * kKvBytes + j * kSlabBytes, lane);
+          if (lane == 0) mbar_arrive(smem_u32(&sm.kv_full[st]));
+        } else {
+          const uint32_t q = kKPerTile * it + 1 + j, slot = q % kKSlots;
+          dead = !wait_warp(sm, sm.k_empty[slot], ((q / kKSlots) & 1u) ^ 1u, p.err);
+          if (dead) break;
+          store_part(cur, base + kKOff + slot * kSlabBytes, lane);
+          if (lane == 0) mbar_arrive(smem_u32(&sm.k_full[slot]));
+        }
+      }
+      __syncwarp();
+    } else {
+      // ---------------------------------------------------------------- rotary slab
+      uint4 k[16];
+      load_rope(p, b, pc.begin, len, lane, k);
+      for (uint32_t t = 0; t < n && !dead; ++t) {
+        const uint32_t q = kKPerTile * (it0 + t), slot = q % kKSlots;
+        dead = !wait_warp(sm, sm.k_empty[slot], ((q / kKSlots) & 1u) ^ 1u, p.err);
+        if (dead) break;
+        store_rope(k, base + kKOff + slot * kSlabBytes, lane);
+        if (lane == 0) mbar_arrive(smem_u32(&sm.k_full[slot]));
+        if (t + 1 < n) load_rope(p, b, pc.begin + t + 1, len, lane, k);
+      }
+      __syncwarp();
+    }
+    it0 += n;
+    __syncthreads();
+    tc_fence_after();
+    if (sm.abort) dead = true;
+  }
+  if (warp == kMmaWarp) {
+    if (lane == 0) {
+      mma_commit(smem_u32(&sm.drain));
+      mbar_wait(smem_u32(&sm.drain), 0, &sm.never, kWaitLimitNs);
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+// Joins the partials of items that were cut: one warp per query row and latent half, in slot order.  Rows of
+// sequences with a bad length become zeros.
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Params p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, hf = (int)(w & 1);
+  const int64_t row = w >> 1;
+  if (row >= (int64_t)p.B * p.R) return;
+  const int b = (int)(row / p.R), r = (int)(row % p.R), g = r / kRows, i = r % kRows;
+  uint4* dst = reinterpret_cast<uint4*>(p.ctx + row * kDC + 256 * hf);
+  if (item_keys(p, b * p.groups + g) == 0) {
+    dst[lane] = make_uint4(0u, 0u, 0u, 0u);
+    if (hf == 0 && lane == 0 && p.lse != nullptr) p.lse[row] = -INFINITY;
+    return;
+  }
+  const int4 e = p.table[b * p.groups + g];
+  if (e.z == 1) return;
+  const int stride = min(p.R, kRows);
+  auto part = [&](int k) { return 2 * (int64_t)(k == 0 ? e.x : 2 * (e.y + k)) + hf; };
+  float M = -INFINITY;
+  for (int k = lane; k < e.z; k += 32) M = fmaxf(M, p.ws_ml[part(k) * kRows + i].x);
+  M = warp_max(M);
+  const float ref = M == -INFINITY ? 0.f : M;
+  float L = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  // lane l holds features 8 l .. 8 l + 7: chunks 2 l and 2 l + 1 of the rotated row
+#pragma unroll 4
+  for (int k = 0; k < e.z; ++k) {
+    const float2 ml = p.ws_ml[part(k) * kRows + i];
+    const float4* src = reinterpret_cast<const float4*>(p.ws_o + (part(k) * stride + i) * 256);
+    const float4 a = src[(2 * lane + i) & 63], c = src[(2 * lane + 1 + i) & 63];
+    if (ml.y == 0.f) continue;  // the row saw none of this piece's keys
+    const float f = exp2f(ml.x - ref);
+    L = fmaf(f, ml.y, L);
+    const float v[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = fmaf(f, v[j], o[j]);
+  }
+  const float inv = (L == 0.f ? 0.f : 1.f / L) * p.kv.latent_scale;
+  dst[lane] = make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv),
+                         pack_bf16x2(o[4] * inv, o[5] * inv), pack_bf16x2(o[6] * inv, o[7] * inv));
+  if (hf == 0 && lane == 0 && p.lse != nullptr) p.lse[row] = L == 0.f ? -INFINITY : M * kLn2 + logf(L);
+}
+
+int max_pairs() {
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms > 1 ? sms / 2 : 1;
+}
+// Pairs that this shape can keep busy at most
+int shape_pairs(int n_h, int B, int T, int n_max) {
+  const int64_t groups = ((int64_t)n_h * T + kRows - 1) / kRows, tiles = groups * B * ((n_max + kTile - 1) / kTile);
+  const int pairs = max_pairs();
+  return (int)(tiles < pairs ? tiles : pairs);
+}
+size_t table_bytes(int n_h, int B, int T) { return (size_t)B * (((size_t)n_h * T + kRows - 1) / kRows) * sizeof(int4); }
+size_t ml_bytes(int pairs) { return (size_t)pairs * 2 * 2 * kRows * sizeof(float2); }
+
+}  // namespace decode_fp4
+
+size_t decode_fp4_tc_workspace(int n_h, int B, int T, int n_max) {
+  using namespace decode_fp4;
+  const int pairs = shape_pairs(n_h, B, T, n_max), R = n_h * T;
+  return table_bytes(n_h, B, T) + ml_bytes(pairs) + (size_t)pairs * 2 * 2 * (R < kRows ? R : kRows) * 256 * sizeof(float);
+}
+
+cudaError_t decode_fp4_tc_launch(const Fp4DecodeArgs& a, void* ws, cudaStream_t st) {
+  using namespace decode_fp4;
+  Params p{};
+  p.kv = a.kv;
+  p.q_tilde = static_cast<const __nv_bfloat16*>(a.q_tilde);
+  p.q_pe = static_cast<const __nv_bfloat16*>(a.q_pe);
+  p.ldqt = a.ldqt; p.ldqp = a.ldqp;
+  p.lengths = a.lengths;
+  p.B = a.B; p.T = a.T; p.n_h = a.n_h; p.n_max = a.n_max;
+  p.R = a.T * a.n_h;
+  p.groups = (p.R + kRows - 1) / kRows;
+  p.pairs = shape_pairs(a.n_h, a.B, a.T, a.n_max);
+  p.scale_log2 = a.scale * kLog2e;
+  p.ctx = static_cast<__nv_bfloat16*>(a.ctx);
+  p.lse = a.lse;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  p.table = reinterpret_cast<int4*>(w);
+  w += table_bytes(a.n_h, a.B, a.T);
+  p.ws_ml = reinterpret_cast<float2*>(w);
+  w += ml_bytes(p.pairs);
+  p.ws_o = reinterpret_cast<float*>(w);
+  p.err = a.err;
+  cudaError_t e = cudaFuncSetAttribute(decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(decode_kernel, dim3(2 * p.pairs), dim3(kThreads), kSmemBytes, st, p);
+  if (e != cudaSuccess) return e;
+  const int64_t warps = (int64_t)p.B * p.R * 2;
+  return launch_pdl(join_kernel, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st, p);
+}
+
+}  // namespace mla

@@ -192,19 +192,18 @@ size_t decode_fp4_simt_workspace(int n_h, int d_c, int B, int n_max) {
   return s == 1 ? 256 : (size_t)s * B * n_h * (d_c * sizeof(float) + sizeof(float2)) + 256;
 }
 
-template <typename T>
 cudaError_t decode_fp4_simt_launch(const Fp4DecodeArgs& a, void* ws, cudaStream_t st) {
   const int q = a.B * a.T, splits = decode_fp4_simt_splits(q, a.n_max);
   float* ws_o = static_cast<float*>(ws);
   float2* ws_ml = reinterpret_cast<float2*>(ws_o + (size_t)splits * q * a.n_h * a.d_c);
   const dim3 grid((a.n_h + kWarps - 1) / kWarps, q, splits);
   if (a.d_c <= 512)
-    decode_fp4_simt<T, 1><<<grid, 32 * kWarps, 0, st>>>(a, splits, ws_o, ws_ml);
+    decode_fp4_simt<float, 1><<<grid, 32 * kWarps, 0, st>>>(a, splits, ws_o, ws_ml);
   else
-    decode_fp4_simt<T, 2><<<grid, 32 * kWarps, 0, st>>>(a, splits, ws_o, ws_ml);
+    decode_fp4_simt<float, 2><<<grid, 32 * kWarps, 0, st>>>(a, splits, ws_o, ws_ml);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || splits == 1) return e;
-  combine_fp4_simt<T><<<dim3(a.n_h, q), 128, 0, st>>>(a, splits, ws_o, ws_ml);
+  combine_fp4_simt<float><<<dim3(a.n_h, q), 128, 0, st>>>(a, splits, ws_o, ws_ml);
   return cudaGetLastError();
 }
 
@@ -218,7 +217,5 @@ cudaError_t weights_simt_launch(const WeightsArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template cudaError_t decode_fp4_simt_launch<float>(const Fp4DecodeArgs&, void*, cudaStream_t);
-template cudaError_t decode_fp4_simt_launch<__nv_bfloat16>(const Fp4DecodeArgs&, void*, cudaStream_t);
 
 }  // namespace mla

@@ -34,8 +34,9 @@ template <typename T>
 cudaError_t cache_read_fp4_launch(const ReadFp4Args& a, cudaStream_t st);
 int decode_fp4_simt_splits(int B, int n_max);
 size_t decode_fp4_simt_workspace(int n_h, int d_c, int B, int n_max);
-template <typename T>
-cudaError_t decode_fp4_simt_launch(const Fp4DecodeArgs& a, void* ws, cudaStream_t st);
+cudaError_t decode_fp4_simt_launch(const Fp4DecodeArgs& a, void* ws, cudaStream_t st);  // fp32
+size_t decode_fp4_tc_workspace(int n_h, int B, int T, int n_max);
+cudaError_t decode_fp4_tc_launch(const Fp4DecodeArgs& a, void* ws, cudaStream_t st);  // bf16
 
 // ---- attention weights and eviction ------------------------------------------------------------
 cudaError_t weights_simt_launch(const WeightsArgs& a, cudaStream_t st);  // fp32

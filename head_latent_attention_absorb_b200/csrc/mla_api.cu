@@ -623,7 +623,8 @@ mla_status mla_cache_read_fp4(mla_dims dims, mla_dtype dtype, int32_t B, int32_t
 
 size_t mla_decode_fp4kv_workspace_size(mla_dims dims, mla_dtype dtype, int32_t B, int32_t T, int32_t n_max) {
   if (check_cache_dims(dims, dtype, true) != MLA_OK || B <= 0 || T < 1 || n_max < T || (int64_t)B * T > 65535) return 0;
-  return mla::decode_fp4_simt_workspace(dims.n_h, dims.d_c, B * T, n_max);
+  return dtype == MLA_BF16 ? mla::decode_fp4_tc_workspace(dims.n_h, B, T, n_max)
+                           : mla::decode_fp4_simt_workspace(dims.n_h, dims.d_c, B * T, n_max);
 }
 
 mla_status mla_decode_absorb_fp4kv(mla_dims dims, mla_dtype dtype, int32_t B, int32_t T, const void* q_tilde,
@@ -651,8 +652,8 @@ mla_status mla_decode_absorb_fp4kv(mla_dims dims, mla_dtype dtype, int32_t B, in
   a.kv.latent_scale = latent_scale;
   a.ctx = ctx_out; a.lse = lse_out;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == MLA_BF16 ? mla::decode_fp4_simt_launch<__nv_bfloat16>(a, workspace, st)
-                                          : mla::decode_fp4_simt_launch<float>(a, workspace, st);
+  const cudaError_t e = dtype == MLA_BF16 ? mla::decode_fp4_tc_launch(a, workspace, st)
+                                          : mla::decode_fp4_simt_launch(a, workspace, st);
   return cuda_status(e, "mla_decode_absorb_fp4kv launch");
 }
 

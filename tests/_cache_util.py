@@ -34,6 +34,10 @@ def values(c4, sc, latent_scale=1.0):
 def reference(q, qp, c, kr, lengths, T, scale):
     """fp64 decode: ctx, lse, the mean |c| under the softmax weights and the bound on a score's error.
 
+    The mean holds 2^-21 of the plain sum of |c| besides: fp16 probabilities have no steps below 2^-24, so each is off
+    by up to 2^-25 beyond its relative rounding, while their sum is at least 2^7 (they are taken relative to 2^-7 of
+    the largest).  That is 2^-32 of the weights' sum per key, and the mean is weighed by at least 2^-11 below.
+
     Scores: products of at most 11-bit by 8-bit factors are exact in fp32, and a sum of 576 of them in any order, with
     truncating adds of 2^-23, is off by at most 576 * 2^-23 of the sum of magnitudes; the scale, the base-2
     exponent and its offset add a few 2^-24 of |z|."""
@@ -56,7 +60,8 @@ def reference(q, qp, c, kr, lengths, T, scale):
             p = np.exp(z - m)
             l = p.sum(-1, keepdims=True)
             p /= l
-            ctx[b, s], mean_abs[b, s] = p @ keys[:n, :c.shape[-1]], p @ np.abs(keys[:n, :c.shape[-1]])
+            ctx[b, s] = p @ keys[:n, :c.shape[-1]]
+            mean_abs[b, s] = (p + 2.0 ** -21) @ np.abs(keys[:n, :c.shape[-1]])
             lse[b, s] = (m + np.log(l))[:, 0]
             ez[b, s] = (mag * 576 * 2.0 ** -23 + np.abs(z) * 2.0 ** -21).max(-1)
     return ctx, lse, mean_abs, ez
