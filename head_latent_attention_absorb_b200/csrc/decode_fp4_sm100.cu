@@ -65,6 +65,7 @@ constexpr uint32_t kTmemCols = 512, kColO = 0, kColS = 256, kColQ = 320;
 // only when a score passes it by kRescale.  So they reach 2^15 at most (fp16 ends at 2^16), the sum is at
 // least 2^kRaise, and a probability that fp16's subnormals round (2^-25) is off by 2^-32 of the sum.
 constexpr float kRaise = 7.f, kRescale = 15.f;
+constexpr int kPrefetch = 4;                     // tiles that L2 is ahead of the decode warps
 constexpr int kPlanRegs = 8;                     // items per lane that the chunk search holds
 constexpr int kSwitchTiles = 5;                  // what a second piece costs a CTA, in tiles
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
@@ -118,11 +119,21 @@ struct Smem {
 constexpr int kSmemBytes = kSmemOff + (int)sizeof(Smem) + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory above 227 KB");
 
-__device__ __forceinline__ bool wait(Smem& sm, uint64_t& bar, uint32_t parity, int32_t* err) {
-  if (mbar_wait(smem_u32(&bar), parity, &sm.abort, kWaitLimitNs)) return true;
+__device__ __forceinline__ uint8_t* shared_base() {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+}
+
+// Bounded wait that records its own expiry; what follows a first failed try is one shared function, since the
+// roles' loops together have to fit the instruction cache.
+__device__ __noinline__ bool wait_more(Smem& sm, uint32_t bar, uint32_t parity, int32_t* err) {
+  if (mbar_wait(bar, parity, &sm.abort, kWaitLimitNs)) return true;
   raise_error(err, MLA_ERR_TIMEOUT);
   sm.abort = 1;
   return false;
+}
+__device__ __forceinline__ bool wait(Smem& sm, uint64_t& bar, uint32_t parity, int32_t* err) {
+  return mbar_try_wait(smem_u32(&bar), parity) || wait_more(sm, smem_u32(&bar), parity, err);
 }
 // All lanes wait; the warp goes on only if all of them saw the phase complete.
 __device__ __forceinline__ bool wait_warp(Smem& sm, uint64_t& bar, uint32_t parity, int32_t* err) {
@@ -260,21 +271,33 @@ __device__ void next_piece(const Params& p, int c, Plan& s, Piece* out) {
   *out = r;
 }
 
-// A decode warp's lane: 32 features of one 64-feature slab for four keys of a tile.
+// A decode warp's lane: 32 features of one 64-feature slab for four keys of a tile (lane / 2 + 16 i).
 struct Part {
   uint4 code[4];
   uint32_t scale[4];
 };
-__device__ __forceinline__ void load_part(const Params& p, int b, int tile, int len, int slab, int lane, Part& k) {
+struct PartSource {
+  const uint8_t* code;
+  const uint8_t* scale;
+  int64_t code16, scale16;  // 16 rows on
+};
+__device__ __forceinline__ PartSource part_source(const Params& p, int b, int tile, int slab, int lane) {
+  const int64_t t = (int64_t)tile * kTile + (lane >> 1);
+  return {p.kv.c4 + b * p.kv.c4_b + t * p.kv.c4_r + 32 * slab + 16 * (lane & 1),
+          p.kv.sc + b * p.kv.sc_b + t * p.kv.sc_r + 4 * slab + 2 * (lane & 1), 16 * p.kv.c4_r, 16 * p.kv.sc_r};
+}
+// Loads the source's tile and moves on to the next one; `left` keys from the lane's first one are in the sequence.
+__device__ __forceinline__ void load_part(PartSource& s, int left, Part& k) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int t = tile * kTile + 16 * i + (lane >> 1);
     k.code[i] = make_uint4(0u, 0u, 0u, 0u);
     k.scale[i] = 0u;
-    if (t < len) {  // rows behind the sequence may hold anything, or not exist
-      k.code[i] = __ldg(reinterpret_cast<const uint4*>(p.kv.c4 + b * p.kv.c4_b + t * p.kv.c4_r + 32 * slab) + (lane & 1));
-      k.scale[i] = __ldg(reinterpret_cast<const uint16_t*>(p.kv.sc + b * p.kv.sc_b + t * p.kv.sc_r + 4 * slab) + (lane & 1));
+    if (16 * i < left) {  // rows behind the sequence may hold anything, or not exist
+      k.code[i] = __ldg(reinterpret_cast<const uint4*>(s.code));
+      k.scale[i] = __ldg(reinterpret_cast<const uint16_t*>(s.scale));
     }
+    s.code += s.code16;
+    s.scale += s.scale16;
   }
 }
 __device__ __forceinline__ void store_part(const Part& k, uint32_t dst, int lane) {
@@ -337,11 +360,12 @@ __device__ __forceinline__ uint4 scale_to_f16(const uint4& v, float a, float b) 
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// The item's query rows: latent part as fp16 (slabs 0..5 into `stage`, 6 and 7 into the resident buffer),
+// The item's query rows: latent part as fp16 (the six slabs of TMEM into `stage`, two into the resident buffer),
 // rotary part as bf16, both times the row's power of two; rows past R as zeros.  Warp w of kQLoaders.
-__device__ __forceinline__ void load_query(const Params& p, Smem& sm, uint32_t stage, uint32_t resident, int b, int g,
-                                           int w, int lane) {
+__device__ __noinline__ void load_query(const Params& p, Smem& sm, uint32_t stage, uint32_t resident, int b, int g,
+                                           int hf, int w, int lane) {
   constexpr int kBatch = 4;
+#pragma unroll 1
   for (int r0 = w; r0 < kRows; r0 += kQLoaders * kBatch) {
     uint4 lat[kBatch][2], rope[kBatch];
 #pragma unroll
@@ -367,7 +391,7 @@ __device__ __forceinline__ void load_query(const Params& p, Smem& sm, uint32_t s
       const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int slab = (lane + 32 * h) >> 3, pos = lane & 7;
+        const int slab = ((lane + 32 * h) >> 3) ^ (4 * hf), pos = lane & 7;  // counted from the own half
         const uint4 v = scale_to_f16(lat[k][h], p.kv.latent_scale, mul);
         const uint32_t base = slab < kQTmemSlabs ? stage + slab * kQSlabBytes : resident + (slab - kQTmemSlabs) * kQSlabBytes;
         st_shared_v4_b32(base + r * 128 + ((pos ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
@@ -385,52 +409,308 @@ __device__ __forceinline__ void load_query(const Params& p, Smem& sm, uint32_t s
   fence_proxy_async_smem();
 }
 
-// One K-major 64-feature slab of the scores: query slab F (8: the rotary part) against the keys at `keys`.
-template <int F>
-__device__ __forceinline__ void slab_scores(uint32_t base, uint32_t tmem, uint32_t keys, bool first) {
-  constexpr uint32_t idesc = F < 8 ? idesc_f16_f32(kRows, kTile, 0, 0) : idesc_bf16_f32(kRows, kTile, 0, 0);
+// Softmax warps: the staged query slabs into TMEM, one row per thread.
+__device__ __noinline__ void query_to_tmem(uint32_t base, uint32_t tmem) {
+  const int r = threadIdx.x;
+#pragma unroll 2
+  for (int j = 0; j < kQTmemSlabs; ++j) {
+    uint32_t v[32];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint64_t bd = smem_desc(keys + 32 * k, 16, 1024, kSwizzle128);
-    const uint32_t add = first && k == 0 ? 0u : 1u;
-    if constexpr (F < kQTmemSlabs)
-      mma_ts(tmem + kColS, tmem + kColQ + 32 * F + 8 * k, bd, idesc, add);
-    else
-      mma_ss(tmem + kColS, smem_desc(base + kQOff + (F - kQTmemSlabs) * kQSlabBytes + 32 * k, 16, 1024, kSwizzle128), bd,
-             idesc, add);
+    for (int c = 0; c < 8; ++c) {
+      const uint4 u = ld_shared_v4_b32(base + j * kQSlabBytes + r * 128 + ((c ^ (r & 7)) << 4));
+      v[4 * c] = u.x;
+      v[4 * c + 1] = u.y;
+      v[4 * c + 2] = u.z;
+      v[4 * c + 3] = u.w;
+    }
+    tmem_st32(tmem + ((uint32_t)(r & 96) << 16) + kColQ + 32 * j, v);
+  }
+  tmem_st_wait();
+  tc_fence_before();
+}
+
+// What a role needs to know of the piece at hand.  The roles are functions of their own so that each has the
+// registers to itself: inlined together they spill.
+struct Work {
+  uint32_t base, tmem;   // shared memory, TMEM
+  uint32_t it0, n;       // tiles of the earlier pieces, tiles of this one
+  int begin, b, g, len, hf;
+  int slot, c0, pieces;  // as in Piece
+};
+
+// A 128-byte-swizzled shared-memory descriptor whose address is at + 32 k: the low word counts 16 bytes.
+__device__ __forceinline__ uint64_t step_desc(uint32_t at, int k, uint32_t lbo_bytes = 16) {
+  constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (kSwizzle128 << 29);
+  return ((uint64_t)hi << 32) | ((lbo_bytes >> 4) << 16 | ((at >> 4) + 2 * k));
+}
+
+// One 64-feature slab of the scores, the query slab in TMEM columns q or in shared memory at q.
+__device__ __forceinline__ void slab_ts(uint32_t s, uint32_t q, uint32_t keys, bool first) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    mma_ts(s, q + 8 * k, step_desc(keys, k), idesc_f16_f32(kRows, kTile, 0, 0), first && k == 0 ? 0u : 1u);
+}
+__device__ __forceinline__ void slab_ss(uint32_t s, uint32_t q, uint32_t keys, uint32_t idesc) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) mma_ss(s, step_desc(q, k), step_desc(keys, k), idesc, 1u);
+}
+
+// One warp: the MMAs of a piece, issued by one thread: S(t), then O(t - 1).  Query slabs are counted from the
+// CTA's own half: 0..3 its half, 4..7 the other one; 0..5 are in TMEM.
+__device__ __noinline__ bool mma_role(const Params& p, uint32_t it0, uint32_t n) {
+  uint8_t* smem = shared_base();
+  Smem& sm = *reinterpret_cast<Smem*>(smem + kSmemOff);
+  const uint32_t base = smem_u32(smem), tmem = sm.tmem_base, tS = tmem + kColS, tQ = tmem + kColQ;
+  bool ok = true;
+  if (elect_one()) {
+#pragma unroll 1
+    for (uint32_t t = 0; t <= n; ++t) {
+      if (t < n) {
+        const uint32_t it = it0 + t, st = it % kKvStages, kv = base + st * kKvBytes;
+        ok = wait(sm, sm.s_empty, (it & 1u) ^ 1u, p.err) && wait(sm, sm.kv_full[st], (it / kKvStages) & 1u, p.err);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) slab_ts(tS, tQ + 32 * j, kv + j * kSlabBytes, j == 0);
+        uint32_t k = kKPerTile * it;
+#pragma unroll 1
+        for (int j = 0; j < kKPerTile; ++j, ++k) {
+          const uint32_t slot = k % kKSlots, keys = base + kKOff + slot * kSlabBytes;
+          ok = wait(sm, sm.k_full[slot], (k / kKSlots) & 1u, p.err);
+          if (!ok) break;
+          tc_fence_after();
+          if (j == 0)
+            slab_ss(tS, base + kQOff + 2 * kQSlabBytes, keys, idesc_bf16_f32(kRows, kTile, 0, 0));
+          else if (j < 3)
+            slab_ts(tS, tQ + 96 + 32 * j, keys, false);
+          else
+            slab_ss(tS, base + kQOff + (j - 3) * kQSlabBytes, keys, idesc_f16_f32(kRows, kTile, 0, 0));
+          mma_commit(smem_u32(&sm.k_empty[slot]));
+        }
+        if (!ok) break;
+        mma_commit(smem_u32(&sm.s_full));
+      }
+      if (t > 0) {
+        const uint32_t it = it0 + t - 1, st = it % kKvStages, kv = base + st * kKvBytes;
+        ok = wait(sm, sm.p_full, it & 1u, p.err);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_ss(tmem + kColO, step_desc(base + kPOff, k), step_desc(kv + 2048 * k, 0, kSlabBytes),
+                 idesc_f16_f32(kRows, 256, 0, 1), t > 1 || k > 0 ? 1u : 0u);
+        mma_commit(smem_u32(&sm.kv_empty[st]));
+        mma_commit(smem_u32(&sm.pv_done));
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+// Four warps, one query row per thread: probabilities, and the piece's result.
+__device__ __noinline__ bool softmax_role(const Params& p, Smem& sm, Work w) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = threadIdx.x;
+  const uint32_t base = w.base, n = w.n, it0 = w.it0;
+  const int b = w.b, g = w.g, len = w.len, hf = w.hf, rows = min(p.R - kRows * g, kRows);
+  const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+  const uint32_t tS = w.tmem + lanes + kColS, tO = w.tmem + lanes + kColO;
+  const uint32_t p_row = base + kPOff + r * 128;
+  const float sl = sm.row_scale[r];
+  // keys that the row, and the group's first row, see
+  const int limit = len - p.T + (kRows * g + min(r, rows - 1)) / p.n_h + 1;
+  const int all_see = len - p.T + (kRows * g) / p.n_h + 1;
+  float ref = -INFINITY, l = 0.f;
+  bool ok = true;
+#pragma unroll 1
+  for (uint32_t t = 0; t < n && ok; ++t) {
+    const uint32_t it = it0 + t;
+    const int k0 = (w.begin + (int)t) * kTile;
+    ok = wait_warp(sm, sm.s_full, it & 1u, p.err);
+    if (!ok) break;
+    tc_fence_after();
+    uint32_t s[2][32];
+    tmem_ld32(tS, s[0]);
+    tmem_ld32(tS + 32, s[1]);
+    tmem_ld_wait();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sm.s_empty));
+    if (k0 + kTile > all_see) {
+#pragma unroll
+      for (int i = 0; i < 64; ++i)
+        if (k0 + i >= limit) s[i >> 5][i & 31] = 0xff800000u;  // -inf
+    }
+    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i >> 5][i & 31]));
+    const float z = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
+    float f = 1.f;
+    const bool raise = z > ref + kRescale;  // ref = -inf: any finite maximum
+    if (raise) {
+      f = ex2f_approx(ref - (z - kRaise));
+      l *= f;
+      ref = z - kRaise;
+    }
+    const float neg = ref == -INFINITY ? 0.f : -ref;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    auto half = [&](int k) {  // probabilities of 32 keys, as fp16 pairs in the first 16 words
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const float a = ex2f_approx(fmaf(__uint_as_float(s[k][i]), sl, neg));
+        const float c = ex2f_approx(fmaf(__uint_as_float(s[k][i + 1]), sl, neg));
+        sum[i & 2] += a;
+        sum[(i & 2) + 1] += c;
+        s[k][i / 2] = pack_f16x2_ieee(a, c);
+      }
+    };
+    auto store = [&](int k) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        st_shared_v4_b32(p_row + (((4 * k + c) ^ (r & 7)) << 4), s[k][4 * c], s[k][4 * c + 1], s[k][4 * c + 2],
+                         s[k][4 * c + 3]);
+    };
+    half(0);
+    if (t > 0) {  // the last tile's probabilities are used up, its context complete
+      ok = wait_warp(sm, sm.pv_done, (it - 1) & 1u, p.err);
+      if (!ok) break;
+      if (__any_sync(0xffffffffu, raise)) {
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < 256; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(tO + c, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+          tmem_st32(tO + c, o);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+      }
+    }
+    store(0);
+    half(1);
+    store(1);
+    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sm.p_full));
+  }
+  if (ok) ok = wait_warp(sm, sm.pv_done, (it0 + n - 1) & 1u, p.err);
+  if (ok) {
+    // -------------------------------------------------------------- the piece's result
+    // through the idle key buffers, 16-byte chunks rotated by the row so that neither the row-wise
+    // writes nor the copies out conflict
+    tc_fence_after();
+    const uint32_t out_row = (uint32_t)b * p.R + kRows * g;  // first query row of the group
+    if (w.pieces == 1) {
+      const float inv = (l == 0.f ? 0.f : 1.f / l) * p.kv.latent_scale;
+      const uint32_t dst = base + r * 512;
+#pragma unroll 1
+      for (int c = 0; c < 256; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(tO + c, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[e] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
+          st_shared_v4_b32(dst + (((c / 8 + i + r) & 31) << 4), v[0], v[1], v[2], v[3]);
+        }
+      }
+      __syncwarp();
+      for (int k = 32 * warp; k < min(32 * warp + 32, rows); ++k) {
+        const uint4 v = ld_shared_v4_b32(base + k * 512 + (((lane + k) & 31) << 4));
+        reinterpret_cast<uint4*>(p.ctx + (int64_t)(out_row + k) * kDC + 256 * hf)[lane] = v;
+      }
+      if (hf == 0 && r < rows && p.lse != nullptr)
+        p.lse[out_row + r] = l == 0.f ? -INFINITY : ref * kLn2 + logf(l);
+    } else {
+      const uint32_t dst = base + r * 1024;
+#pragma unroll 1
+      for (int c = 0; c < 256; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(tO + c, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          st_shared_v4_b32(dst + (((c / 4 + i + r) & 63) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      const int64_t part = 2 * (int64_t)w.slot + hf;
+      const int mine = min(32, rows - 32 * warp);
+      if (lane == 0 && mine > 0) {
+        bulk_store_s2g(p.ws_o + (part * min(p.R, kRows) + 32 * warp) * 256, base + 32 * warp * 1024, mine * 1024);
+        bulk_group_commit();
+        bulk_group_wait_all();
+      }
+      if (r < rows) p.ws_ml[part * kRows + r] = make_float2(ref, l);
+    }
+    if (threadIdx.x == 0 && hf == 0 && w.begin == 0) p.table[w.b * p.groups + w.g] = make_int4(w.slot, w.c0, w.pieces, 0);
+    tc_fence_before();
+  }
+  return ok;
+}
+
+// One warp: its latent slab of every tile, loaded one tile ahead (from L2: the rotary warp prefetches).
+__device__ __noinline__ bool latent_role(const Params& p, Smem& sm, Work w) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool own = warp < kKWarp0;  // a slab of this CTA's half
+  const int j = own ? warp - kKvWarp0 : warp - kKWarp0;
+  PartSource src = part_source(p, w.b, w.begin, 4 * (own ? w.hf : 1 - w.hf) + j, lane);
+  int left = w.len - w.begin * kTile - (lane >> 1);
+  Part k;
+  load_part(src, left, k);
+#pragma unroll 1
+  for (uint32_t t = 0; t < w.n; ++t) {
+    const uint32_t it = w.it0 + t, q = kKPerTile * it + 1 + j;
+    const uint32_t slot = own ? it % kKvStages : q % kKSlots, use = own ? it / kKvStages : q / kKSlots;
+    if (!wait_warp(sm, own ? sm.kv_empty[slot] : sm.k_empty[slot], (use & 1u) ^ 1u, p.err)) return false;
+    store_part(k, w.base + (own ? slot * kKvBytes + j * kSlabBytes : kKOff + slot * kSlabBytes), lane);
+    if (lane == 0) mbar_arrive(smem_u32(own ? &sm.kv_full[slot] : &sm.k_full[slot]));
+    left -= kTile;
+    load_part(src, left, k);
+  }
+  return true;
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* a) { asm volatile("prefetch.global.L2 [%0];" ::"l"(a)); }
+// One warp: the cached rows of a tile into L2.
+__device__ __forceinline__ void prefetch_tile(const Params& p, int b, int tile, int len, int lane) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t t = (int64_t)tile * kTile + 32 * i + lane;
+    if (t >= len) return;
+    const uint8_t* c = p.kv.c4 + b * p.kv.c4_b + t * p.kv.c4_r;
+    prefetch_l2(c);
+    prefetch_l2(c + 128);
+    prefetch_l2(p.kv.sc + b * p.kv.sc_b + t * p.kv.sc_r);
+    prefetch_l2(static_cast<const __nv_bfloat16*>(p.kv.k_r) + b * p.kv.kr_b + t * p.kv.kr_r);
   }
 }
 
-// The score MMAs of tile `it` for the CTA of half H: its own half's slabs, the rotary one, the other half's.
-template <int H>
-__device__ __forceinline__ bool issue_scores(Smem& sm, uint32_t base, uint32_t tmem, uint32_t it, int32_t* err) {
-  if (!wait(sm, sm.s_empty, (it & 1u) ^ 1u, err)) return false;
-  const uint32_t st = it % kKvStages, kv = base + st * kKvBytes;
-  if (!wait(sm, sm.kv_full[st], (it / kKvStages) & 1u, err)) return false;
-  tc_fence_after();
-  slab_scores<4 * H>(base, tmem, kv, true);
-  slab_scores<4 * H + 1>(base, tmem, kv + kSlabBytes, false);
-  slab_scores<4 * H + 2>(base, tmem, kv + 2 * kSlabBytes, false);
-  slab_scores<4 * H + 3>(base, tmem, kv + 3 * kSlabBytes, false);
-#pragma unroll
-  for (int j = 0; j < kKPerTile; ++j) {
-    const uint32_t k = kKPerTile * it + j, slot = k % kKSlots, keys = base + kKOff + slot * kSlabBytes;
-    if (!wait(sm, sm.k_full[slot], (k / kKSlots) & 1u, err)) return false;
-    tc_fence_after();
-    if (j == 0) slab_scores<8>(base, tmem, keys, false);
-    if (j == 1) slab_scores<4 - 4 * H>(base, tmem, keys, false);
-    if (j == 2) slab_scores<5 - 4 * H>(base, tmem, keys, false);
-    if (j == 3) slab_scores<6 - 4 * H>(base, tmem, keys, false);
-    if (j == 4) slab_scores<7 - 4 * H>(base, tmem, keys, false);
-    mma_commit(smem_u32(&sm.k_empty[slot]));
+// One warp: the rotary slab of every tile, and the tiles' way into L2.
+__device__ __noinline__ bool rope_role(const Params& p, Smem& sm, Work w) {
+  const int lane = threadIdx.x & 31;
+  uint4 k[16];
+  load_rope(p, w.b, w.begin, w.len, lane, k);
+#pragma unroll 1
+  for (uint32_t t = 0; t < w.n; ++t) {
+    const uint32_t q = kKPerTile * (w.it0 + t), slot = q % kKSlots;
+    if (!wait_warp(sm, sm.k_empty[slot], ((q / kKSlots) & 1u) ^ 1u, p.err)) return false;
+    store_rope(k, w.base + kKOff + slot * kSlabBytes, lane);
+    if (lane == 0) mbar_arrive(smem_u32(&sm.k_full[slot]));
+    load_rope(p, w.b, w.begin + t + 1, w.len, lane, k);
+    if (t + kPrefetch < w.n) prefetch_tile(p, w.b, w.begin + t + kPrefetch, w.len, lane);
   }
-  mma_commit(smem_u32(&sm.s_full));
   return true;
 }
 
 __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ Params p) {
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem = shared_base();
   Smem& sm = *reinterpret_cast<Smem*>(smem + kSmemOff);
   const uint32_t base = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -473,251 +753,41 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
   uint32_t it0 = 0;
   bool dead = false;
   while (true) {
-    const Piece pc = sm.piece;
-    if (pc.item < 0) break;
-    const int b = pc.item / p.groups, g = pc.item % p.groups, len = p.lengths[b];
-    const int rows = min(p.R - kRows * g, kRows);
-    const uint32_t n = (uint32_t)(pc.end - pc.begin);
-    const bool whole = pc.n == 1;
-
-    // ------------------------------------------------------------------ query into TMEM and shared memory
-    if (warp < kQLoaders + 1 && warp != kMmaWarp)
-      load_query(p, sm, base, base + kQOff, b, g, warp < kMmaWarp ? warp : warp - 1, lane);
+    if (sm.piece.item < 0) break;
+    Work w;
+    w.base = base;
+    w.tmem = tmem;
+    w.it0 = it0;
+    w.begin = sm.piece.begin;
+    w.n = (uint32_t)(sm.piece.end - w.begin);
+    w.b = sm.piece.item / p.groups;
+    w.g = sm.piece.item % p.groups;
+    w.len = p.lengths[w.b];
+    w.hf = hf;
+    w.slot = sm.piece.slot;
+    w.c0 = sm.piece.c0;
+    w.pieces = sm.piece.n;
+    if (warp == kRopeWarp)
+      for (int t = 0; t < kPrefetch && t < (int)w.n; ++t) prefetch_tile(p, w.b, w.begin + t, w.len, lane);
+    if (warp <= kQLoaders && warp != kMmaWarp)
+      load_query(p, sm, base, base + kQOff, w.b, w.g, hf, warp < kMmaWarp ? warp : warp - 1, lane);
     __syncthreads();
-    if (warp < 4) {
-      const int r = threadIdx.x;
-#pragma unroll
-      for (int j = 0; j < kQTmemSlabs; ++j) {
-        uint32_t v[32];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint4 u = ld_shared_v4_b32(base + j * kQSlabBytes + r * 128 + ((c ^ (r & 7)) << 4));
-          v[4 * c] = u.x;
-          v[4 * c + 1] = u.y;
-          v[4 * c + 2] = u.z;
-          v[4 * c + 3] = u.w;
-        }
-        tmem_st32(tmem + ((uint32_t)(32 * warp) << 16) + kColQ + 32 * j, v);
-      }
-      tmem_st_wait();
-      tc_fence_before();
-    }
+    if (warp < 4) query_to_tmem(base, tmem);
     __syncthreads();
     tc_fence_after();
-
-    if (warp == kMmaWarp) {
-      // ---------------------------------------------------------------- MMAs
-      if (lane == 0 && !dead) {
-        const uint32_t id_o = idesc_f16_f32(kRows, 256, 0, 1), tO = tmem + kColO;
-        auto scores = [&](uint32_t it) {
-          return hf == 0 ? issue_scores<0>(sm, base, tmem, it, p.err) : issue_scores<1>(sm, base, tmem, it, p.err);
-        };
-        auto values = [&](uint32_t it, bool first) {
-          if (!wait(sm, sm.p_full, it & 1u, p.err)) return false;
-          tc_fence_after();
-          const uint32_t st = it % kKvStages;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_ss(tO, smem_desc(base + kPOff + 32 * k, 16, 1024, kSwizzle128),
-                   smem_desc(base + st * kKvBytes + 2048 * k, kSlabBytes, 1024, kSwizzle128), id_o,
-                   !first || k > 0 ? 1u : 0u);
-          mma_commit(smem_u32(&sm.kv_empty[st]));
-          mma_commit(smem_u32(&sm.pv_done));
-          return true;
-        };
-        bool ok = scores(it0);
-        for (uint32_t t = 0; t < n && ok; ++t) {
-          if (t + 1 < n) ok = scores(it0 + t + 1);
-          ok = ok && values(it0 + t, t == 0);
-        }
-        dead = !ok;
-      }
-      __syncwarp();
-    } else if (warp < 4) {
-      // ---------------------------------------------------------------- softmax, one query row per thread
-      const int r = threadIdx.x;
-      const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-      const uint32_t tS = tmem + lanes + kColS, tO = tmem + lanes + kColO;
-      const uint32_t p_row = base + kPOff + r * 128;
-      const float sl = sm.row_scale[r];
-      // keys that the row, and the group's first row, see
-      const int limit = len - p.T + (kRows * g + min(r, rows - 1)) / p.n_h + 1;
-      const int all_see = len - p.T + (kRows * g) / p.n_h + 1;
-      float ref = -INFINITY, l = 0.f;
-      for (uint32_t t = 0; t < n && !dead; ++t) {
-        const uint32_t it = it0 + t;
-        const int k0 = (pc.begin + (int)t) * kTile;
-        dead = !wait_warp(sm, sm.s_full, it & 1u, p.err);
-        if (dead) break;
-        tc_fence_after();
-        float s[64];
-        {
-          uint32_t v[32];
-          tmem_ld32(tS, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(v[i]);
-          tmem_ld32(tS + 32, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) s[32 + i] = __uint_as_float(v[i]);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.s_empty));
-        if (k0 + kTile > all_see) {
-#pragma unroll
-          for (int i = 0; i < 64; ++i) s[i] = k0 + i < limit ? s[i] : -INFINITY;
-        }
-        float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-        for (int i = 4; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
-        const float z = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
-        float f = 1.f;
-        const bool raise = z > ref + kRescale;  // ref = -inf: any finite maximum
-        if (raise) {
-          f = ex2f_approx(ref - (z - kRaise));
-          l *= f;
-          ref = z - kRaise;
-        }
-        const float neg = ref == -INFINITY ? 0.f : -ref;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t h[32];
-#pragma unroll
-        for (int i = 0; i < 64; i += 2) {
-          const float a = ex2f_approx(fmaf(s[i], sl, neg)), c = ex2f_approx(fmaf(s[i + 1], sl, neg));
-          sum[i & 2] += a;
-          sum[(i & 2) + 1] += c;
-          h[i / 2] = pack_f16x2_ieee(a, c);
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        if (t > 0) {  // the last tile's probabilities are used up, its context complete
-          dead = !wait_warp(sm, sm.pv_done, (it - 1) & 1u, p.err);
-          if (dead) break;
-          if (__any_sync(0xffffffffu, raise)) {
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < 256; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(tO + c, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st32(tO + c, o);
-            }
-            tmem_st_wait();
-            tc_fence_before();
-          }
-        }
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          st_shared_v4_b32(p_row + ((c ^ (r & 7)) << 4), h[4 * c], h[4 * c + 1], h[4 * c + 2], h[4 * c + 3]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.p_full));
-      }
-      if (!dead) dead = !wait_warp(sm, sm.pv_done, (it0 + n - 1) & 1u, p.err);
-      if (!dead) {
-        // -------------------------------------------------------------- the piece's result
-        // through the idle key buffers, 16-byte chunks rotated by the row so that neither the row-wise
-        // writes nor the copies out conflict
-        tc_fence_after();
-        const uint32_t out_row = (uint32_t)b * p.R + kRows * g;  // first query row of the group
-        if (whole) {
-          const float inv = (l == 0.f ? 0.f : 1.f / l) * p.kv.latent_scale;
-          const uint32_t dst = base + r * 512;
-#pragma unroll 1
-          for (int c = 0; c < 256; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(tO + c, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t v[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                v[e] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
-              st_shared_v4_b32(dst + (((c / 8 + i + r) & 31) << 4), v[0], v[1], v[2], v[3]);
-            }
-          }
-          __syncwarp();
-          for (int k = 32 * warp; k < min(32 * warp + 32, rows); ++k) {
-            const uint4 v = ld_shared_v4_b32(base + k * 512 + (((lane + k) & 31) << 4));
-            reinterpret_cast<uint4*>(p.ctx + (int64_t)(out_row + k) * kDC + 256 * hf)[lane] = v;
-          }
-          if (hf == 0 && r < rows && p.lse != nullptr)
-            p.lse[out_row + r] = l == 0.f ? -INFINITY : ref * kLn2 + logf(l);
-        } else {
-          const uint32_t dst = base + r * 1024;
-#pragma unroll 1
-          for (int c = 0; c < 256; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(tO + c, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              st_shared_v4_b32(dst + (((c / 4 + i + r) & 63) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          const int64_t part = 2 * (int64_t)pc.slot + hf;
-          const int mine = min(32, rows - 32 * warp);
-          if (lane == 0 && mine > 0) {
-            bulk_store_s2g(p.ws_o + (part * min(p.R, kRows) + 32 * warp) * 256, base + 32 * warp * 1024, mine * 1024);
-            bulk_group_commit();
-            bulk_group_wait_all();
-          }
-          if (r < rows) p.ws_ml[part * kRows + r] = make_float2(ref, l);
-        }
-        if (threadIdx.x == 0 && hf == 0 && pc.begin == 0) p.table[pc.item] = make_int4(pc.slot, pc.c0, pc.n, 0);
-        tc_fence_before();
-      }
-      __syncwarp();
-      if (threadIdx.x == 0) next_piece(p, pair, sm.plan, &sm.piece);
-      __syncwarp();
-    } else if (warp < kRopeWarp) {
-      // ---------------------------------------------------------------- latent slabs
-      const bool own = warp < kKWarp0;  // a slab of this CTA's half
-      const int j = own ? warp - kKvWarp0 : warp - kKWarp0;
-      const int slab = 4 * (own ? hf : 1 - hf) + j;
-      Part k0, k1;
-      load_part(p, b, pc.begin, len, slab, lane, k0);
-      load_part(p, b, pc.begin + 1, len, slab, lane, k1);
-      for (uint32_t t = 0; t < n && !dead; ++t) {
-        const uint32_t it = it0 + t;
-        const Part cur = k0;
-        k0 = k1;
-        if (t + 2 < n) load_part(p, b, pc.begin + t + 2, len, slab, lane, k1);
-        if (own) {
-          const uint32_t st = it % kKvStages;
-          dead = !wait_warp(sm, sm.kv_empty[st], ((it / kKvStages) & 1u) ^ 1u, p.err);
-          if (dead) break;
-          store_part(cur, base + st * kKvBytes + j * kSlabBytes, lane);
-          if (lane == 0) mbar_arrive(smem_u32(&sm.kv_full[st]));
-        } else {
-          const uint32_t q = kKPerTile * it + 1 + j, slot = q % kKSlots;
-          dead = !wait_warp(sm, sm.k_empty[slot], ((q / kKSlots) & 1u) ^ 1u, p.err);
-          if (dead) break;
-          store_part(cur, base + kKOff + slot * kSlabBytes, lane);
-          if (lane == 0) mbar_arrive(smem_u32(&sm.k_full[slot]));
-        }
-      }
-      __syncwarp();
-    } else {
-      // ---------------------------------------------------------------- rotary slab
-      uint4 k[16];
-      load_rope(p, b, pc.begin, len, lane, k);
-      for (uint32_t t = 0; t < n && !dead; ++t) {
-        const uint32_t q = kKPerTile * (it0 + t), slot = q % kKSlots;
-        dead = !wait_warp(sm, sm.k_empty[slot], ((q / kKSlots) & 1u) ^ 1u, p.err);
-        if (dead) break;
-        store_rope(k, base + kKOff + slot * kSlabBytes, lane);
-        if (lane == 0) mbar_arrive(smem_u32(&sm.k_full[slot]));
-        if (t + 1 < n) load_rope(p, b, pc.begin + t + 1, len, lane, k);
-      }
-      __syncwarp();
+    if (!dead) {
+      bool ok = true;
+      if (warp < 4)
+        ok = softmax_role(p, sm, w);
+      else if (warp > kMmaWarp)
+        ok = warp < kRopeWarp ? latent_role(p, sm, w) : rope_role(p, sm, w);
+      else
+        ok = mma_role(p, it0, w.n);
+      dead = !ok;
     }
-    it0 += n;
+    __syncwarp();
+    it0 += w.n;
+    if (threadIdx.x == 0) next_piece(p, pair, sm.plan, &sm.piece);
     __syncthreads();
     tc_fence_after();
     if (sm.abort) dead = true;
@@ -751,8 +821,10 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Param
     if (hf == 0 && lane == 0 && p.lse != nullptr) p.lse[row] = -INFINITY;
     return;
   }
-  const int4 e = p.table[b * p.groups + g];
+  int4 e = p.table[b * p.groups + g];
   if (e.z == 1) return;
+  // a decode that gave up may have left no entry
+  if ((unsigned)e.x >= 2u * p.pairs || e.y < 0 || e.z < 0 || e.z > p.pairs || e.y > p.pairs - e.z) e.z = 0;
   const int stride = min(p.R, kRows);
   auto part = [&](int k) { return 2 * (int64_t)(k == 0 ? e.x : 2 * (e.y + k)) + hf; };
   float M = -INFINITY;

@@ -126,6 +126,15 @@ __device__ __forceinline__ float4 ld_shared_v4(uint32_t addr) {
   return v;
 }
 
+// True in one lane of the converged warp.  A block under this condition is known to run in a single thread,
+// so the compiler keeps descriptors in uniform registers; under `lane == 0` it moves every operand over one
+// by one, and an issuing thread then needs about 100 cycles per MMA (measured, N = 64; 42 with this).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // ------------------------------------------------------------------------------------------
 // mbarrier
 // ------------------------------------------------------------------------------------------

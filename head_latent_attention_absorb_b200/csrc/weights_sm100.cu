@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kFp4 ? kThreadsFp4 : kThreadsBf16, 1) weights_
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- S^T = K Q^T
-    if (lane == 0) {
+    if (elect_one()) {
       uint32_t n = 0, tile = 0, pass = 0;
       for_each_pass(p, sm, [&](int, int, int g, int t0, int t1) {
         const int cols = (min(R - kRows * g, kRows) + 31) & ~31;  // zero rows pad to the readers' 32 columns
