@@ -37,13 +37,14 @@
 #include "fp4.cuh"
 #include "kernels.h"
 #include "sm100_ptx.cuh"
+#include "tma_host.h"
 
 namespace mla {
 namespace decode_fp4 {
 
 using namespace sm100;
 
-constexpr int kDC = 512;
+constexpr int kDC = 512, kDR = 64;
 constexpr int kTile = 64;                        // keys per tile
 constexpr int kRows = 128;                       // query rows per group: the rows of every MMA
 constexpr int kSlabBytes = kTile * 128;          // 64 keys of 64 features
@@ -58,24 +59,23 @@ constexpr int kSmemOff = kPOff + kRows * 128;
 static_assert(kQTmemSlabs * kQSlabBytes <= kQOff, "the query is staged in the key buffers");
 static_assert(kRows * 256 * 4 <= kQOff, "the partial context is staged in the key buffers");
 constexpr int kMmaWarp = 4, kKvWarp0 = 5, kKWarp0 = 9, kRopeWarp = 13;
-constexpr int kThreads = 32 * 14;
-constexpr int kQLoaders = 12;                    // softmax and latent decode warps load the query
+constexpr int kPrefetchWarp = 14;
+constexpr int kThreads = 32 * 15;
 constexpr uint32_t kTmemCols = 512, kColO = 0, kColS = 256, kColQ = 320;
 // Probabilities are 2^(z - ref): ref is set kRaise below the largest score so far (log2 units) and moved up
 // only when a score passes it by kRescale.  So they reach 2^15 at most (fp16 ends at 2^16), the sum is at
 // least 2^kRaise, and a probability that fp16's subnormals round (2^-25) is off by 2^-32 of the sum.
 constexpr float kRaise = 7.f, kRescale = 15.f;
 constexpr int kPrefetch = 4;                     // tiles that L2 is ahead of the decode warps
-constexpr int kPlanRegs = 8;                     // items per lane that the chunk search holds
+constexpr int kPlanRegs = 3;                     // items per lane that the chunk search holds (more than the pairs)
 constexpr int kSwitchTiles = 5;                  // what a second piece costs a CTA, in tiles
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct Params {
+  CUtensorMap tm_q;   // (d_c, R, B) query rows, box (64, 128, 1), 128-byte swizzle: rows past R read as zeros
+  CUtensorMap tm_qp;  // (d_r, R, B), same box
   CacheView kv;
-  const __nv_bfloat16* q_tilde;
-  const __nv_bfloat16* q_pe;
-  int64_t ldqt, ldqp;
   const int32_t* lengths;
   int B, T, n_h, n_max, R, groups, pairs;
   float scale_log2;
@@ -109,12 +109,13 @@ struct Piece {
 
 struct Smem {
   uint64_t kv_full[kKvStages], kv_empty[kKvStages], k_full[kKSlots], k_empty[kKSlots];
-  uint64_t s_full, s_empty, p_full, pv_done, drain;
+  uint64_t q_full, s_full, s_empty, p_full, pv_done, drain;
   alignas(16) float row_scale[kRows];  // softmax scale of a query row, log2 units
   Plan plan;
   Piece piece;
+  float row_max[2][kRows];  // largest element of a query row, each half of its slabs
   uint32_t tmem_base;
-  int abort, never;
+  int abort, never, progress;
 };
 constexpr int kSmemBytes = kSmemOff + (int)sizeof(Smem) + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory above 227 KB");
@@ -140,21 +141,25 @@ __device__ __forceinline__ bool wait_warp(Smem& sm, uint64_t& bar, uint32_t pari
   return __all_sync(0xffffffffu, wait(sm, bar, parity, err));
 }
 
-__device__ __forceinline__ int warp_sum_int(int v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+// total c / nc, in 32 bits where they hold the product.
+__device__ __forceinline__ long long share(long long total, int c, int nc) {
+  return total < (1 << 22) ? (long long)((uint32_t)total * (uint32_t)c / (uint32_t)nc) : total * c / nc;
 }
-__device__ __forceinline__ int warp_max_int(int v) { return __reduce_max_sync(0xffffffffu, v); }
+// The pair that holds tile t: ((t + 1) nc - 1) / total.
+__device__ __forceinline__ int holder(long long t, long long total, int nc) {
+  return total < (1 << 22) ? (int)(((uint32_t)(t + 1) * (uint32_t)nc - 1u) / (uint32_t)total)
+                           : (int)(((t + 1) * nc - 1) / total);
+}
 
 // One warp: the share of pair c.
-__device__ void make_plan(const Params& p, int c, Plan* out) {
+__device__ __noinline__ void make_plan(const Params& p, int c, Plan* out) {
   const int lane = threadIdx.x & 31, items = p.B * p.groups;
   long long total = 0;
   int longest = 0, nonempty = 0, nt[kPlanRegs];
   bool bad = false;
 #pragma unroll
   for (int k = 0; k < kPlanRegs; ++k) nt[k] = 0;
+#pragma unroll 1
   for (int i0 = 0, k = 0; i0 < items; i0 += 32, ++k) {
     const int n = i0 + lane < items ? item_tiles(p, i0 + lane) : 0;
     bad |= i0 + lane < items && n == 0;
@@ -167,8 +172,8 @@ __device__ void make_plan(const Params& p, int c, Plan* out) {
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  longest = warp_max_int(longest);
-  nonempty = warp_sum_int(nonempty);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  nonempty = __reduce_add_sync(0xffffffffu, nonempty);
   if (__any_sync(0xffffffffu, bad) && c == 0 && lane == 0) raise_error(p.err, MLA_ERR_LENGTH);
   Plan r;
   r.total = total;
@@ -180,31 +185,33 @@ __device__ void make_plan(const Params& p, int c, Plan* out) {
     if (lane == 0) *out = r;
     return;
   }
-  auto chunks = [&](int size) {
-    int n = 0;
+  // the smallest chunk whose chunks fit the pairs, if that is little above the even share
+  const int even = (int)share(total + r.nc - 1, 1, r.nc);
+  if (items <= 32 * kPlanRegs && nonempty <= r.nc && longest < (1 << 22)) {
+#pragma unroll 1
+    for (int size = even; size <= even + kSwitchTiles; ++size) {
+      const float inv = 1.f / (float)size;
+      int n = 0;
 #pragma unroll
-    for (int k = 0; k < kPlanRegs; ++k) n += (nt[k] + size - 1) / size;
-    return warp_sum_int(n);
-  };
-  // the smallest chunk whose chunks fit the pairs
-  const int even = (int)((total + r.nc - 1) / r.nc);
-  if (items <= 32 * kPlanRegs && nonempty <= r.nc) {
-    int lo = even, hi = longest;
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      if (chunks(mid) <= r.nc)
-        hi = mid;
-      else
-        lo = mid + 1;
+      for (int k = 0; k < kPlanRegs; ++k) {
+        // ceil(nt / size): the float quotient is within one of the exact one
+        int q = (int)((float)nt[k] * inv);
+        q += (q * size < nt[k]) + ((q + 1) * size < nt[k]) - ((q - 1) * size >= nt[k] && q > 0);
+        n += q;
+      }
+      if ((int)__reduce_add_sync(0xffffffffu, n) <= r.nc) {
+        r.chunk = size;
+        break;
+      }
     }
-    if (lo <= even + kSwitchTiles) r.chunk = lo;
   }
   if (r.chunk == 0) {
-    r.lo = total * c / r.nc;
-    r.hi = total * (c + 1) / r.nc;
+    r.lo = share(total, c, r.nc);
+    r.hi = share(total, c + 1, r.nc);
   }
   long long base = 0;  // chunks or tiles before item i0
   const long long at = r.chunk > 0 ? c : r.lo;
+#pragma unroll 1
   for (int i0 = 0; i0 < items; i0 += 32) {
     const int tiles = i0 + lane < items ? item_tiles(p, i0 + lane) : 0;
     const int n = r.chunk > 0 ? (tiles + r.chunk - 1) / r.chunk : tiles;
@@ -229,7 +236,7 @@ __device__ void make_plan(const Params& p, int c, Plan* out) {
 }
 
 // One thread: the next piece of pair c.
-__device__ void next_piece(const Params& p, int c, Plan& s, Piece* out) {
+__device__ __noinline__ void next_piece(const Params& p, int c, Plan& s, Piece* out) {
   Piece r;
   r.item = -1;
   r.begin = r.end = r.tiles = r.slot = r.c0 = r.n = 0;
@@ -256,10 +263,9 @@ __device__ void next_piece(const Params& p, int c, Plan& s, Piece* out) {
       r.tiles = nt;
       r.begin = (int)(s.lo - s.tb);
       r.end = (int)(end - s.tb);
-      // the pair that holds tile t is ((t + 1) nc - 1) / total
-      r.c0 = (int)(((s.tb + 1) * s.nc - 1) / s.total);
-      r.n = (int)(((s.tb + nt) * s.nc - 1) / s.total) - r.c0 + 1;
-      r.slot = 2 * c + (s.total * c / s.nc < s.tb ? 1 : 0);  // a pair's first and its later pieces
+      r.c0 = holder(s.tb, s.total, s.nc);
+      r.n = holder(s.tb + nt - 1, s.total, s.nc) - r.c0 + 1;
+      r.slot = 2 * c + (share(s.total, c, s.nc) < s.tb ? 1 : 0);  // a pair's first and its later pieces
       s.lo = end;
       s.tb += nt;
       ++s.item;
@@ -320,14 +326,14 @@ __device__ __forceinline__ void store_part(const Part& k, uint32_t dst, int lane
   fence_proxy_async_smem();
   __syncwarp();
 }
-__device__ __forceinline__ void load_rope(const Params& p, int b, int tile, int len, int lane, uint4 (&k)[16]) {
+// The rotary warp's lane: half of the rotary row of the same four keys.
+__device__ __forceinline__ void load_rope(const uint8_t*& src, int64_t rows16, int left, uint4 (&k)[16]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int t = tile * kTile + 16 * i + (lane >> 1);
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.kv.k_r) + b * p.kv.kr_b +
-                                                      t * p.kv.kr_r) + 4 * (lane & 1);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) k[4 * i + j] = t < len ? __ldg(src + j) : make_uint4(0u, 0u, 0u, 0u);
+    for (int j = 0; j < 4; ++j)
+      k[4 * i + j] = 16 * i < left ? __ldg(reinterpret_cast<const uint4*>(src) + j) : make_uint4(0u, 0u, 0u, 0u);
+    src += rows16;
   }
 }
 __device__ __forceinline__ void store_rope(const uint4 (&k)[16], uint32_t dst, int lane) {
@@ -345,88 +351,85 @@ __device__ __forceinline__ void store_rope(const uint4 (&k)[16], uint32_t dst, i
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-__device__ __forceinline__ float max_abs4(const uint4& v) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  float m = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
-  return m;
-}
-__device__ __forceinline__ uint4 scale_to_f16(const uint4& v, float a, float b) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t r[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = pack_f16x2_ieee(bf16_lo(w[i]) * a * b, bf16_hi(w[i]) * a * b);
-  return make_uint4(r[0], r[1], r[2], r[3]);
+
+// One thread: the item's query rows as they are (bf16, rows past R as zeros): the six slabs of TMEM over the
+// value buffers, the other two and the rotary one to their place.  Slabs count from the CTA's own half.
+__device__ __noinline__ void fetch_query(const Params& p, Smem& sm, uint32_t base, int b, int g, int hf) {
+  fence_proxy_async_smem();  // the buffers were read and written by threads before
+  const uint64_t pol = policy_evict_last();
+  const uint32_t bar = smem_u32(&sm.q_full);
+  mbar_arrive_expect_tx(bar, 9 * kQSlabBytes);
+#pragma unroll 1
+  for (int j = 0; j < 8; ++j)
+    tma_load_3d(base + (j < kQTmemSlabs ? 0 : kQOff - kQTmemSlabs * kQSlabBytes) + j * kQSlabBytes, &p.tm_q, bar,
+                64 * (j ^ (4 * hf)), kRows * g, b, pol);
+  tma_load_3d(base + kQOff + 2 * kQSlabBytes, &p.tm_qp, bar, 0, kRows * g, b, pol);
 }
 
-// The item's query rows: latent part as fp16 (the six slabs of TMEM into `stage`, two into the resident buffer),
-// rotary part as bf16, both times the row's power of two; rows past R as zeros.  Warp w of kQLoaders.
-__device__ __noinline__ void load_query(const Params& p, Smem& sm, uint32_t stage, uint32_t resident, int b, int g,
-                                           int hf, int w, int lane) {
-  constexpr int kBatch = 4;
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("{\n\t.reg .b32 t;\n\tabs.bf16x2 t, %2;\n\tmax.bf16x2 %0, %1, t;\n\t}" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The query rows in place, by the softmax warps (h = 0: the own half's slabs) and the four warps that decode the
+// other half (h = 1: its slabs and the rotary one), one row per thread of each: the row's power of two, its latent
+// part to fp16 (in TMEM, or where it is), its rotary part scaled where it is.
+__device__ __noinline__ bool place_query(const Params& p, Smem& sm, uint32_t base, uint32_t tmem, int h, uint32_t parity) {
+  const int r = 32 * ((threadIdx.x >> 5) & 3) + (threadIdx.x & 31);  // the row is the warp's TMEM lane
+  const bool ok = wait_warp(sm, sm.q_full, parity, p.err);
+  auto chunk = [&](int j, int c) {  // address of 16-byte chunk c of slab j (8: rotary)
+    return base + (j < kQTmemSlabs ? 0 : kQOff - kQTmemSlabs * kQSlabBytes) + j * kQSlabBytes + r * 128 + ((c ^ (r & 7)) << 4);
+  };
+  const float ls = p.kv.latent_scale;
+  float m = 0.f;
+  uint32_t big = 0u;
 #pragma unroll 1
-  for (int r0 = w; r0 < kRows; r0 += kQLoaders * kBatch) {
-    uint4 lat[kBatch][2], rope[kBatch];
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int r = r0 + k * kQLoaders;
-      lat[k][0] = lat[k][1] = rope[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < kRows && kRows * g + r < p.R) {
-        const int64_t row = (int64_t)b * p.R + kRows * g + r;
-        const uint4* q = reinterpret_cast<const uint4*>(p.q_tilde + row * p.ldqt);
-        lat[k][0] = __ldg(q + lane);
-        lat[k][1] = __ldg(q + 32 + lane);
-        if (lane < 8) rope[k] = __ldg(reinterpret_cast<const uint4*>(p.q_pe + row * p.ldqp) + lane);
-      }
+  for (int j = 4 * h; j < 4 + 5 * h; ++j) {
+    if (j == 8) {
+      m = fmaxf(bf16_lo(big), bf16_hi(big)) * ls;
+      big = 0u;
     }
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int r = r0 + k * kQLoaders;
-      if (r >= kRows) break;
-      float m = fmaxf(fmaxf(max_abs4(lat[k][0]), max_abs4(lat[k][1])) * p.kv.latent_scale, max_abs4(rope[k]));
-      m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
-      // 2^e that puts the largest element into [2^14, 2^15)
-      const int e = m > 0.f ? max(-126, min(126, 14 + 127 - (int)(__float_as_uint(m) >> 23))) : 0;
-      const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int slab = ((lane + 32 * h) >> 3) ^ (4 * hf), pos = lane & 7;  // counted from the own half
-        const uint4 v = scale_to_f16(lat[k][h], p.kv.latent_scale, mul);
-        const uint32_t base = slab < kQTmemSlabs ? stage + slab * kQSlabBytes : resident + (slab - kQTmemSlabs) * kQSlabBytes;
-        st_shared_v4_b32(base + r * 128 + ((pos ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
-      }
-      if (lane < 8) {
-        const uint32_t x[4] = {rope[k].x, rope[k].y, rope[k].z, rope[k].w};
-        uint32_t y[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = pack_bf16x2(bf16_lo(x[i]) * mul, bf16_hi(x[i]) * mul);
-        st_shared_v4_b32(resident + 2 * kQSlabBytes + r * 128 + ((lane ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
-      }
-      if (lane == 0) sm.row_scale[r] = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23), 1.2e-38f);
+    for (int c = 0; c < 8; ++c) {
+      const uint4 u = ld_shared_v4_b32(chunk(j, c));
+      big = max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(big, u.x), u.y), u.z), u.w);
     }
   }
-  fence_proxy_async_smem();
-}
-
-// Softmax warps: the staged query slabs into TMEM, one row per thread.
-__device__ __noinline__ void query_to_tmem(uint32_t base, uint32_t tmem) {
-  const int r = threadIdx.x;
-#pragma unroll 2
-  for (int j = 0; j < kQTmemSlabs; ++j) {
+  m = fmaxf(m, fmaxf(bf16_lo(big), bf16_hi(big)) * (h ? 1.f : ls));
+  sm.row_max[h][r] = m;
+  named_bar_sync(1, 256);
+  m = fmaxf(m, sm.row_max[1 - h][r]);
+  // 2^e that puts the row's largest element into [2^14, 2^15)
+  const int e = m > 0.f ? max(-126, min(126, 14 + 127 - (int)(__float_as_uint(m) >> 23))) : 0;
+  const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
+  if (h == 0) sm.row_scale[r] = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23), 1.2e-38f);
+#pragma unroll 1
+  for (int j = 4 * h; j < 4 + 5 * h; ++j) {
+    const float a = j < 8 ? ls : 1.f;
     uint32_t v[32];
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      const uint4 u = ld_shared_v4_b32(base + j * kQSlabBytes + r * 128 + ((c ^ (r & 7)) << 4));
-      v[4 * c] = u.x;
-      v[4 * c + 1] = u.y;
-      v[4 * c + 2] = u.z;
-      v[4 * c + 3] = u.w;
+      const uint4 u = ld_shared_v4_b32(chunk(j, c));
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float lo = bf16_lo(w[i]) * a * mul, hi = bf16_hi(w[i]) * a * mul;
+        v[4 * c + i] = j < 8 ? pack_f16x2_ieee(lo, hi) : pack_bf16x2(lo, hi);
+      }
     }
-    tmem_st32(tmem + ((uint32_t)(r & 96) << 16) + kColQ + 32 * j, v);
+    if (j < kQTmemSlabs) {
+      tmem_st32(tmem + ((uint32_t)(r & 96) << 16) + kColQ + 32 * j, v);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        st_shared_v4_b32(chunk(j, c), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+    }
   }
   tmem_st_wait();
   tc_fence_before();
+  fence_proxy_async_smem();
+  return ok;
 }
 
 // What a role needs to know of the piece at hand.  The roles are functions of their own so that each has the
@@ -466,19 +469,19 @@ __device__ __noinline__ bool mma_role(const Params& p, uint32_t it0, uint32_t n)
 #pragma unroll 1
     for (uint32_t t = 0; t <= n; ++t) {
       if (t < n) {
-        const uint32_t it = it0 + t, st = it % kKvStages, kv = base + st * kKvBytes;
+        // All waits first: they run under O(t - 2), and the issue below then stays ahead of the tensor pipe.
+        const uint32_t it = it0 + t, st = it % kKvStages, kv = base + st * kKvBytes, k = kKPerTile * it;
         ok = wait(sm, sm.s_empty, (it & 1u) ^ 1u, p.err) && wait(sm, sm.kv_full[st], (it / kKvStages) & 1u, p.err);
+#pragma unroll 1
+        for (uint32_t j = 0; j < kKPerTile && ok; ++j)
+          ok = wait(sm, sm.k_full[(k + j) % kKSlots], ((k + j) / kKSlots) & 1u, p.err);
         if (!ok) break;
         tc_fence_after();
-#pragma unroll 1
+#pragma unroll
         for (int j = 0; j < 4; ++j) slab_ts(tS, tQ + 32 * j, kv + j * kSlabBytes, j == 0);
-        uint32_t k = kKPerTile * it;
-#pragma unroll 1
-        for (int j = 0; j < kKPerTile; ++j, ++k) {
-          const uint32_t slot = k % kKSlots, keys = base + kKOff + slot * kSlabBytes;
-          ok = wait(sm, sm.k_full[slot], (k / kKSlots) & 1u, p.err);
-          if (!ok) break;
-          tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < kKPerTile; ++j) {
+          const uint32_t slot = (k + j) % kKSlots, keys = base + kKOff + slot * kSlabBytes;
           if (j == 0)
             slab_ss(tS, base + kQOff + 2 * kQSlabBytes, keys, idesc_bf16_f32(kRows, kTile, 0, 0));
           else if (j < 3)
@@ -487,7 +490,6 @@ __device__ __noinline__ bool mma_role(const Params& p, uint32_t it0, uint32_t n)
             slab_ss(tS, base + kQOff + (j - 3) * kQSlabBytes, keys, idesc_f16_f32(kRows, kTile, 0, 0));
           mma_commit(smem_u32(&sm.k_empty[slot]));
         }
-        if (!ok) break;
         mma_commit(smem_u32(&sm.s_full));
       }
       if (t > 0) {
@@ -645,12 +647,13 @@ __device__ __noinline__ bool softmax_role(const Params& p, Smem& sm, Work w) {
       if (lane == 0 && mine > 0) {
         bulk_store_s2g(p.ws_o + (part * min(p.R, kRows) + 32 * warp) * 256, base + 32 * warp * 1024, mine * 1024);
         bulk_group_commit();
-        bulk_group_wait_all();
+        bulk_group_wait_read_all();
       }
       if (r < rows) p.ws_ml[part * kRows + r] = make_float2(ref, l);
     }
     if (threadIdx.x == 0 && hf == 0 && w.begin == 0) p.table[w.b * p.groups + w.g] = make_int4(w.slot, w.c0, w.pieces, 0);
     tc_fence_before();
+    fence_proxy_async_smem();
   }
   return ok;
 }
@@ -671,6 +674,7 @@ __device__ __noinline__ bool latent_role(const Params& p, Smem& sm, Work w) {
     if (!wait_warp(sm, own ? sm.kv_empty[slot] : sm.k_empty[slot], (use & 1u) ^ 1u, p.err)) return false;
     store_part(k, w.base + (own ? slot * kKvBytes + j * kSlabBytes : kKOff + slot * kSlabBytes), lane);
     if (lane == 0) mbar_arrive(smem_u32(own ? &sm.kv_full[slot] : &sm.k_full[slot]));
+    if (warp == kKvWarp0 && lane == 0) *const_cast<volatile int*>(&sm.progress) = (int)t;
     left -= kTile;
     load_part(src, left, k);
   }
@@ -692,19 +696,34 @@ __device__ __forceinline__ void prefetch_tile(const Params& p, int b, int tile, 
   }
 }
 
-// One warp: the rotary slab of every tile, and the tiles' way into L2.
+// One warp: the tiles' way into L2, kPrefetch tiles ahead of the decode warps.
+__device__ __noinline__ void prefetch_role(const Params& p, Smem& sm, Work w) {
+  const int lane = threadIdx.x & 31;
+  const volatile int* progress = &sm.progress;
+  const volatile int* abort = &sm.abort;
+#pragma unroll 1
+  for (int t = kPrefetch; t < (int)w.n; ++t) {
+    while (*progress + kPrefetch < t && !*abort) __nanosleep(100);  // the decode warps' waits are bounded
+    prefetch_tile(p, w.b, w.begin + t, w.len, lane);
+  }
+}
+
+// One warp: the rotary slab of every tile.
 __device__ __noinline__ bool rope_role(const Params& p, Smem& sm, Work w) {
   const int lane = threadIdx.x & 31;
+  const uint8_t* src = reinterpret_cast<const uint8_t*>(static_cast<const __nv_bfloat16*>(p.kv.k_r) + w.b * p.kv.kr_b +
+                                                        ((int64_t)w.begin * kTile + (lane >> 1)) * p.kv.kr_r) + 64 * (lane & 1);
+  int left = w.len - w.begin * kTile - (lane >> 1);
   uint4 k[16];
-  load_rope(p, w.b, w.begin, w.len, lane, k);
+  load_rope(src, 32 * p.kv.kr_r, left, k);
 #pragma unroll 1
   for (uint32_t t = 0; t < w.n; ++t) {
     const uint32_t q = kKPerTile * (w.it0 + t), slot = q % kKSlots;
     if (!wait_warp(sm, sm.k_empty[slot], ((q / kKSlots) & 1u) ^ 1u, p.err)) return false;
     store_rope(k, w.base + kKOff + slot * kSlabBytes, lane);
     if (lane == 0) mbar_arrive(smem_u32(&sm.k_full[slot]));
-    load_rope(p, w.b, w.begin + t + 1, w.len, lane, k);
-    if (t + kPrefetch < w.n) prefetch_tile(p, w.b, w.begin + t + kPrefetch, w.len, lane);
+    left -= kTile;
+    load_rope(src, 32 * p.kv.kr_r, left, k);
   }
   return true;
 }
@@ -726,6 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
       mbar_init(smem_u32(&sm.k_full[s]), 1);
       mbar_init(smem_u32(&sm.k_empty[s]), 1);
     }
+    mbar_init(smem_u32(&sm.q_full), 1);
     mbar_init(smem_u32(&sm.s_full), 1);
     mbar_init(smem_u32(&sm.s_empty), 4);
     mbar_init(smem_u32(&sm.p_full), 4);
@@ -750,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
   const uint32_t tmem = sm.tmem_base;
 
   // it0: tiles of the earlier pieces.  All warps take every barrier of every piece, also after a failed wait.
-  uint32_t it0 = 0;
+  uint32_t it0 = 0, pieces = 0;
   bool dead = false;
   while (true) {
     if (sm.piece.item < 0) break;
@@ -767,22 +787,29 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     w.slot = sm.piece.slot;
     w.c0 = sm.piece.c0;
     w.pieces = sm.piece.n;
-    if (warp == kRopeWarp)
+    if (threadIdx.x == 0) {
+      sm.progress = 0;
+      fetch_query(p, sm, base, w.b, w.g, hf);
+    }
+    if (warp == kPrefetchWarp)
       for (int t = 0; t < kPrefetch && t < (int)w.n; ++t) prefetch_tile(p, w.b, w.begin + t, w.len, lane);
-    if (warp <= kQLoaders && warp != kMmaWarp)
-      load_query(p, sm, base, base + kQOff, w.b, w.g, hf, warp < kMmaWarp ? warp : warp - 1, lane);
-    __syncthreads();
-    if (warp < 4) query_to_tmem(base, tmem);
+    __syncwarp();
+    // (all eight warps come here in every piece: they meet inside)
+    if (warp < 4 || (warp >= kKWarp0 && warp < kRopeWarp))
+      dead |= !place_query(p, sm, base, tmem, warp >= kKWarp0 ? 1 : 0, pieces & 1u);
+    ++pieces;
     __syncthreads();
     tc_fence_after();
+    if (sm.abort) dead = true;
     if (!dead) {
       bool ok = true;
       if (warp < 4)
         ok = softmax_role(p, sm, w);
       else if (warp > kMmaWarp)
-        ok = warp < kRopeWarp ? latent_role(p, sm, w) : rope_role(p, sm, w);
+        ok = warp < kRopeWarp ? latent_role(p, sm, w) : warp > kRopeWarp || rope_role(p, sm, w);
       else
         ok = mma_role(p, it0, w.n);
+      if (warp == kPrefetchWarp) prefetch_role(p, sm, w);
       dead = !ok;
     }
     __syncwarp();
@@ -799,6 +826,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     }
     __syncwarp();
   }
+  if (threadIdx.x == 0 && sm.abort && pieces > 0)  // a query still on its way lands before the block leaves
+    mbar_wait(smem_u32(&sm.q_full), (pieces - 1) & 1u, &sm.never, kWaitLimitNs);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -851,6 +880,12 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Param
   if (hf == 0 && lane == 0 && p.lse != nullptr) p.lse[row] = L == 0.f ? -INFINITY : M * kLn2 + logf(L);
 }
 
+bool query_map(CUtensorMap* m, const void* base, int width, int R, int B, int64_t ld) {
+  const uint64_t dims[3] = {(uint64_t)width, (uint64_t)R, (uint64_t)B};
+  const uint64_t strides[2] = {(uint64_t)ld * 2, (uint64_t)ld * 2 * R};
+  const uint32_t box[3] = {64, kRows, 1};
+  return make_tensor_map_bf16(m, base, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
 int max_pairs() {
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
@@ -878,13 +913,12 @@ cudaError_t decode_fp4_tc_launch(const Fp4DecodeArgs& a, void* ws, cudaStream_t 
   using namespace decode_fp4;
   Params p{};
   p.kv = a.kv;
-  p.q_tilde = static_cast<const __nv_bfloat16*>(a.q_tilde);
-  p.q_pe = static_cast<const __nv_bfloat16*>(a.q_pe);
-  p.ldqt = a.ldqt; p.ldqp = a.ldqp;
   p.lengths = a.lengths;
   p.B = a.B; p.T = a.T; p.n_h = a.n_h; p.n_max = a.n_max;
   p.R = a.T * a.n_h;
   p.groups = (p.R + kRows - 1) / kRows;
+  if (!query_map(&p.tm_q, a.q_tilde, kDC, p.R, a.B, a.ldqt) || !query_map(&p.tm_qp, a.q_pe, kDR, p.R, a.B, a.ldqp))
+    return cudaErrorInvalidValue;
   p.pairs = shape_pairs(a.n_h, a.B, a.T, a.n_max);
   p.scale_log2 = a.scale * kLog2e;
   p.ctx = static_cast<__nv_bfloat16*>(a.ctx);
