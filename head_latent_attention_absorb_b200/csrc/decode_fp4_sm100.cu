@@ -7,29 +7,38 @@
 // 669 a byte, far right of the GPU's ridge.
 //
 // Why this split.  The fp32 context of 128 rows x 512 features fills TMEM, so no SM can hold it beside
-// scores.  A CTA therefore keeps one half of the latent features of the context (256 columns) and computes
-// all 576 features of the scores itself: the score work is done twice, 27.3 instead of 17.8 MFLOP per 64
-// rows and two CTAs, and in return nothing is exchanged, no CTA waits for another one and the halves need
-// not even run at the same time.  (Exchanging partial scores between two CTAs through distributed shared
-// memory holds the bf16 decode at one third of the tensor peak.)
+// scores.  Every MMA therefore spans a CTA pair (cta_group::2, M = 128): each CTA holds 64 of the rows with their
+// whole context (256 columns).  The pair's MMAs take B from both CTAs' shared memory, the scores' keys split
+// by position (64 of a tile's 128 each), the values' by feature (256 of 512 each).  So a CTA decodes 64 whole
+// rows, and the values of its 256 features for the other 64 rows: 1.5 times the cache's elements per pair, and
+// no data crosses between the CTAs, only barrier arrivals.  Pair MMAs of these shapes run at the full rate also
+// with A in shared memory (2190 cycles a tile measured alone; single-CTA M = 128 MMAs with N = 64 need 42 cycles
+// instead of 32, and 75 with A in shared memory).
 //
 // * Operands are fp16: code * scale has at most six significant bits and lies in 2^-10 .. 2688, so the cache
 //   is exact; a query row is scaled by a power of two that puts its largest element into [2^14, 2^15), so that
 //   bf16 elements are exact down to 2^-31 of it, and the power goes into the row's softmax scale.  The rotary
 //   part stays in bf16 (separate MMAs into the same accumulator).  Probabilities are rounded to fp16.
-// * Tiles of 64 keys.  TMEM: context 256 columns, scores 64, query features [0, 384) 192 columns as the A
-//   operand; the other query features and the probabilities are A operands in shared memory.
-// * Nine warps decode: lane pairs own a key, 16-byte loads of codes two tiles ahead in registers, cvt to fp16,
-//   one product with the block's scale, stores in the 128-byte-swizzled layout.  The four slabs of the
-//   CTA's own half serve the scores (K-major) and the values (MN-major) and stay until the values are used: three
-//   buffers.  The other half's slabs and the rotary slab are free once the scores are done: a ring of eight.
+// * Shared memory (224 KB): region X holds the key slabs of features 0..255 (three buffers), region Y those of
+//   256..511 (two), the rotary slab (two), query features 384..511 and the rotary query, the probabilities.
+//   One of the regions holds the CTA's own half of the features: its slabs serve the scores (K-major) and are the
+//   values of these 64 rows (MN-major).  In the other one the values of the other 64 rows replace the slabs once
+//   the scores are done.  Then X holds the values of the tile's first 64 rows and Y of its last 64, in both CTAs.
+// * TMEM: context 256 columns, scores 64, query features 0..383 192 columns (A operand, in both lane halves).
+// * Nine warps decode: lane pairs own a key, 16-byte loads of codes one tile ahead in registers (a warp of its
+//   own brings the rows to L2 four tiles ahead), cvt to fp16, one product with the block's scale, stores in the
+//   128-byte-swizzled layout.
 // * MMA order S(t + 1), O(t), S(t + 2), ...: the softmax of tile t runs under S(t + 1), and the tensor pipe
-//   works on O(t - 1) while S(t) is read from TMEM.
-// * Four softmax warps, one query row per thread; base-2 exponentials, their reference moved (and the context
-//   rescaled in TMEM) only when the running maximum grows by more than 8.
-// * Work: chunks of single sequences when each can have CTAs of its own and the chunks come out balanced, else
+//   works on O(t - 1) while S(t) is read from TMEM.  The scores start with X, whose third buffer is decoded ahead,
+//   while Y's are decoded behind O.
+// * Four softmax warps: a thread has 64 keys of a query row and agrees with the thread that has the row's other
+//   64 on the reference of the base-2 exponentials, which moves (and the context is rescaled in TMEM) only when the
+//   running maximum grows by more than 8.
+// * Work: chunks of single sequences when each can have pairs of its own and the chunks come out balanced, else
 //   equal ranges of all tiles.  A sequence that is cut leaves fp32 partials and a second kernel joins them in a
 //   fixed order.
+// * The roles are functions with compact loops: together they have to fit the instruction cache (unrolled, the
+//   loops took twice as long).
 // * Every wait is bounded; on expiry the kernel records MLA_ERR_TIMEOUT and all warps run out their barriers.
 #include <math.h>
 
@@ -45,21 +54,20 @@ namespace decode_fp4 {
 using namespace sm100;
 
 constexpr int kDC = 512, kDR = 64;
-constexpr int kTile = 64;                        // keys per tile
-constexpr int kRows = 128;                       // query rows per group: the rows of every MMA
-constexpr int kSlabBytes = kTile * 128;          // 64 keys of 64 features
-constexpr int kKvStages = 3, kKvBytes = 4 * kSlabBytes;
-constexpr int kKSlots = 8, kKPerTile = 5;        // rotary slab and the other half's four slabs
-constexpr int kQSlabBytes = kRows * 128;         // 128 query rows of 64 features
+constexpr int kTile = 128, kKeys = 64;           // keys per tile, and of it per CTA
+constexpr int kRows = 128, kMyRows = 64;         // query rows per group, and per CTA
+constexpr int kSlabBytes = 64 * 128;             // 64 rows (keys or query rows) of 64 features
+constexpr int kRegion = 4 * kSlabBytes;          // half of the latent features of 64 keys
+constexpr int kXBufs = 3, kYBufs = 2, kRopeBufs = 2;
 constexpr int kQTmemSlabs = 6;                   // query slabs in TMEM; the other two and the rotary one in shared memory
-constexpr int kKOff = kKvStages * kKvBytes;
-constexpr int kQOff = kKOff + kKSlots * kSlabBytes;
-constexpr int kPOff = kQOff + 3 * kQSlabBytes;
-constexpr int kSmemOff = kPOff + kRows * 128;
-static_assert(kQTmemSlabs * kQSlabBytes <= kQOff, "the query is staged in the key buffers");
-static_assert(kRows * 256 * 4 <= kQOff, "the partial context is staged in the key buffers");
-constexpr int kMmaWarp = 4, kKvWarp0 = 5, kKWarp0 = 9, kRopeWarp = 13;
-constexpr int kPrefetchWarp = 14;
+constexpr int kYOff = kXBufs * kRegion;
+constexpr int kRopeOff = kYOff + kYBufs * kRegion;
+constexpr int kQOff = kRopeOff + kRopeBufs * kSlabBytes;
+constexpr int kPOff = kQOff + 3 * kSlabBytes;    // probabilities of the first and the last 64 keys
+constexpr int kSmemOff = kPOff + 2 * kSlabBytes;
+static_assert(kQTmemSlabs * kSlabBytes <= kYOff, "the query is staged in region X");
+static_assert(kMyRows * kDC * 4 <= kRopeOff, "the partial context is staged in the regions");
+constexpr int kMmaWarp = 4, kXWarp0 = 5, kYWarp0 = 9, kRopeWarp = 13, kPrefetchWarp = 14;
 constexpr int kThreads = 32 * 15;
 constexpr uint32_t kTmemCols = 512, kColO = 0, kColS = 256, kColQ = 320;
 // Probabilities are 2^(z - ref): ref is set kRaise below the largest score so far (log2 units) and moved up
@@ -68,12 +76,12 @@ constexpr uint32_t kTmemCols = 512, kColO = 0, kColS = 256, kColQ = 320;
 constexpr float kRaise = 7.f, kRescale = 15.f;
 constexpr int kPrefetch = 4;                     // tiles that L2 is ahead of the decode warps
 constexpr int kPlanRegs = 3;                     // items per lane that the chunk search holds (more than the pairs)
-constexpr int kSwitchTiles = 5;                  // what a second piece costs a CTA, in tiles
+constexpr int kSwitchTiles = 3;                  // what a second piece costs a CTA, in tiles
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct Params {
-  CUtensorMap tm_q;   // (d_c, R, B) query rows, box (64, 128, 1), 128-byte swizzle: rows past R read as zeros
+  CUtensorMap tm_q;   // (d_c, R, B) query rows, box (64, 64, 1), 128-byte swizzle: rows past R read as zeros
   CUtensorMap tm_qp;  // (d_r, R, B), same box
   CacheView kv;
   const int32_t* lengths;
@@ -82,7 +90,7 @@ struct Params {
   __nv_bfloat16* ctx;
   float* lse;
   int4* table;    // [B * groups] partials of an item: first slot, first CTA pair, number
-  float2* ws_ml;  // [2 pairs slots][2 halves][128] (reference in log2 units, sum)
+  float2* ws_ml;  // [2 pairs slots][128] (reference in log2 units, sum)
   float* ws_o;    // [slots][2 halves][min(R, 128)][256], 16-byte chunk j of row r at (j + r) % 64
   int32_t* err;
 };
@@ -108,12 +116,15 @@ struct Piece {
 };
 
 struct Smem {
-  uint64_t kv_full[kKvStages], kv_empty[kKvStages], k_full[kKSlots], k_empty[kKSlots];
-  uint64_t q_full, s_full, s_empty, p_full, pv_done, drain;
-  alignas(16) float row_scale[kRows];  // softmax scale of a query row, log2 units
+  // waited for in the even CTA only; arrivals from both CTAs
+  uint64_t x_full[kXBufs], y_full[kYBufs], rope_full[kRopeBufs], v_full[2], s_empty, p_full;
+  // in each CTA; arrivals from the MMAs
+  uint64_t x_empty[kXBufs], y_empty[kYBufs], rope_empty[kRopeBufs], s_full, pv_done, drain;
+  uint64_t q_full, ref_bar[2], sum_bar[2];
+  alignas(16) float row_scale[kRows];  // by TMEM lane: softmax scale of the query row, log2 units
+  float row_max[2][kRows];             // by TMEM lane: exchange between the threads of a row
   Plan plan;
   Piece piece;
-  float row_max[2][kRows];  // largest element of a query row, each half of its slabs
   uint32_t tmem_base;
   int abort, never, progress;
 };
@@ -126,19 +137,29 @@ __device__ __forceinline__ uint8_t* shared_base() {
 }
 
 // Bounded wait that records its own expiry; what follows a first failed try is one shared function, since the
-// roles' loops together have to fit the instruction cache.
-__device__ __noinline__ bool wait_more(Smem& sm, uint32_t bar, uint32_t parity, int32_t* err) {
-  if (mbar_wait(bar, parity, &sm.abort, kWaitLimitNs)) return true;
+// roles' loops together have to fit the instruction cache.  `cluster`: the arrivals come from both CTAs.
+__device__ __noinline__ bool wait_more(Smem& sm, uint32_t bar, uint32_t parity, bool cluster, int32_t* err) {
+  if (mbar_wait(bar, parity, &sm.abort, kWaitLimitNs, cluster)) return true;
   raise_error(err, MLA_ERR_TIMEOUT);
   sm.abort = 1;
   return false;
 }
 __device__ __forceinline__ bool wait(Smem& sm, uint64_t& bar, uint32_t parity, int32_t* err) {
-  return mbar_try_wait(smem_u32(&bar), parity) || wait_more(sm, smem_u32(&bar), parity, err);
+  return mbar_try_wait(smem_u32(&bar), parity) || wait_more(sm, smem_u32(&bar), parity, false, err);
+}
+__device__ __forceinline__ bool wait_both(Smem& sm, uint64_t& bar, uint32_t parity, int32_t* err) {
+  return mbar_try_wait_cluster(smem_u32(&bar), parity) || wait_more(sm, smem_u32(&bar), parity, true, err);
 }
 // All lanes wait; the warp goes on only if all of them saw the phase complete.
 __device__ __forceinline__ bool wait_warp(Smem& sm, uint64_t& bar, uint32_t parity, int32_t* err) {
   return __all_sync(0xffffffffu, wait(sm, bar, parity, err));
+}
+// Arrival on a barrier of the even CTA.
+__device__ __forceinline__ void arrive_even(uint64_t& bar, uint32_t rank) {
+  if (rank == 0)
+    mbar_arrive(smem_u32(&bar));
+  else
+    mbar_arrive_remote_cta(mapa(smem_u32(&bar), 0));
 }
 
 // total c / nc, in 32 bits where they hold the product.
@@ -277,7 +298,7 @@ __device__ __noinline__ void next_piece(const Params& p, int c, Plan& s, Piece* 
   *out = r;
 }
 
-// A decode warp's lane: 32 features of one 64-feature slab for four keys of a tile (lane / 2 + 16 i).
+// A decode warp's lane: 32 features of one 64-feature slab for four of 64 keys (lane / 2 + 16 i).
 struct Part {
   uint4 code[4];
   uint32_t scale[4];
@@ -287,12 +308,13 @@ struct PartSource {
   const uint8_t* scale;
   int64_t code16, scale16;  // 16 rows on
 };
-__device__ __forceinline__ PartSource part_source(const Params& p, int b, int tile, int slab, int lane) {
-  const int64_t t = (int64_t)tile * kTile + (lane >> 1);
+// From key `first` on
+__device__ __forceinline__ PartSource part_source(const Params& p, int b, int first, int slab, int lane) {
+  const int64_t t = (int64_t)first + (lane >> 1);
   return {p.kv.c4 + b * p.kv.c4_b + t * p.kv.c4_r + 32 * slab + 16 * (lane & 1),
           p.kv.sc + b * p.kv.sc_b + t * p.kv.sc_r + 4 * slab + 2 * (lane & 1), 16 * p.kv.c4_r, 16 * p.kv.sc_r};
 }
-// Loads the source's tile and moves on to the next one; `left` keys from the lane's first one are in the sequence.
+// Loads the source's keys and moves on to the next tile's; `left` keys from the lane's first one are in the sequence.
 __device__ __forceinline__ void load_part(PartSource& s, int left, Part& k) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -305,6 +327,8 @@ __device__ __forceinline__ void load_part(PartSource& s, int left, Part& k) {
     s.code += s.code16;
     s.scale += s.scale16;
   }
+  s.code += 4 * s.code16;
+  s.scale += 4 * s.scale16;
 }
 __device__ __forceinline__ void store_part(const Part& k, uint32_t dst, int lane) {
   const int half = lane & 1;
@@ -335,6 +359,7 @@ __device__ __forceinline__ void load_rope(const uint8_t*& src, int64_t rows16, i
       k[4 * i + j] = 16 * i < left ? __ldg(reinterpret_cast<const uint4*>(src) + j) : make_uint4(0u, 0u, 0u, 0u);
     src += rows16;
   }
+  src += 4 * rows16;
 }
 __device__ __forceinline__ void store_rope(const uint4 (&k)[16], uint32_t dst, int lane) {
 #pragma unroll
@@ -352,18 +377,20 @@ __device__ __forceinline__ void store_rope(const uint4 (&k)[16], uint32_t dst, i
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// One thread: the item's query rows as they are (bf16, rows past R as zeros): the six slabs of TMEM over the
-// value buffers, the other two and the rotary one to their place.  Slabs count from the CTA's own half.
-__device__ __noinline__ void fetch_query(const Params& p, Smem& sm, uint32_t base, int b, int g, int hf) {
+// Where slab j of the query lands (8: the rotary one).
+__device__ __forceinline__ uint32_t query_slab(uint32_t base, int j) {
+  return base + (j < kQTmemSlabs ? 0 : kQOff - kQTmemSlabs * kSlabBytes) + j * kSlabBytes;
+}
+
+// One thread: the CTA's 64 query rows of the item as they are (bf16, rows past R as zeros).
+__device__ __noinline__ void fetch_query(const Params& p, Smem& sm, uint32_t base, int b, int row) {
   fence_proxy_async_smem();  // the buffers were read and written by threads before
-  const uint64_t pol = policy_evict_last();
+  const uint64_t pol = policy_evict_first();
   const uint32_t bar = smem_u32(&sm.q_full);
-  mbar_arrive_expect_tx(bar, 9 * kQSlabBytes);
+  mbar_arrive_expect_tx(bar, 9 * kSlabBytes);
 #pragma unroll 1
-  for (int j = 0; j < 8; ++j)
-    tma_load_3d(base + (j < kQTmemSlabs ? 0 : kQOff - kQTmemSlabs * kQSlabBytes) + j * kQSlabBytes, &p.tm_q, bar,
-                64 * (j ^ (4 * hf)), kRows * g, b, pol);
-  tma_load_3d(base + kQOff + 2 * kQSlabBytes, &p.tm_qp, bar, 0, kRows * g, b, pol);
+  for (int j = 0; j < 8; ++j) tma_load_3d(query_slab(base, j), &p.tm_q, bar, 64 * j, row, b, pol);
+  tma_load_3d(query_slab(base, 8), &p.tm_qp, bar, 0, row, b, pol);
 }
 
 __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
@@ -372,15 +399,13 @@ __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// The query rows in place, by the softmax warps (h = 0: the own half's slabs) and the four warps that decode the
-// other half (h = 1: its slabs and the rotary one), one row per thread of each: the row's power of two, its latent
+// The query rows in place, by the softmax warps (h = 0: slabs 0..3) and warps kYWarp0.. (h = 1: slabs 4..7 and the
+// rotary one), one row per thread and TMEM lane (lanes 64.. repeat the rows): the row's power of two, its latent
 // part to fp16 (in TMEM, or where it is), its rotary part scaled where it is.
 __device__ __noinline__ bool place_query(const Params& p, Smem& sm, uint32_t base, uint32_t tmem, int h, uint32_t parity) {
-  const int r = 32 * ((threadIdx.x >> 5) & 3) + (threadIdx.x & 31);  // the row is the warp's TMEM lane
+  const int lane = 32 * ((threadIdx.x >> 5) & 3) + (threadIdx.x & 31), r = lane & (kMyRows - 1);
   const bool ok = wait_warp(sm, sm.q_full, parity, p.err);
-  auto chunk = [&](int j, int c) {  // address of 16-byte chunk c of slab j (8: rotary)
-    return base + (j < kQTmemSlabs ? 0 : kQOff - kQTmemSlabs * kQSlabBytes) + j * kQSlabBytes + r * 128 + ((c ^ (r & 7)) << 4);
-  };
+  auto chunk = [&](int j, int c) { return query_slab(base, j) + r * 128 + ((c ^ (r & 7)) << 4); };
   const float ls = p.kv.latent_scale;
   float m = 0.f;
   uint32_t big = 0u;
@@ -397,13 +422,13 @@ __device__ __noinline__ bool place_query(const Params& p, Smem& sm, uint32_t bas
     }
   }
   m = fmaxf(m, fmaxf(bf16_lo(big), bf16_hi(big)) * (h ? 1.f : ls));
-  sm.row_max[h][r] = m;
+  sm.row_max[h][lane] = m;
   named_bar_sync(1, 256);
-  m = fmaxf(m, sm.row_max[1 - h][r]);
+  m = fmaxf(m, sm.row_max[1 - h][lane]);
   // 2^e that puts the row's largest element into [2^14, 2^15)
   const int e = m > 0.f ? max(-126, min(126, 14 + 127 - (int)(__float_as_uint(m) >> 23))) : 0;
   const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
-  if (h == 0) sm.row_scale[r] = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23), 1.2e-38f);
+  if (h == 0) sm.row_scale[lane] = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23), 1.2e-38f);
 #pragma unroll 1
   for (int j = 4 * h; j < 4 + 5 * h; ++j) {
     const float a = j < 8 ? ls : 1.f;
@@ -419,8 +444,8 @@ __device__ __noinline__ bool place_query(const Params& p, Smem& sm, uint32_t bas
       }
     }
     if (j < kQTmemSlabs) {
-      tmem_st32(tmem + ((uint32_t)(r & 96) << 16) + kColQ + 32 * j, v);
-    } else {
+      tmem_st32(tmem + ((uint32_t)(lane & 96) << 16) + kColQ + 32 * j, v);
+    } else if (lane < kMyRows) {
 #pragma unroll
       for (int c = 0; c < 8; ++c)
         st_shared_v4_b32(chunk(j, c), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
@@ -437,8 +462,10 @@ __device__ __noinline__ bool place_query(const Params& p, Smem& sm, uint32_t bas
 struct Work {
   uint32_t base, tmem;   // shared memory, TMEM
   uint32_t it0, n;       // tiles of the earlier pieces, tiles of this one
-  int begin, b, g, len, hf;
+  int begin, b, g, len;
+  int rank;
   int slot, c0, pieces;  // as in Piece
+  int index;             // pieces before this one
 };
 
 // A 128-byte-swizzled shared-memory descriptor whose address is at + 32 k: the low word counts 16 bytes.
@@ -451,82 +478,89 @@ __device__ __forceinline__ uint64_t step_desc(uint32_t at, int k, uint32_t lbo_b
 __device__ __forceinline__ void slab_ts(uint32_t s, uint32_t q, uint32_t keys, bool first) {
 #pragma unroll
   for (int k = 0; k < 4; ++k)
-    mma_ts(s, q + 8 * k, step_desc(keys, k), idesc_f16_f32(kRows, kTile, 0, 0), first && k == 0 ? 0u : 1u);
+    mma_pair_ts(s, q + 8 * k, step_desc(keys, k), idesc_f16_f32(kRows, kTile, 0, 0), first && k == 0 ? 0u : 1u);
 }
 __device__ __forceinline__ void slab_ss(uint32_t s, uint32_t q, uint32_t keys, uint32_t idesc) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) mma_ss(s, step_desc(q, k), step_desc(keys, k), idesc, 1u);
+  for (int k = 0; k < 4; ++k) mma_pair_ss(s, step_desc(q, k), step_desc(keys, k), idesc, 1u);
+}
+// The context from 64 keys: their values at `v`, their probabilities at `pr`; 128 of each CTA's features at a time.
+__device__ __forceinline__ void values(uint32_t o, uint32_t pr, uint32_t v, bool first) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      mma_pair_ss(o + 128 * i, step_desc(pr, k), step_desc(v + 2 * i * kSlabBytes + 2048 * k, 0, kSlabBytes),
+                  idesc_f16_f32(kRows, 256, 0, 1), first && k == 0 ? 0u : 1u);
 }
 
-// One warp: the MMAs of a piece, issued by one thread: S(t), then O(t - 1).  Query slabs are counted from the
-// CTA's own half: 0..3 its half, 4..7 the other one; 0..5 are in TMEM.
+// One warp of the even CTA: the pair's MMAs of a piece, issued by one thread: S(t), then O(t - 1).
 __device__ __noinline__ bool mma_role(const Params& p, uint32_t it0, uint32_t n) {
   uint8_t* smem = shared_base();
   Smem& sm = *reinterpret_cast<Smem*>(smem + kSmemOff);
-  const uint32_t base = smem_u32(smem), tmem = sm.tmem_base, tS = tmem + kColS, tQ = tmem + kColQ;
+  const uint32_t base = smem_u32(smem), tmem = sm.tmem_base, tS = tmem + kColS, tQ = tmem + kColQ, tO = tmem + kColO;
+  constexpr uint16_t kBoth = 3;
   bool ok = true;
   if (elect_one()) {
 #pragma unroll 1
     for (uint32_t t = 0; t <= n; ++t) {
       if (t < n) {
-        // All waits first: they run under O(t - 2), and the issue below then stays ahead of the tensor pipe.
-        const uint32_t it = it0 + t, st = it % kKvStages, kv = base + st * kKvBytes, k = kKPerTile * it;
-        ok = wait(sm, sm.s_empty, (it & 1u) ^ 1u, p.err) && wait(sm, sm.kv_full[st], (it / kKvStages) & 1u, p.err);
-#pragma unroll 1
-        for (uint32_t j = 0; j < kKPerTile && ok; ++j)
-          ok = wait(sm, sm.k_full[(k + j) % kKSlots], ((k + j) / kKSlots) & 1u, p.err);
+        const uint32_t it = it0 + t, xb = it % kXBufs, yb = it % kYBufs, rb = it % kRopeBufs;
+        ok = wait_both(sm, sm.s_empty, (it & 1u) ^ 1u, p.err) && wait_both(sm, sm.x_full[xb], (it / kXBufs) & 1u, p.err) &&
+             wait_both(sm, sm.rope_full[rb], (it / kRopeBufs) & 1u, p.err);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t x = base + xb * kRegion, y = base + kYOff + yb * kRegion;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) slab_ts(tS, tQ + 32 * j, x + j * kSlabBytes, j == 0);
+        slab_ss(tS, base + kQOff + 2 * kSlabBytes, base + kRopeOff + rb * kSlabBytes, idesc_bf16_f32(kRows, kTile, 0, 0));
+        mma_commit_pair(smem_u32(&sm.rope_empty[rb]), kBoth);
+        ok = wait_both(sm, sm.y_full[yb], (it / kYBufs) & 1u, p.err);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) slab_ts(tS, tQ + 32 * j, kv + j * kSlabBytes, j == 0);
+        for (int j = 0; j < 2; ++j) slab_ts(tS, tQ + 128 + 32 * j, y + j * kSlabBytes, false);
 #pragma unroll
-        for (int j = 0; j < kKPerTile; ++j) {
-          const uint32_t slot = (k + j) % kKSlots, keys = base + kKOff + slot * kSlabBytes;
-          if (j == 0)
-            slab_ss(tS, base + kQOff + 2 * kQSlabBytes, keys, idesc_bf16_f32(kRows, kTile, 0, 0));
-          else if (j < 3)
-            slab_ts(tS, tQ + 96 + 32 * j, keys, false);
-          else
-            slab_ss(tS, base + kQOff + (j - 3) * kQSlabBytes, keys, idesc_f16_f32(kRows, kTile, 0, 0));
-          mma_commit(smem_u32(&sm.k_empty[slot]));
-        }
-        mma_commit(smem_u32(&sm.s_full));
+        for (int j = 2; j < 4; ++j)
+          slab_ss(tS, base + kQOff + (j - 2) * kSlabBytes, y + j * kSlabBytes, idesc_f16_f32(kRows, kTile, 0, 0));
+        mma_commit_pair(smem_u32(&sm.s_full), kBoth);
       }
       if (t > 0) {
-        const uint32_t it = it0 + t - 1, st = it % kKvStages, kv = base + st * kKvBytes;
-        ok = wait(sm, sm.p_full, it & 1u, p.err);
+        const uint32_t it = it0 + t - 1, xb = it % kXBufs, yb = it % kYBufs;
+        ok = wait_both(sm, sm.v_full[it & 1u], (it >> 1) & 1u, p.err) && wait_both(sm, sm.p_full, it & 1u, p.err);
         if (!ok) break;
         tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_ss(tmem + kColO, step_desc(base + kPOff, k), step_desc(kv + 2048 * k, 0, kSlabBytes),
-                 idesc_f16_f32(kRows, 256, 0, 1), t > 1 || k > 0 ? 1u : 0u);
-        mma_commit(smem_u32(&sm.kv_empty[st]));
-        mma_commit(smem_u32(&sm.pv_done));
+        values(tO, base + kPOff + kSlabBytes, base + kYOff + yb * kRegion, t == 1);
+        mma_commit_pair(smem_u32(&sm.y_empty[yb]), kBoth);
+        values(tO, base + kPOff, base + xb * kRegion, false);
+        mma_commit_pair(smem_u32(&sm.x_empty[xb]), kBoth);
+        mma_commit_pair(smem_u32(&sm.pv_done), kBoth);
       }
     }
   }
   return __all_sync(0xffffffffu, ok);
 }
 
-// Four warps, one query row per thread: probabilities, and the piece's result.
+// Four warps, 64 keys of a query row per thread: probabilities, and the piece's result.
 __device__ __noinline__ bool softmax_role(const Params& p, Smem& sm, Work w) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = threadIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tl = threadIdx.x, r = tl & (kMyRows - 1), half = tl >> 6, pairing = warp & 1;  // TMEM lane, row, keys
   const uint32_t base = w.base, n = w.n, it0 = w.it0;
-  const int b = w.b, g = w.g, len = w.len, hf = w.hf, rows = min(p.R - kRows * g, kRows);
+  const int b = w.b, g = w.g, len = w.len;
+  const int row = kMyRows * w.rank + r, rows = min(p.R - kRows * g, kRows);  // row of the group, rows that it has
   const uint32_t lanes = (uint32_t)(32 * warp) << 16;
   const uint32_t tS = w.tmem + lanes + kColS, tO = w.tmem + lanes + kColO;
-  const uint32_t p_row = base + kPOff + r * 128;
-  const float sl = sm.row_scale[r];
+  const uint32_t p_row = base + kPOff + half * kSlabBytes + r * 128;
+  const float sl = sm.row_scale[tl];
   // keys that the row, and the group's first row, see
-  const int limit = len - p.T + (kRows * g + min(r, rows - 1)) / p.n_h + 1;
+  const int limit = len - p.T + (kRows * g + min(row, rows - 1)) / p.n_h + 1;
   const int all_see = len - p.T + (kRows * g) / p.n_h + 1;
   float ref = -INFINITY, l = 0.f;
   bool ok = true;
 #pragma unroll 1
   for (uint32_t t = 0; t < n && ok; ++t) {
     const uint32_t it = it0 + t;
-    const int k0 = (w.begin + (int)t) * kTile;
+    const int k0 = (w.begin + (int)t) * kTile + kKeys * half;
     ok = wait_warp(sm, sm.s_full, it & 1u, p.err);
     if (!ok) break;
     tc_fence_after();
@@ -536,8 +570,8 @@ __device__ __noinline__ bool softmax_role(const Params& p, Smem& sm, Work w) {
     tmem_ld_wait();
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&sm.s_empty));
-    if (k0 + kTile > all_see) {
+    if (lane == 0) arrive_even(sm.s_empty, w.rank);
+    if (k0 + kKeys > all_see) {
 #pragma unroll
       for (int i = 0; i < 64; ++i)
         if (k0 + i >= limit) s[i >> 5][i & 31] = 0xff800000u;  // -inf
@@ -545,7 +579,13 @@ __device__ __noinline__ bool softmax_role(const Params& p, Smem& sm, Work w) {
     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
     for (int i = 0; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i >> 5][i & 31]));
-    const float z = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
+    float z = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
+    sm.row_max[it & 1u][tl] = z;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sm.ref_bar[pairing]));
+    ok = wait_warp(sm, sm.ref_bar[pairing], it & 1u, p.err);
+    if (!ok) break;
+    z = fmaxf(z, sm.row_max[it & 1u][tl ^ kMyRows]);
     float f = 1.f;
     const bool raise = z > ref + kRescale;  // ref = -inf: any finite maximum
     if (raise) {
@@ -555,7 +595,7 @@ __device__ __noinline__ bool softmax_role(const Params& p, Smem& sm, Work w) {
     }
     const float neg = ref == -INFINITY ? 0.f : -ref;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    auto half = [&](int k) {  // probabilities of 32 keys, as fp16 pairs in the first 16 words
+    auto exps = [&](int k) {  // probabilities of 32 keys, as fp16 pairs in the first 16 words
 #pragma unroll
       for (int i = 0; i < 32; i += 2) {
         const float a = ex2f_approx(fmaf(__uint_as_float(s[k][i]), sl, neg));
@@ -571,7 +611,7 @@ __device__ __noinline__ bool softmax_role(const Params& p, Smem& sm, Work w) {
         st_shared_v4_b32(p_row + (((4 * k + c) ^ (r & 7)) << 4), s[k][4 * c], s[k][4 * c + 1], s[k][4 * c + 2],
                          s[k][4 * c + 3]);
     };
-    half(0);
+    exps(0);
     if (t > 0) {  // the last tile's probabilities are used up, its context complete
       ok = wait_warp(sm, sm.pv_done, (it - 1) & 1u, p.err);
       if (!ok) break;
@@ -591,23 +631,32 @@ __device__ __noinline__ bool softmax_role(const Params& p, Smem& sm, Work w) {
       }
     }
     store(0);
-    half(1);
+    exps(1);
     store(1);
     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&sm.p_full));
+    if (lane == 0) arrive_even(sm.p_full, w.rank);
+  }
+  if (ok) {  // the row's sum (of the exchange buffers the last tile used the other one)
+    float* other = sm.row_max[(it0 + n) & 1u];
+    other[tl] = l;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sm.sum_bar[pairing]));
+    ok = wait_warp(sm, sm.sum_bar[pairing], w.index & 1u, p.err);
+    l = half == 0 ? l + other[tl ^ kMyRows] : other[tl ^ kMyRows] + l;
   }
   if (ok) ok = wait_warp(sm, sm.pv_done, (it0 + n - 1) & 1u, p.err);
   if (ok) {
     // -------------------------------------------------------------- the piece's result
-    // through the idle key buffers, 16-byte chunks rotated by the row so that neither the row-wise
-    // writes nor the copies out conflict
+    // The thread has the row's features [256 half, 256 half + 256).  They go through the idle regions, 16-byte
+    // chunks rotated by the lane so that neither the row-wise writes nor the copies out conflict.
     tc_fence_after();
-    const uint32_t out_row = (uint32_t)b * p.R + kRows * g;  // first query row of the group
+    const int64_t out_row = (int64_t)b * p.R + kRows * g + kMyRows * w.rank;  // the CTA's first query row
+    const int first = 32 * (warp & 1), mine = min(32, rows - kMyRows * w.rank - first);  // the warp's rows of it
     if (w.pieces == 1) {
       const float inv = (l == 0.f ? 0.f : 1.f / l) * p.kv.latent_scale;
-      const uint32_t dst = base + r * 512;
+      const uint32_t dst = base + tl * 512;
 #pragma unroll 1
       for (int c = 0; c < 256; c += 32) {
         uint32_t o[32];
@@ -619,18 +668,20 @@ __device__ __noinline__ bool softmax_role(const Params& p, Smem& sm, Work w) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             v[e] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
-          st_shared_v4_b32(dst + (((c / 8 + i + r) & 31) << 4), v[0], v[1], v[2], v[3]);
+          st_shared_v4_b32(dst + (((c / 8 + i + tl) & 31) << 4), v[0], v[1], v[2], v[3]);
         }
       }
       __syncwarp();
-      for (int k = 32 * warp; k < min(32 * warp + 32, rows); ++k) {
-        const uint4 v = ld_shared_v4_b32(base + k * 512 + (((lane + k) & 31) << 4));
-        reinterpret_cast<uint4*>(p.ctx + (int64_t)(out_row + k) * kDC + 256 * hf)[lane] = v;
+#pragma unroll 4
+      for (int k = 0; k < mine; ++k) {
+        const int at = 32 * warp + k;
+        reinterpret_cast<uint4*>(p.ctx + (out_row + first + k) * kDC + 256 * half)[lane] =
+            ld_shared_v4_b32(base + at * 512 + (((lane + at) & 31) << 4));
       }
-      if (hf == 0 && r < rows && p.lse != nullptr)
+      if (half == 0 && row < rows && p.lse != nullptr)
         p.lse[out_row + r] = l == 0.f ? -INFINITY : ref * kLn2 + logf(l);
     } else {
-      const uint32_t dst = base + r * 1024;
+      const uint32_t dst = base + tl * 1024;
 #pragma unroll 1
       for (int c = 0; c < 256; c += 32) {
         uint32_t o[32];
@@ -638,55 +689,65 @@ __device__ __noinline__ bool softmax_role(const Params& p, Smem& sm, Work w) {
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          st_shared_v4_b32(dst + (((c / 4 + i + r) & 63) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          st_shared_v4_b32(dst + (((c / 4 + i + row) & 63) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
       }
       fence_proxy_async_smem();
       __syncwarp();
-      const int64_t part = 2 * (int64_t)w.slot + hf;
-      const int mine = min(32, rows - 32 * warp);
       if (lane == 0 && mine > 0) {
-        bulk_store_s2g(p.ws_o + (part * min(p.R, kRows) + 32 * warp) * 256, base + 32 * warp * 1024, mine * 1024);
+        const int64_t part = (2 * (int64_t)w.slot + half) * min(p.R, kRows) + kMyRows * w.rank + first;
+        bulk_store_s2g(p.ws_o + part * 256, base + 32 * warp * 1024, mine * 1024);
         bulk_group_commit();
         bulk_group_wait_read_all();
       }
-      if (r < rows) p.ws_ml[part * kRows + r] = make_float2(ref, l);
+      if (half == 0 && row < rows) p.ws_ml[(int64_t)w.slot * kRows + row] = make_float2(ref, l);
     }
-    if (threadIdx.x == 0 && hf == 0 && w.begin == 0) p.table[w.b * p.groups + w.g] = make_int4(w.slot, w.c0, w.pieces, 0);
+    if (threadIdx.x == 0 && w.rank == 0 && w.begin == 0) p.table[w.b * p.groups + w.g] = make_int4(w.slot, w.c0, w.pieces, 0);
     tc_fence_before();
     fence_proxy_async_smem();
   }
   return ok;
 }
 
-// One warp: its latent slab of every tile, loaded one tile ahead (from L2: the rotary warp prefetches).
+// One warp: a latent slab of the CTA's keys in every tile, loaded one tile ahead (from L2: another warp prefetches).
+// Warps of the region that holds the other half's features also replace their slab by values of the other CTA's
+// keys once its scores are done.
 __device__ __noinline__ bool latent_role(const Params& p, Smem& sm, Work w) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool own = warp < kKWarp0;  // a slab of this CTA's half
-  const int j = own ? warp - kKvWarp0 : warp - kKWarp0;
-  PartSource src = part_source(p, w.b, w.begin, 4 * (own ? w.hf : 1 - w.hf) + j, lane);
-  int left = w.len - w.begin * kTile - (lane >> 1);
-  Part k;
+  const int region = warp >= kYWarp0 ? 1 : 0, j = warp - (region ? kYWarp0 : kXWarp0);
+  const bool does_values = region != w.rank;
+  const int keys = w.begin * kTile + kKeys * w.rank, others = w.begin * kTile + kKeys * (1 - w.rank);
+  PartSource src = part_source(p, w.b, keys, 4 * region + j, lane);
+  PartSource vsrc = part_source(p, w.b, others, 4 * w.rank + j, lane);
+  int left = w.len - keys - (lane >> 1), vleft = does_values ? w.len - others - (lane >> 1) : 0;
+  Part k, v;
   load_part(src, left, k);
+  load_part(vsrc, vleft, v);
 #pragma unroll 1
   for (uint32_t t = 0; t < w.n; ++t) {
-    const uint32_t it = w.it0 + t, q = kKPerTile * it + 1 + j;
-    const uint32_t slot = own ? it % kKvStages : q % kKSlots, use = own ? it / kKvStages : q / kKSlots;
-    if (!wait_warp(sm, own ? sm.kv_empty[slot] : sm.k_empty[slot], (use & 1u) ^ 1u, p.err)) return false;
-    store_part(k, w.base + (own ? slot * kKvBytes + j * kSlabBytes : kKOff + slot * kSlabBytes), lane);
-    if (lane == 0) mbar_arrive(smem_u32(own ? &sm.kv_full[slot] : &sm.k_full[slot]));
-    if (warp == kKvWarp0 && lane == 0) *const_cast<volatile int*>(&sm.progress) = (int)t;
+    const uint32_t it = w.it0 + t, bufs = region ? kYBufs : kXBufs, buf = it % bufs, use = it / bufs;
+    const uint32_t slab = w.base + (region ? kYOff : 0) + buf * kRegion + j * kSlabBytes;
+    if (!wait_warp(sm, region ? sm.y_empty[buf] : sm.x_empty[buf], (use & 1u) ^ 1u, p.err)) return false;
+    store_part(k, slab, lane);
+    if (lane == 0) arrive_even(region ? sm.y_full[buf] : sm.x_full[buf], w.rank);
+    if (warp == kXWarp0 && lane == 0) *const_cast<volatile int*>(&sm.progress) = (int)t;
     left -= kTile;
     load_part(src, left, k);
+    if (!does_values) continue;
+    if (!wait_warp(sm, sm.s_full, it & 1u, p.err)) return false;
+    store_part(v, slab, lane);
+    if (lane == 0) arrive_even(sm.v_full[it & 1u], w.rank);
+    vleft -= kTile;
+    load_part(vsrc, vleft, v);
   }
   return true;
 }
 
 __device__ __forceinline__ void prefetch_l2(const void* a) { asm volatile("prefetch.global.L2 [%0];" ::"l"(a)); }
-// One warp: the cached rows of a tile into L2.
-__device__ __forceinline__ void prefetch_tile(const Params& p, int b, int tile, int len, int lane) {
+// One warp: 64 cached rows into L2.
+__device__ __forceinline__ void prefetch_rows(const Params& p, int b, int first, int len, int lane) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int64_t t = (int64_t)tile * kTile + 32 * i + lane;
+    const int64_t t = (int64_t)first + 32 * i + lane;
     if (t >= len) return;
     const uint8_t* c = p.kv.c4 + b * p.kv.c4_b + t * p.kv.c4_r;
     prefetch_l2(c);
@@ -704,59 +765,64 @@ __device__ __noinline__ void prefetch_role(const Params& p, Smem& sm, Work w) {
 #pragma unroll 1
   for (int t = kPrefetch; t < (int)w.n; ++t) {
     while (*progress + kPrefetch < t && !*abort) __nanosleep(100);  // the decode warps' waits are bounded
-    prefetch_tile(p, w.b, w.begin + t, w.len, lane);
+    prefetch_rows(p, w.b, (w.begin + t) * kTile + kKeys * w.rank, w.len, lane);
   }
 }
 
 // One warp: the rotary slab of every tile.
 __device__ __noinline__ bool rope_role(const Params& p, Smem& sm, Work w) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, keys = w.begin * kTile + kKeys * w.rank;
   const uint8_t* src = reinterpret_cast<const uint8_t*>(static_cast<const __nv_bfloat16*>(p.kv.k_r) + w.b * p.kv.kr_b +
-                                                        ((int64_t)w.begin * kTile + (lane >> 1)) * p.kv.kr_r) + 64 * (lane & 1);
-  int left = w.len - w.begin * kTile - (lane >> 1);
+                                                        ((int64_t)keys + (lane >> 1)) * p.kv.kr_r) + 64 * (lane & 1);
+  int left = w.len - keys - (lane >> 1);
   uint4 k[16];
   load_rope(src, 32 * p.kv.kr_r, left, k);
 #pragma unroll 1
   for (uint32_t t = 0; t < w.n; ++t) {
-    const uint32_t q = kKPerTile * (w.it0 + t), slot = q % kKSlots;
-    if (!wait_warp(sm, sm.k_empty[slot], ((q / kKSlots) & 1u) ^ 1u, p.err)) return false;
-    store_rope(k, w.base + kKOff + slot * kSlabBytes, lane);
-    if (lane == 0) mbar_arrive(smem_u32(&sm.k_full[slot]));
+    const uint32_t it = w.it0 + t, buf = it % kRopeBufs;
+    if (!wait_warp(sm, sm.rope_empty[buf], ((it / kRopeBufs) & 1u) ^ 1u, p.err)) return false;
+    store_rope(k, w.base + kRopeOff + buf * kSlabBytes, lane);
+    if (lane == 0) arrive_even(sm.rope_full[buf], w.rank);
     left -= kTile;
     load_rope(src, 32 * p.kv.kr_r, left, k);
   }
   return true;
 }
 
-__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ Params p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ Params p) {
   uint8_t* smem = shared_base();
   Smem& sm = *reinterpret_cast<Smem*>(smem + kSmemOff);
   const uint32_t base = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int pair = blockIdx.x >> 1, hf = blockIdx.x & 1;
+  const int pair = blockIdx.x >> 1, rank = (int)cluster_ctarank();
 
   griddep_launch_dependents();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kKvStages; ++s) {
-      mbar_init(smem_u32(&sm.kv_full[s]), 4);
-      mbar_init(smem_u32(&sm.kv_empty[s]), 1);
+    for (int i = 0; i < kXBufs; ++i) {
+      mbar_init(smem_u32(&sm.x_full[i]), 8);
+      mbar_init(smem_u32(&sm.x_empty[i]), 1);
     }
-    for (int s = 0; s < kKSlots; ++s) {
-      mbar_init(smem_u32(&sm.k_full[s]), 1);
-      mbar_init(smem_u32(&sm.k_empty[s]), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sm.y_full[i]), 8);
+      mbar_init(smem_u32(&sm.y_empty[i]), 1);
+      mbar_init(smem_u32(&sm.rope_full[i]), 2);
+      mbar_init(smem_u32(&sm.rope_empty[i]), 1);
+      mbar_init(smem_u32(&sm.v_full[i]), 8);
+      mbar_init(smem_u32(&sm.ref_bar[i]), 2);
+      mbar_init(smem_u32(&sm.sum_bar[i]), 2);
     }
-    mbar_init(smem_u32(&sm.q_full), 1);
+    mbar_init(smem_u32(&sm.s_empty), 8);
+    mbar_init(smem_u32(&sm.p_full), 8);
     mbar_init(smem_u32(&sm.s_full), 1);
-    mbar_init(smem_u32(&sm.s_empty), 4);
-    mbar_init(smem_u32(&sm.p_full), 4);
     mbar_init(smem_u32(&sm.pv_done), 1);
     mbar_init(smem_u32(&sm.drain), 1);
+    mbar_init(smem_u32(&sm.q_full), 1);
     sm.abort = sm.never = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
-    tmem_alloc(smem_u32(&sm.tmem_base), kTmemCols);
-    tmem_relinquish();
+    tmem_alloc_pair(smem_u32(&sm.tmem_base), kTmemCols);
+    tmem_relinquish_pair();
   }
   griddep_wait();
   if (warp == 0) {
@@ -769,11 +835,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
 
-  // it0: tiles of the earlier pieces.  All warps take every barrier of every piece, also after a failed wait.
+  // it0: tiles of the earlier pieces.  Both CTAs walk the same pieces, and all warps take every barrier of every
+  // piece, also after a failed wait.
   uint32_t it0 = 0, pieces = 0;
   bool dead = false;
-  while (true) {
-    if (sm.piece.item < 0) break;
+  while (sm.piece.item >= 0) {
     Work w;
     w.base = base;
     w.tmem = tmem;
@@ -783,33 +849,39 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     w.b = sm.piece.item / p.groups;
     w.g = sm.piece.item % p.groups;
     w.len = p.lengths[w.b];
-    w.hf = hf;
+    w.rank = rank;
     w.slot = sm.piece.slot;
     w.c0 = sm.piece.c0;
     w.pieces = sm.piece.n;
+    w.index = (int)pieces;
     if (threadIdx.x == 0) {
       sm.progress = 0;
-      fetch_query(p, sm, base, w.b, w.g, hf);
+      fetch_query(p, sm, base, w.b, kRows * w.g + kMyRows * rank);
     }
     if (warp == kPrefetchWarp)
-      for (int t = 0; t < kPrefetch && t < (int)w.n; ++t) prefetch_tile(p, w.b, w.begin + t, w.len, lane);
+      for (int t = 0; t < kPrefetch && t < (int)w.n; ++t)
+        prefetch_rows(p, w.b, (w.begin + t) * kTile + kKeys * rank, w.len, lane);
     __syncwarp();
     // (all eight warps come here in every piece: they meet inside)
-    if (warp < 4 || (warp >= kKWarp0 && warp < kRopeWarp))
-      dead |= !place_query(p, sm, base, tmem, warp >= kKWarp0 ? 1 : 0, pieces & 1u);
+    if (warp < 4 || (warp >= kYWarp0 && warp < kRopeWarp))
+      dead |= !place_query(p, sm, base, tmem, warp >= kYWarp0 ? 1 : 0, pieces & 1u);
     ++pieces;
-    __syncthreads();
+    __syncwarp();
+    cluster_sync();  // the query is in place in both CTAs (in the first piece: and their barriers)
     tc_fence_after();
     if (sm.abort) dead = true;
     if (!dead) {
       bool ok = true;
       if (warp < 4)
         ok = softmax_role(p, sm, w);
-      else if (warp > kMmaWarp)
-        ok = warp < kRopeWarp ? latent_role(p, sm, w) : warp > kRopeWarp || rope_role(p, sm, w);
+      else if (warp == kMmaWarp)
+        ok = rank != 0 || mma_role(p, it0, w.n);
+      else if (warp < kRopeWarp)
+        ok = latent_role(p, sm, w);
+      else if (warp == kRopeWarp)
+        ok = rope_role(p, sm, w);
       else
-        ok = mma_role(p, it0, w.n);
-      if (warp == kPrefetchWarp) prefetch_role(p, sm, w);
+        prefetch_role(p, sm, w);
       dead = !ok;
     }
     __syncwarp();
@@ -819,19 +891,19 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     tc_fence_after();
     if (sm.abort) dead = true;
   }
-  if (warp == kMmaWarp) {
-    if (lane == 0) {
-      mma_commit(smem_u32(&sm.drain));
-      mbar_wait(smem_u32(&sm.drain), 0, &sm.never, kWaitLimitNs);
-    }
-    __syncwarp();
-  }
   if (threadIdx.x == 0 && sm.abort && pieces > 0)  // a query still on its way lands before the block leaves
     mbar_wait(smem_u32(&sm.q_full), (pieces - 1) & 1u, &sm.never, kWaitLimitNs);
+  __syncwarp();
+  if (warp == kMmaWarp && pieces > 0) {
+    if (rank == 0 && elect_one()) mma_commit_pair(smem_u32(&sm.drain), 3);
+    __syncwarp();
+    mbar_wait(smem_u32(&sm.drain), 0, &sm.never, kWaitLimitNs);
+    __syncwarp();
+  }
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();  // neither CTA leaves while the other may still arrive on its barriers or read its shared memory
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+  if (warp == kMmaWarp) tmem_dealloc_pair(tmem, kTmemCols);
 }
 
 // Joins the partials of items that were cut: one warp per query row and latent half, in slot order.  Rows of
@@ -857,14 +929,14 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Param
   const int stride = min(p.R, kRows);
   auto part = [&](int k) { return 2 * (int64_t)(k == 0 ? e.x : 2 * (e.y + k)) + hf; };
   float M = -INFINITY;
-  for (int k = lane; k < e.z; k += 32) M = fmaxf(M, p.ws_ml[part(k) * kRows + i].x);
+  for (int k = lane; k < e.z; k += 32) M = fmaxf(M, p.ws_ml[(part(k) >> 1) * kRows + i].x);
   M = warp_max(M);
   const float ref = M == -INFINITY ? 0.f : M;
   float L = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   // lane l holds features 8 l .. 8 l + 7: chunks 2 l and 2 l + 1 of the rotated row
 #pragma unroll 4
   for (int k = 0; k < e.z; ++k) {
-    const float2 ml = p.ws_ml[part(k) * kRows + i];
+    const float2 ml = p.ws_ml[(part(k) >> 1) * kRows + i];
     const float4* src = reinterpret_cast<const float4*>(p.ws_o + (part(k) * stride + i) * 256);
     const float4 a = src[(2 * lane + i) & 63], c = src[(2 * lane + 1 + i) & 63];
     if (ml.y == 0.f) continue;  // the row saw none of this piece's keys
@@ -883,7 +955,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Param
 bool query_map(CUtensorMap* m, const void* base, int width, int R, int B, int64_t ld) {
   const uint64_t dims[3] = {(uint64_t)width, (uint64_t)R, (uint64_t)B};
   const uint64_t strides[2] = {(uint64_t)ld * 2, (uint64_t)ld * 2 * R};
-  const uint32_t box[3] = {64, kRows, 1};
+  const uint32_t box[3] = {64, kMyRows, 1};
   return make_tensor_map_bf16(m, base, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 int max_pairs() {
@@ -893,19 +965,35 @@ int max_pairs() {
   return sms > 1 ? sms / 2 : 1;
 }
 // Pairs that this shape can keep busy at most
-int shape_pairs(int n_h, int B, int T, int n_max) {
+int shape_pairs(int pairs, int n_h, int B, int T, int n_max) {
   const int64_t groups = ((int64_t)n_h * T + kRows - 1) / kRows, tiles = groups * B * ((n_max + kTile - 1) / kTile);
-  const int pairs = max_pairs();
   return (int)(tiles < pairs ? tiles : pairs);
 }
+// Pairs that are resident at once (a GPC with an odd number of SMs leaves one over): one wave.  Per device.
+int resident_pairs() {
+  static int cache[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && cache[dev] > 0) return cache[dev];
+  int pairs = max_pairs(), active = 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  if (cudaOccupancyMaxActiveClusters(&active, decode_kernel, &cfg) == cudaSuccess && active > 0 && active < pairs)
+    pairs = active;
+  cudaGetLastError();  // a failed query leaves no sticky state
+  if (dev >= 0 && dev < 64) cache[dev] = pairs;
+  return pairs;
+}
 size_t table_bytes(int n_h, int B, int T) { return (size_t)B * (((size_t)n_h * T + kRows - 1) / kRows) * sizeof(int4); }
-size_t ml_bytes(int pairs) { return (size_t)pairs * 2 * 2 * kRows * sizeof(float2); }
+size_t ml_bytes(int pairs) { return (size_t)pairs * 2 * kRows * sizeof(float2); }
 
 }  // namespace decode_fp4
 
 size_t decode_fp4_tc_workspace(int n_h, int B, int T, int n_max) {
   using namespace decode_fp4;
-  const int pairs = shape_pairs(n_h, B, T, n_max), R = n_h * T;
+  const int pairs = shape_pairs(max_pairs(), n_h, B, T, n_max), R = n_h * T;
   return table_bytes(n_h, B, T) + ml_bytes(pairs) + (size_t)pairs * 2 * 2 * (R < kRows ? R : kRows) * 256 * sizeof(float);
 }
 
@@ -919,7 +1007,9 @@ cudaError_t decode_fp4_tc_launch(const Fp4DecodeArgs& a, void* ws, cudaStream_t 
   p.groups = (p.R + kRows - 1) / kRows;
   if (!query_map(&p.tm_q, a.q_tilde, kDC, p.R, a.B, a.ldqt) || !query_map(&p.tm_qp, a.q_pe, kDR, p.R, a.B, a.ldqp))
     return cudaErrorInvalidValue;
-  p.pairs = shape_pairs(a.n_h, a.B, a.T, a.n_max);
+  cudaError_t e = cudaFuncSetAttribute(decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  p.pairs = shape_pairs(resident_pairs(), a.n_h, a.B, a.T, a.n_max);
   p.scale_log2 = a.scale * kLog2e;
   p.ctx = static_cast<__nv_bfloat16*>(a.ctx);
   p.lse = a.lse;
@@ -930,8 +1020,6 @@ cudaError_t decode_fp4_tc_launch(const Fp4DecodeArgs& a, void* ws, cudaStream_t 
   w += ml_bytes(p.pairs);
   p.ws_o = reinterpret_cast<float*>(w);
   p.err = a.err;
-  cudaError_t e = cudaFuncSetAttribute(decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  if (e != cudaSuccess) return e;
   e = launch_pdl(decode_kernel, dim3(2 * p.pairs), dim3(kThreads), kSmemBytes, st, p);
   if (e != cudaSuccess) return e;
   const int64_t warps = (int64_t)p.B * p.R * 2;
