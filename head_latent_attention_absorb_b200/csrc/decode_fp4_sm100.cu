@@ -31,8 +31,8 @@
 // * MMA order S(t + 1), O(t), S(t + 2), ...: the softmax of tile t runs under S(t + 1), and the tensor pipe
 //   works on O(t - 1) while S(t) is read from TMEM.  The scores start with X, whose third buffer is decoded ahead,
 //   while Y's are decoded behind O.
-// * Four softmax warps: a thread has 64 keys of a query row and agrees with the thread that has the row's other
-//   64 on the reference of the base-2 exponentials, which moves (and the context is rescaled in TMEM) only when the
+// * Eight softmax warps: a thread has 32 keys of a query row and agrees with the three threads that have the row's
+//   others on the reference of the base-2 exponentials, which moves (and the context is rescaled in TMEM) only when the
 //   running maximum grows by more than 8.
 // * Work: chunks of single sequences when each can have pairs of its own and the chunks come out balanced, else
 //   equal ranges of all tiles.  A sequence that is cut leaves fp32 partials and a second kernel joins them in a
@@ -67,8 +67,8 @@ constexpr int kPOff = kQOff + 3 * kSlabBytes;    // probabilities of the first a
 constexpr int kSmemOff = kPOff + 2 * kSlabBytes;
 static_assert(kQTmemSlabs * kSlabBytes <= kYOff, "the query is staged in region X");
 static_assert(kMyRows * kDC * 4 <= kRopeOff, "the partial context is staged in the regions");
-constexpr int kMmaWarp = 4, kXWarp0 = 5, kYWarp0 = 9, kRopeWarp = 13, kPrefetchWarp = 14;
-constexpr int kThreads = 32 * 15;
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kXWarp0 = 9, kYWarp0 = 13, kRopeWarp = 17, kPrefetchWarp = 18;
+constexpr int kThreads = 32 * 19;
 constexpr uint32_t kTmemCols = 512, kColO = 0, kColS = 256, kColQ = 320;
 // Probabilities are 2^(z - ref): ref is set kRaise below the largest score so far (log2 units) and moved up
 // only when a score passes it by kRescale.  So they reach 2^15 at most (fp16 ends at 2^16), the sum is at
@@ -91,7 +91,7 @@ struct Params {
   float* lse;
   int4* table;    // [B * groups] partials of an item: first slot, first CTA pair, number
   float2* ws_ml;  // [2 pairs slots][128] (reference in log2 units, sum)
-  float* ws_o;    // [slots][2 halves][min(R, 128)][256], 16-byte chunk j of row r at (j + r) % 64
+  float* ws_o;    // [slots][4 quarters of the features][min(R, 128)][128], 16-byte chunk j of row r at (j + r) % 32
   int32_t* err;
 };
 
@@ -116,13 +116,14 @@ struct Piece {
 };
 
 struct Smem {
-  // waited for in the even CTA only; arrivals from both CTAs
+  // Waited for in the even CTA only; arrivals from both CTAs.  (The waiting thread reads nothing that they
+  // guard, it issues MMAs; an acquire at cluster scope would cost it some hundred cycles a wait.)
   uint64_t x_full[kXBufs], y_full[kYBufs], rope_full[kRopeBufs], v_full[2], s_empty, p_full;
   // in each CTA; arrivals from the MMAs
-  uint64_t x_empty[kXBufs], y_empty[kYBufs], rope_empty[kRopeBufs], s_full, pv_done, drain;
-  uint64_t q_full, ref_bar[2], sum_bar[2];
+  uint64_t x_empty[kXBufs], y_empty[kYBufs], rope_empty[kRopeBufs], s_full[2], pv_done, drain;
+  uint64_t q_full;
   alignas(16) float row_scale[kRows];  // by TMEM lane: softmax scale of the query row, log2 units
-  float row_max[2][kRows];             // by TMEM lane: exchange between the threads of a row
+  float share[2][4][kMyRows];          // exchange between the four threads of a row
   Plan plan;
   Piece piece;
   uint32_t tmem_base;
@@ -137,18 +138,15 @@ __device__ __forceinline__ uint8_t* shared_base() {
 }
 
 // Bounded wait that records its own expiry; what follows a first failed try is one shared function, since the
-// roles' loops together have to fit the instruction cache.  `cluster`: the arrivals come from both CTAs.
-__device__ __noinline__ bool wait_more(Smem& sm, uint32_t bar, uint32_t parity, bool cluster, int32_t* err) {
-  if (mbar_wait(bar, parity, &sm.abort, kWaitLimitNs, cluster)) return true;
+// roles' loops together have to fit the instruction cache.
+__device__ __noinline__ bool wait_more(Smem& sm, uint32_t bar, uint32_t parity, int32_t* err) {
+  if (mbar_wait(bar, parity, &sm.abort, kWaitLimitNs)) return true;
   raise_error(err, MLA_ERR_TIMEOUT);
   sm.abort = 1;
   return false;
 }
 __device__ __forceinline__ bool wait(Smem& sm, uint64_t& bar, uint32_t parity, int32_t* err) {
-  return mbar_try_wait(smem_u32(&bar), parity) || wait_more(sm, smem_u32(&bar), parity, false, err);
-}
-__device__ __forceinline__ bool wait_both(Smem& sm, uint64_t& bar, uint32_t parity, int32_t* err) {
-  return mbar_try_wait_cluster(smem_u32(&bar), parity) || wait_more(sm, smem_u32(&bar), parity, true, err);
+  return mbar_try_wait(smem_u32(&bar), parity) || wait_more(sm, smem_u32(&bar), parity, err);
 }
 // All lanes wait; the warp goes on only if all of them saw the phase complete.
 __device__ __forceinline__ bool wait_warp(Smem& sm, uint64_t& bar, uint32_t parity, int32_t* err) {
@@ -399,7 +397,7 @@ __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// The query rows in place, by the softmax warps (h = 0: slabs 0..3) and warps kYWarp0.. (h = 1: slabs 4..7 and the
+// The query rows in place, by the softmax warps (the first four, h = 0: slabs 0..3, the others, h = 1: slabs 4..7 and the
 // rotary one), one row per thread and TMEM lane (lanes 64.. repeat the rows): the row's power of two, its latent
 // part to fp16 (in TMEM, or where it is), its rotary part scaled where it is.
 __device__ __noinline__ bool place_query(const Params& p, Smem& sm, uint32_t base, uint32_t tmem, int h, uint32_t parity) {
@@ -422,9 +420,9 @@ __device__ __noinline__ bool place_query(const Params& p, Smem& sm, uint32_t bas
     }
   }
   m = fmaxf(m, fmaxf(bf16_lo(big), bf16_hi(big)) * (h ? 1.f : ls));
-  sm.row_max[h][lane] = m;
+  sm.share[0][h][r] = m;
   named_bar_sync(1, 256);
-  m = fmaxf(m, sm.row_max[1 - h][lane]);
+  m = fmaxf(m, sm.share[0][1 - h][r]);
   // 2^e that puts the row's largest element into [2^14, 2^15)
   const int e = m > 0.f ? max(-126, min(126, 14 + 127 - (int)(__float_as_uint(m) >> 23))) : 0;
   const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
@@ -465,7 +463,6 @@ struct Work {
   int begin, b, g, len;
   int rank;
   int slot, c0, pieces;  // as in Piece
-  int index;             // pieces before this one
 };
 
 // A 128-byte-swizzled shared-memory descriptor whose address is at + 32 k: the low word counts 16 bytes.
@@ -506,8 +503,8 @@ __device__ __noinline__ bool mma_role(const Params& p, uint32_t it0, uint32_t n)
     for (uint32_t t = 0; t <= n; ++t) {
       if (t < n) {
         const uint32_t it = it0 + t, xb = it % kXBufs, yb = it % kYBufs, rb = it % kRopeBufs;
-        ok = wait_both(sm, sm.s_empty, (it & 1u) ^ 1u, p.err) && wait_both(sm, sm.x_full[xb], (it / kXBufs) & 1u, p.err) &&
-             wait_both(sm, sm.rope_full[rb], (it / kRopeBufs) & 1u, p.err);
+        ok = wait(sm, sm.s_empty, (it & 1u) ^ 1u, p.err) && wait(sm, sm.x_full[xb], (it / kXBufs) & 1u, p.err) &&
+             wait(sm, sm.rope_full[rb], (it / kRopeBufs) & 1u, p.err);
         if (!ok) break;
         tc_fence_after();
         const uint32_t x = base + xb * kRegion, y = base + kYOff + yb * kRegion;
@@ -515,7 +512,7 @@ __device__ __noinline__ bool mma_role(const Params& p, uint32_t it0, uint32_t n)
         for (int j = 0; j < 4; ++j) slab_ts(tS, tQ + 32 * j, x + j * kSlabBytes, j == 0);
         slab_ss(tS, base + kQOff + 2 * kSlabBytes, base + kRopeOff + rb * kSlabBytes, idesc_bf16_f32(kRows, kTile, 0, 0));
         mma_commit_pair(smem_u32(&sm.rope_empty[rb]), kBoth);
-        ok = wait_both(sm, sm.y_full[yb], (it / kYBufs) & 1u, p.err);
+        ok = wait(sm, sm.y_full[yb], (it / kYBufs) & 1u, p.err);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
@@ -523,11 +520,11 @@ __device__ __noinline__ bool mma_role(const Params& p, uint32_t it0, uint32_t n)
 #pragma unroll
         for (int j = 2; j < 4; ++j)
           slab_ss(tS, base + kQOff + (j - 2) * kSlabBytes, y + j * kSlabBytes, idesc_f16_f32(kRows, kTile, 0, 0));
-        mma_commit_pair(smem_u32(&sm.s_full), kBoth);
+        mma_commit_pair(smem_u32(&sm.s_full[it & 1u]), kBoth);
       }
       if (t > 0) {
         const uint32_t it = it0 + t - 1, xb = it % kXBufs, yb = it % kYBufs;
-        ok = wait_both(sm, sm.v_full[it & 1u], (it >> 1) & 1u, p.err) && wait_both(sm, sm.p_full, it & 1u, p.err);
+        ok = wait(sm, sm.v_full[it & 1u], (it >> 1) & 1u, p.err) && wait(sm, sm.p_full, it & 1u, p.err);
         if (!ok) break;
         tc_fence_after();
         values(tO, base + kPOff + kSlabBytes, base + kYOff + yb * kRegion, t == 1);
@@ -541,15 +538,16 @@ __device__ __noinline__ bool mma_role(const Params& p, uint32_t it0, uint32_t n)
   return __all_sync(0xffffffffu, ok);
 }
 
-// Four warps, 64 keys of a query row per thread: probabilities, and the piece's result.
+// Eight warps, 32 keys of a query row per thread: probabilities, and the piece's result.
 __device__ __noinline__ bool softmax_role(const Params& p, Smem& sm, Work w) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tl = threadIdx.x, r = tl & (kMyRows - 1), half = tl >> 6, pairing = warp & 1;  // TMEM lane, row, keys
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, col = warp >> 2;
+  const int tl = 32 * quad + lane, r = tl & (kMyRows - 1), half = tl >> 6;  // TMEM lane, row, half of the tile's keys
+  const int part = 2 * half + col;                                          // the row's quarter of keys and features
   const uint32_t base = w.base, n = w.n, it0 = w.it0;
   const int b = w.b, g = w.g, len = w.len;
   const int row = kMyRows * w.rank + r, rows = min(p.R - kRows * g, kRows);  // row of the group, rows that it has
-  const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-  const uint32_t tS = w.tmem + lanes + kColS, tO = w.tmem + lanes + kColO;
+  const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+  const uint32_t tS = w.tmem + lanes + kColS + 32 * col, tO = w.tmem + lanes + kColO + 128 * col;
   const uint32_t p_row = base + kPOff + half * kSlabBytes + r * 128;
   const float sl = sm.row_scale[tl];
   // keys that the row, and the group's first row, see
@@ -557,35 +555,39 @@ __device__ __noinline__ bool softmax_role(const Params& p, Smem& sm, Work w) {
   const int all_see = len - p.T + (kRows * g) / p.n_h + 1;
   float ref = -INFINITY, l = 0.f;
   bool ok = true;
+  // The four warps that have the same rows meet once a tile and once more at the end.  A warp whose wait failed
+  // still comes to all the meetings.
+  uint32_t met = 0;
+  auto meet = [&]() {
+    named_bar_sync(2 + (quad & 1), 128);
+    ++met;
+  };
 #pragma unroll 1
-  for (uint32_t t = 0; t < n && ok; ++t) {
+  for (uint32_t t = 0; t < n; ++t) {
     const uint32_t it = it0 + t;
-    const int k0 = (w.begin + (int)t) * kTile + kKeys * half;
-    ok = wait_warp(sm, sm.s_full, it & 1u, p.err);
+    const int k0 = (w.begin + (int)t) * kTile + 32 * part;
+    ok = wait_warp(sm, sm.s_full[it & 1u], (it >> 1) & 1u, p.err);
     if (!ok) break;
     tc_fence_after();
-    uint32_t s[2][32];
-    tmem_ld32(tS, s[0]);
-    tmem_ld32(tS + 32, s[1]);
+    uint32_t s[32];
+    tmem_ld32(tS, s);
     tmem_ld_wait();
     tc_fence_before();
     __syncwarp();
     if (lane == 0) arrive_even(sm.s_empty, w.rank);
-    if (k0 + kKeys > all_see) {
+    if (k0 + 32 > all_see) {
 #pragma unroll
-      for (int i = 0; i < 64; ++i)
-        if (k0 + i >= limit) s[i >> 5][i & 31] = 0xff800000u;  // -inf
+      for (int i = 0; i < 32; ++i)
+        if (k0 + i >= limit) s[i] = 0xff800000u;  // -inf
     }
     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int i = 0; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i >> 5][i & 31]));
-    float z = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
-    sm.row_max[it & 1u][tl] = z;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&sm.ref_bar[pairing]));
-    ok = wait_warp(sm, sm.ref_bar[pairing], it & 1u, p.err);
-    if (!ok) break;
-    z = fmaxf(z, sm.row_max[it & 1u][tl ^ kMyRows]);
+    for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
+    const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
+    float(&x)[4][kMyRows] = sm.share[it & 1u];
+    x[part][r] = mine;
+    meet();
+    const float z = fmaxf(fmaxf(x[0][r], x[1][r]), fmaxf(x[2][r], x[3][r]));
     float f = 1.f;
     const bool raise = z > ref + kRescale;  // ref = -inf: any finite maximum
     if (raise) {
@@ -595,30 +597,22 @@ __device__ __noinline__ bool softmax_role(const Params& p, Smem& sm, Work w) {
     }
     const float neg = ref == -INFINITY ? 0.f : -ref;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    auto exps = [&](int k) {  // probabilities of 32 keys, as fp16 pairs in the first 16 words
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        const float a = ex2f_approx(fmaf(__uint_as_float(s[k][i]), sl, neg));
-        const float c = ex2f_approx(fmaf(__uint_as_float(s[k][i + 1]), sl, neg));
-        sum[i & 2] += a;
-        sum[(i & 2) + 1] += c;
-        s[k][i / 2] = pack_f16x2_ieee(a, c);
-      }
-    };
-    auto store = [&](int k) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        st_shared_v4_b32(p_row + (((4 * k + c) ^ (r & 7)) << 4), s[k][4 * c], s[k][4 * c + 1], s[k][4 * c + 2],
-                         s[k][4 * c + 3]);
-    };
-    exps(0);
+    for (int i = 0; i < 32; i += 2) {  // fp16 pairs in the first 16 words
+      const float a = ex2f_approx(fmaf(__uint_as_float(s[i]), sl, neg));
+      const float c = ex2f_approx(fmaf(__uint_as_float(s[i + 1]), sl, neg));
+      sum[i & 2] += a;
+      sum[(i & 2) + 1] += c;
+      s[i / 2] = pack_f16x2_ieee(a, c);
+    }
+    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     if (t > 0) {  // the last tile's probabilities are used up, its context complete
       ok = wait_warp(sm, sm.pv_done, (it - 1) & 1u, p.err);
       if (!ok) break;
       if (__any_sync(0xffffffffu, raise)) {
         tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < 256; c += 32) {
+        for (int c = 0; c < 128; c += 32) {
           uint32_t o[32];
           tmem_ld32(tO + c, o);
           tmem_ld_wait();
@@ -630,76 +624,68 @@ __device__ __noinline__ bool softmax_role(const Params& p, Smem& sm, Work w) {
         tc_fence_before();
       }
     }
-    store(0);
-    exps(1);
-    store(1);
-    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      st_shared_v4_b32(p_row + (((4 * col + c) ^ (r & 7)) << 4), s[4 * c], s[4 * c + 1], s[4 * c + 2], s[4 * c + 3]);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) arrive_even(sm.p_full, w.rank);
   }
-  if (ok) {  // the row's sum (of the exchange buffers the last tile used the other one)
-    float* other = sm.row_max[(it0 + n) & 1u];
-    other[tl] = l;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&sm.sum_bar[pairing]));
-    ok = wait_warp(sm, sm.sum_bar[pairing], w.index & 1u, p.err);
-    l = half == 0 ? l + other[tl ^ kMyRows] : other[tl ^ kMyRows] + l;
+  if (ok) {  // the row's sum (the last tile used the other buffer)
+    float(&x)[4][kMyRows] = sm.share[(it0 + n) & 1u];
+    x[part][r] = l;
+    meet();
+    l = (x[0][r] + x[1][r]) + (x[2][r] + x[3][r]);
+    ok = wait_warp(sm, sm.pv_done, (it0 + n - 1) & 1u, p.err);
   }
-  if (ok) ok = wait_warp(sm, sm.pv_done, (it0 + n - 1) & 1u, p.err);
+  while (met <= n) meet();
   if (ok) {
     // -------------------------------------------------------------- the piece's result
-    // The thread has the row's features [256 half, 256 half + 256).  They go through the idle regions, 16-byte
-    // chunks rotated by the lane so that neither the row-wise writes nor the copies out conflict.
+    // The thread has the row's features [128 part, 128 part + 128).  They go through the idle regions, 16-byte
+    // chunks rotated by the row so that neither the row-wise writes nor the copies out conflict.
     tc_fence_after();
     const int64_t out_row = (int64_t)b * p.R + kRows * g + kMyRows * w.rank;  // the CTA's first query row
-    const int first = 32 * (warp & 1), mine = min(32, rows - kMyRows * w.rank - first);  // the warp's rows of it
-    if (w.pieces == 1) {
-      const float inv = (l == 0.f ? 0.f : 1.f / l) * p.kv.latent_scale;
-      const uint32_t dst = base + tl * 512;
+    const int first = 32 * (quad & 1), mine = min(32, rows - kMyRows * w.rank - first);  // the warp's rows of it
+    const bool whole = w.pieces == 1;
+    const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) * p.kv.latent_scale : 1.f;
+    const uint32_t src = base + warp * (32 * 512), dst = src + lane * 512;
 #pragma unroll 1
-      for (int c = 0; c < 256; c += 32) {
-        uint32_t o[32];
-        tmem_ld32(tO + c, o);
-        tmem_ld_wait();
+    for (int c = 0; c < 128; c += 32) {
+      uint32_t o[32];
+      tmem_ld32(tO + c, o);
+      tmem_ld_wait();
+      if (whole) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t v[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             v[e] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
-          st_shared_v4_b32(dst + (((c / 8 + i + tl) & 31) << 4), v[0], v[1], v[2], v[3]);
+          st_shared_v4_b32(dst + (((c / 8 + i + r) & 15) << 4), v[0], v[1], v[2], v[3]);
         }
-      }
-      __syncwarp();
-#pragma unroll 4
-      for (int k = 0; k < mine; ++k) {
-        const int at = 32 * warp + k;
-        reinterpret_cast<uint4*>(p.ctx + (out_row + first + k) * kDC + 256 * half)[lane] =
-            ld_shared_v4_b32(base + at * 512 + (((lane + at) & 31) << 4));
-      }
-      if (half == 0 && row < rows && p.lse != nullptr)
-        p.lse[out_row + r] = l == 0.f ? -INFINITY : ref * kLn2 + logf(l);
-    } else {
-      const uint32_t dst = base + tl * 1024;
-#pragma unroll 1
-      for (int c = 0; c < 256; c += 32) {
-        uint32_t o[32];
-        tmem_ld32(tO + c, o);
-        tmem_ld_wait();
+      } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          st_shared_v4_b32(dst + (((c / 4 + i + row) & 63) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          st_shared_v4_b32(dst + (((c / 4 + i + r) & 31) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (whole) {
+#pragma unroll 4
+      for (int k = lane >> 4; k < mine; k += 2)
+        reinterpret_cast<uint4*>(p.ctx + (out_row + first + k) * kDC + 128 * part)[lane & 15] =
+            ld_shared_v4_b32(src + k * 512 + (((lane + first + k) & 15) << 4));
+      if (part == 0 && row < rows && p.lse != nullptr)
+        p.lse[out_row + r] = l == 0.f ? -INFINITY : ref * kLn2 + logf(l);
+    } else {
       if (lane == 0 && mine > 0) {
-        const int64_t part = (2 * (int64_t)w.slot + half) * min(p.R, kRows) + kMyRows * w.rank + first;
-        bulk_store_s2g(p.ws_o + part * 256, base + 32 * warp * 1024, mine * 1024);
+        const int64_t at = (4 * (int64_t)w.slot + part) * min(p.R, kRows) + kMyRows * w.rank + first;
+        bulk_store_s2g(p.ws_o + at * 128, src, mine * 512);
         bulk_group_commit();
         bulk_group_wait_read_all();
       }
-      if (half == 0 && row < rows) p.ws_ml[(int64_t)w.slot * kRows + row] = make_float2(ref, l);
+      if (part == 0 && row < rows) p.ws_ml[(int64_t)w.slot * kRows + row] = make_float2(ref, l);
     }
     if (threadIdx.x == 0 && w.rank == 0 && w.begin == 0) p.table[w.b * p.groups + w.g] = make_int4(w.slot, w.c0, w.pieces, 0);
     tc_fence_before();
@@ -710,31 +696,38 @@ __device__ __noinline__ bool softmax_role(const Params& p, Smem& sm, Work w) {
 
 // One warp: a latent slab of the CTA's keys in every tile, loaded one tile ahead (from L2: another warp prefetches).
 // Warps of the region that holds the other half's features also replace their slab by values of the other CTA's
-// keys once its scores are done.
+// keys once its scores are done: X's (three buffers) after the next tile's slab, Y's (two) before it.
 __device__ __noinline__ bool latent_role(const Params& p, Smem& sm, Work w) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int region = warp >= kYWarp0 ? 1 : 0, j = warp - (region ? kYWarp0 : kXWarp0);
-  const bool does_values = region != w.rank;
+  const bool values = region != w.rank;
+  const int bufs = region ? kYBufs : kXBufs, lead = values ? bufs - 2 : 0;
   const int keys = w.begin * kTile + kKeys * w.rank, others = w.begin * kTile + kKeys * (1 - w.rank);
   PartSource src = part_source(p, w.b, keys, 4 * region + j, lane);
   PartSource vsrc = part_source(p, w.b, others, 4 * w.rank + j, lane);
-  int left = w.len - keys - (lane >> 1), vleft = does_values ? w.len - others - (lane >> 1) : 0;
+  int left = w.len - keys - (lane >> 1), vleft = !values ? 0 : w.len - others - (lane >> 1);
+  const uint32_t slabs = w.base + (region ? kYOff : 0) + j * kSlabBytes;
   Part k, v;
   load_part(src, left, k);
   load_part(vsrc, vleft, v);
+  // step t: the slab of tile t, then the values of tile t - lead
 #pragma unroll 1
-  for (uint32_t t = 0; t < w.n; ++t) {
-    const uint32_t it = w.it0 + t, bufs = region ? kYBufs : kXBufs, buf = it % bufs, use = it / bufs;
-    const uint32_t slab = w.base + (region ? kYOff : 0) + buf * kRegion + j * kSlabBytes;
-    if (!wait_warp(sm, region ? sm.y_empty[buf] : sm.x_empty[buf], (use & 1u) ^ 1u, p.err)) return false;
-    store_part(k, slab, lane);
-    if (lane == 0) arrive_even(region ? sm.y_full[buf] : sm.x_full[buf], w.rank);
-    if (warp == kXWarp0 && lane == 0) *const_cast<volatile int*>(&sm.progress) = (int)t;
-    left -= kTile;
-    load_part(src, left, k);
-    if (!does_values) continue;
-    if (!wait_warp(sm, sm.s_full, it & 1u, p.err)) return false;
-    store_part(v, slab, lane);
+  for (int t = 0; t < (int)w.n + lead; ++t) {
+    if (t < (int)w.n) {
+      const uint32_t it = w.it0 + t, buf = it % bufs;
+      if (!wait_warp(sm, region ? sm.y_empty[buf] : sm.x_empty[buf], ((it / bufs) & 1u) ^ 1u, p.err)) return false;
+      store_part(k, slabs + buf * kRegion, lane);
+      if (lane == 0) arrive_even(region ? sm.y_full[buf] : sm.x_full[buf], w.rank);
+      if (warp == kXWarp0 && lane == 0) *const_cast<volatile int*>(&sm.progress) = t;
+      left -= kTile;
+      load_part(src, left, k);
+    }
+    if (!values || t < lead) continue;
+    const uint32_t it = w.it0 + t - lead;
+    // (a barrier for even and one for odd tiles: the scores of the next tile may be done as well by now, those
+    // of the one after it wait for this warp)
+    if (!wait_warp(sm, sm.s_full[it & 1u], (it >> 1) & 1u, p.err)) return false;
+    store_part(v, slabs + it % bufs * kRegion, lane);
     if (lane == 0) arrive_even(sm.v_full[it & 1u], w.rank);
     vleft -= kTile;
     load_part(vsrc, vleft, v);
@@ -808,12 +801,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
       mbar_init(smem_u32(&sm.rope_full[i]), 2);
       mbar_init(smem_u32(&sm.rope_empty[i]), 1);
       mbar_init(smem_u32(&sm.v_full[i]), 8);
-      mbar_init(smem_u32(&sm.ref_bar[i]), 2);
-      mbar_init(smem_u32(&sm.sum_bar[i]), 2);
+      mbar_init(smem_u32(&sm.s_full[i]), 1);
     }
-    mbar_init(smem_u32(&sm.s_empty), 8);
-    mbar_init(smem_u32(&sm.p_full), 8);
-    mbar_init(smem_u32(&sm.s_full), 1);
+    mbar_init(smem_u32(&sm.s_empty), 2 * kSoftmaxWarps);
+    mbar_init(smem_u32(&sm.p_full), 2 * kSoftmaxWarps);
     mbar_init(smem_u32(&sm.pv_done), 1);
     mbar_init(smem_u32(&sm.drain), 1);
     mbar_init(smem_u32(&sm.q_full), 1);
@@ -853,7 +844,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
     w.slot = sm.piece.slot;
     w.c0 = sm.piece.c0;
     w.pieces = sm.piece.n;
-    w.index = (int)pieces;
     if (threadIdx.x == 0) {
       sm.progress = 0;
       fetch_query(p, sm, base, w.b, kRows * w.g + kMyRows * rank);
@@ -862,9 +852,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
       for (int t = 0; t < kPrefetch && t < (int)w.n; ++t)
         prefetch_rows(p, w.b, (w.begin + t) * kTile + kKeys * rank, w.len, lane);
     __syncwarp();
-    // (all eight warps come here in every piece: they meet inside)
-    if (warp < 4 || (warp >= kYWarp0 && warp < kRopeWarp))
-      dead |= !place_query(p, sm, base, tmem, warp >= kYWarp0 ? 1 : 0, pieces & 1u);
+    // (all eight come here in every piece: they meet inside)
+    if (warp < kSoftmaxWarps) dead |= !place_query(p, sm, base, tmem, warp >> 2, pieces & 1u);
     ++pieces;
     __syncwarp();
     cluster_sync();  // the query is in place in both CTAs (in the first piece: and their barriers)
@@ -872,7 +861,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
     if (sm.abort) dead = true;
     if (!dead) {
       bool ok = true;
-      if (warp < 4)
+      if (warp < kSoftmaxWarps)
         ok = softmax_role(p, sm, w);
       else if (warp == kMmaWarp)
         ok = rank != 0 || mma_role(p, it0, w.n);
@@ -927,18 +916,18 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Param
   // a decode that gave up may have left no entry
   if ((unsigned)e.x >= 2u * p.pairs || e.y < 0 || e.z < 0 || e.z > p.pairs || e.y > p.pairs - e.z) e.z = 0;
   const int stride = min(p.R, kRows);
-  auto part = [&](int k) { return 2 * (int64_t)(k == 0 ? e.x : 2 * (e.y + k)) + hf; };
+  auto slot = [&](int k) { return (int64_t)(k == 0 ? e.x : 2 * (e.y + k)); };
   float M = -INFINITY;
-  for (int k = lane; k < e.z; k += 32) M = fmaxf(M, p.ws_ml[(part(k) >> 1) * kRows + i].x);
+  for (int k = lane; k < e.z; k += 32) M = fmaxf(M, p.ws_ml[slot(k) * kRows + i].x);
   M = warp_max(M);
   const float ref = M == -INFINITY ? 0.f : M;
   float L = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  // lane l holds features 8 l .. 8 l + 7: chunks 2 l and 2 l + 1 of the rotated row
+  // lane l holds features 8 l .. 8 l + 7 of the half: two chunks of a rotated row
 #pragma unroll 4
   for (int k = 0; k < e.z; ++k) {
-    const float2 ml = p.ws_ml[(part(k) >> 1) * kRows + i];
-    const float4* src = reinterpret_cast<const float4*>(p.ws_o + (part(k) * stride + i) * 256);
-    const float4 a = src[(2 * lane + i) & 63], c = src[(2 * lane + 1 + i) & 63];
+    const float2 ml = p.ws_ml[slot(k) * kRows + i];
+    const float4* src = reinterpret_cast<const float4*>(p.ws_o + ((4 * slot(k) + 2 * hf + (lane >> 4)) * stride + i) * 128);
+    const float4 a = src[(2 * lane + i) & 31], c = src[(2 * lane + 1 + i) & 31];
     if (ml.y == 0.f) continue;  // the row saw none of this piece's keys
     const float f = exp2f(ml.x - ref);
     L = fmaf(f, ml.y, L);
