@@ -25,7 +25,7 @@
 //   values of these 64 rows (MN-major).  In the other one the values of the other 64 rows replace the slabs once
 //   the scores are done.  Then X holds the values of the tile's first 64 rows and Y of its last 64, in both CTAs.
 // * TMEM: context 256 columns, scores 64, query features 0..383 192 columns (A operand, in both lane halves).
-// * Nine warps decode: lane pairs own a key, 16-byte loads of codes one tile ahead in registers (a warp of its
+// * Thirteen warps decode: 16-byte loads of codes one tile ahead in registers (a warp of its
 //   own brings the rows to L2 four tiles ahead), cvt to fp16, one product with the block's scale, stores in the
 //   128-byte-swizzled layout.
 // * MMA order S(t + 1), O(t), S(t + 2), ...: the softmax of tile t runs under S(t + 1), and the tensor pipe
@@ -67,8 +67,8 @@ constexpr int kPOff = kQOff + 3 * kSlabBytes;    // probabilities of the first a
 constexpr int kSmemOff = kPOff + 2 * kSlabBytes;
 static_assert(kQTmemSlabs * kSlabBytes <= kYOff, "the query is staged in region X");
 static_assert(kMyRows * kDC * 4 <= kRopeOff, "the partial context is staged in the regions");
-constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kXWarp0 = 9, kYWarp0 = 13, kRopeWarp = 17, kPrefetchWarp = 18;
-constexpr int kThreads = 32 * 19;
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kXWarp0 = 9, kYWarp0 = 13, kVWarp0 = 17, kRopeWarp = 21, kPrefetchWarp = 22;
+constexpr int kThreads = 32 * 23;
 constexpr uint32_t kTmemCols = 512, kColO = 0, kColS = 256, kColQ = 320;
 // Probabilities are 2^(z - ref): ref is set kRaise below the largest score so far (log2 units) and moved up
 // only when a score passes it by kRescale.  So they reach 2^15 at most (fp16 ends at 2^16), the sum is at
@@ -296,7 +296,11 @@ __device__ __noinline__ void next_piece(const Params& p, int c, Plan& s, Piece* 
   *out = r;
 }
 
-// A decode warp's lane: 32 features of one 64-feature slab for four of 64 keys (lane / 2 + 16 i).
+// A decode warp has 16 of 64 keys and one half of the latent features, 128 bytes of codes: eight lanes cover a
+// key's, so an instruction reads four keys in about six cache lines (one key per lane pair, 64 features each,
+// needed sixteen, and the L1 lookups then bounded the kernel).  Lane l has 32 features, of slab (l & 7) / 2, and
+// of the keys 4 i + r, i = 0..3, the r that makes the eight lanes of a store phase hit distinct banks: the four
+// slabs take four different rows.
 struct Part {
   uint4 code[4];
   uint32_t scale[4];
@@ -304,35 +308,38 @@ struct Part {
 struct PartSource {
   const uint8_t* code;
   const uint8_t* scale;
-  int64_t code16, scale16;  // 16 rows on
+  int64_t code4, scale4;  // four rows on
+  int left;               // keys from the lane's first one on that are in the sequence
 };
-// From key `first` on
-__device__ __forceinline__ PartSource part_source(const Params& p, int b, int first, int slab, int lane) {
-  const int64_t t = (int64_t)first + (lane >> 1);
-  return {p.kv.c4 + b * p.kv.c4_b + t * p.kv.c4_r + 32 * slab + 16 * (lane & 1),
-          p.kv.sc + b * p.kv.sc_b + t * p.kv.sc_r + 4 * slab + 2 * (lane & 1), 16 * p.kv.c4_r, 16 * p.kv.sc_r};
+__device__ __forceinline__ int part_row(int lane) { return ((lane >> 3) + ((lane & 7) >> 1)) & 3; }
+// From key `first` on, half `region` of the features, by warp j of four
+__device__ __forceinline__ PartSource part_source(const Params& p, int b, int len, int first, int region, int j, int lane) {
+  const int64_t t = (int64_t)first + 16 * j + part_row(lane);
+  return {p.kv.c4 + b * p.kv.c4_b + t * p.kv.c4_r + 128 * region + 16 * (lane & 7),
+          p.kv.sc + b * p.kv.sc_b + t * p.kv.sc_r + 16 * region + 2 * (lane & 7), 4 * p.kv.c4_r, 4 * p.kv.sc_r,
+          (int)(len - t)};
 }
-// Loads the source's keys and moves on to the next tile's; `left` keys from the lane's first one are in the sequence.
-__device__ __forceinline__ void load_part(PartSource& s, int left, Part& k) {
+// Loads the source's keys and moves on to the next tile's.
+__device__ __forceinline__ void load_part(PartSource& s, Part& k) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     k.code[i] = make_uint4(0u, 0u, 0u, 0u);
     k.scale[i] = 0u;
-    if (16 * i < left) {  // rows behind the sequence may hold anything, or not exist
-      k.code[i] = __ldg(reinterpret_cast<const uint4*>(s.code));
-      k.scale[i] = __ldg(reinterpret_cast<const uint16_t*>(s.scale));
+    if (4 * i < s.left) {  // rows behind the sequence may hold anything, or not exist
+      k.code[i] = __ldg(reinterpret_cast<const uint4*>(s.code + i * s.code4));
+      k.scale[i] = __ldg(reinterpret_cast<const uint16_t*>(s.scale + i * s.scale4));
     }
-    s.code += s.code16;
-    s.scale += s.scale16;
   }
-  s.code += 4 * s.code16;
-  s.scale += 4 * s.scale16;
+  s.code += kTile / 4 * s.code4;
+  s.scale += kTile / 4 * s.scale4;
+  s.left -= kTile;
 }
-__device__ __forceinline__ void store_part(const Part& k, uint32_t dst, int lane) {
-  const int half = lane & 1;
+// Decodes into the region at `dst`.
+__device__ __forceinline__ void store_part(const Part& k, uint32_t dst, int j, int lane) {
+  const int half = lane & 1, r = part_row(lane);
+  dst += ((lane & 7) >> 1) * kSlabBytes + (16 * j + r) * 128;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int row = 16 * i + (lane >> 1);
     const uint32_t s2 = fp4::scales_to_f16(k.scale[i]);
     const uint32_t s[2] = {__byte_perm(s2, s2, 0x1010), __byte_perm(s2, s2, 0x3232)};
     const uint32_t words[4] = {k.code[i].x, k.code[i].y, k.code[i].z, k.code[i].w};
@@ -342,32 +349,24 @@ __device__ __forceinline__ void store_part(const Part& k, uint32_t dst, int lane
       fp4::codes_to_f16(words[w], h);
 #pragma unroll
       for (int e = 0; e < 4; ++e) h[e] = fp4::mul_f16x2(h[e], s[w >> 1]);
-      st_shared_v4_b32(dst + row * 128 + (((4 * half + w) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
+      st_shared_v4_b32(dst + 512 * i + (((4 * (half ^ (i & 1)) + w) ^ r) << 4), h[0], h[1], h[2], h[3]);
     }
   }
   fence_proxy_async_smem();
   __syncwarp();
 }
-// The rotary warp's lane: half of the rotary row of the same four keys.
-__device__ __forceinline__ void load_rope(const uint8_t*& src, int64_t rows16, int left, uint4 (&k)[16]) {
+// The rotary warp: eight lanes cover a key's row, lane l has the keys l / 8 + 4 i.
+__device__ __forceinline__ void load_rope(const uint8_t*& src, int64_t rows4, int left, uint4 (&k)[16]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      k[4 * i + j] = 16 * i < left ? __ldg(reinterpret_cast<const uint4*>(src) + j) : make_uint4(0u, 0u, 0u, 0u);
-    src += rows16;
-  }
-  src += 4 * rows16;
+  for (int i = 0; i < 16; ++i)
+    k[i] = 4 * i < left ? __ldg(reinterpret_cast<const uint4*>(src + i * rows4)) : make_uint4(0u, 0u, 0u, 0u);
+  src += kTile / 4 * rows4;
 }
 __device__ __forceinline__ void store_rope(const uint4 (&k)[16], uint32_t dst, int lane) {
+  dst += (lane >> 3) * 128;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = 16 * i + (lane >> 1);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      st_shared_v4_b32(dst + row * 128 + (((4 * (lane & 1) + j) ^ (row & 7)) << 4), k[4 * i + j].x, k[4 * i + j].y,
-                       k[4 * i + j].z, k[4 * i + j].w);
-  }
+  for (int i = 0; i < 16; ++i)
+    st_shared_v4_b32(dst + 512 * i + (((lane & 7) ^ (lane >> 3) ^ (4 * (i & 1))) << 4), k[i].x, k[i].y, k[i].z, k[i].w);
   fence_proxy_async_smem();
   __syncwarp();
 }
@@ -694,43 +693,28 @@ __device__ __noinline__ bool softmax_role(const Params& p, Smem& sm, Work w) {
   return ok;
 }
 
-// One warp: a latent slab of the CTA's keys in every tile, loaded one tile ahead (from L2: another warp prefetches).
-// Warps of the region that holds the other half's features also replace their slab by values of the other CTA's
-// keys once its scores are done: X's (three buffers) after the next tile's slab, Y's (two) before it.
+// One warp: 16 keys of every tile, loaded one tile ahead (from L2: another warp prefetches).  Four warps have the
+// CTA's keys in region X, four in region Y, and four replace the slabs of the half that is not the CTA's by
+// values of the other CTA's keys once the tile's scores are done.
 __device__ __noinline__ bool latent_role(const Params& p, Smem& sm, Work w) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int region = warp >= kYWarp0 ? 1 : 0, j = warp - (region ? kYWarp0 : kXWarp0);
-  const bool values = region != w.rank;
-  const int bufs = region ? kYBufs : kXBufs, lead = values ? bufs - 2 : 0;
-  const int keys = w.begin * kTile + kKeys * w.rank, others = w.begin * kTile + kKeys * (1 - w.rank);
-  PartSource src = part_source(p, w.b, keys, 4 * region + j, lane);
-  PartSource vsrc = part_source(p, w.b, others, 4 * w.rank + j, lane);
-  int left = w.len - keys - (lane >> 1), vleft = !values ? 0 : w.len - others - (lane >> 1);
-  const uint32_t slabs = w.base + (region ? kYOff : 0) + j * kSlabBytes;
-  Part k, v;
-  load_part(src, left, k);
-  load_part(vsrc, vleft, v);
-  // step t: the slab of tile t, then the values of tile t - lead
+  const bool values = warp >= kVWarp0;
+  const int region = values ? 1 - w.rank : warp >= kYWarp0 ? 1 : 0, j = (warp - kXWarp0) & 3;
+  const uint32_t bufs = region ? kYBufs : kXBufs, slabs = w.base + (region ? kYOff : 0);
+  PartSource src = part_source(p, w.b, w.len, w.begin * kTile + kKeys * (values ? 1 - w.rank : w.rank),
+                               values ? w.rank : region, j, lane);
+  Part k;
+  load_part(src, k);
 #pragma unroll 1
-  for (int t = 0; t < (int)w.n + lead; ++t) {
-    if (t < (int)w.n) {
-      const uint32_t it = w.it0 + t, buf = it % bufs;
-      if (!wait_warp(sm, region ? sm.y_empty[buf] : sm.x_empty[buf], ((it / bufs) & 1u) ^ 1u, p.err)) return false;
-      store_part(k, slabs + buf * kRegion, lane);
-      if (lane == 0) arrive_even(region ? sm.y_full[buf] : sm.x_full[buf], w.rank);
-      if (warp == kXWarp0 && lane == 0) *const_cast<volatile int*>(&sm.progress) = t;
-      left -= kTile;
-      load_part(src, left, k);
-    }
-    if (!values || t < lead) continue;
-    const uint32_t it = w.it0 + t - lead;
-    // (a barrier for even and one for odd tiles: the scores of the next tile may be done as well by now, those
-    // of the one after it wait for this warp)
-    if (!wait_warp(sm, sm.s_full[it & 1u], (it >> 1) & 1u, p.err)) return false;
-    store_part(v, slabs + it % bufs * kRegion, lane);
-    if (lane == 0) arrive_even(sm.v_full[it & 1u], w.rank);
-    vleft -= kTile;
-    load_part(vsrc, vleft, v);
+  for (uint32_t t = 0; t < w.n; ++t) {
+    const uint32_t it = w.it0 + t, buf = it % bufs;
+    uint64_t &from = values ? sm.s_full[it & 1u] : region ? sm.y_empty[buf] : sm.x_empty[buf],
+             &to = values ? sm.v_full[it & 1u] : region ? sm.y_full[buf] : sm.x_full[buf];
+    if (!wait_warp(sm, from, values ? (it >> 1) & 1u : ((it / bufs) & 1u) ^ 1u, p.err)) return false;
+    store_part(k, slabs + buf * kRegion, j, lane);
+    if (lane == 0) arrive_even(to, w.rank);
+    if (warp == kXWarp0 && lane == 0) *const_cast<volatile int*>(&sm.progress) = (int)t;
+    load_part(src, k);
   }
   return true;
 }
@@ -766,10 +750,10 @@ __device__ __noinline__ void prefetch_role(const Params& p, Smem& sm, Work w) {
 __device__ __noinline__ bool rope_role(const Params& p, Smem& sm, Work w) {
   const int lane = threadIdx.x & 31, keys = w.begin * kTile + kKeys * w.rank;
   const uint8_t* src = reinterpret_cast<const uint8_t*>(static_cast<const __nv_bfloat16*>(p.kv.k_r) + w.b * p.kv.kr_b +
-                                                        ((int64_t)keys + (lane >> 1)) * p.kv.kr_r) + 64 * (lane & 1);
-  int left = w.len - keys - (lane >> 1);
+                                                        ((int64_t)keys + (lane >> 3)) * p.kv.kr_r) + 16 * (lane & 7);
+  int left = w.len - keys - (lane >> 3);
   uint4 k[16];
-  load_rope(src, 32 * p.kv.kr_r, left, k);
+  load_rope(src, 8 * p.kv.kr_r, left, k);
 #pragma unroll 1
   for (uint32_t t = 0; t < w.n; ++t) {
     const uint32_t it = w.it0 + t, buf = it % kRopeBufs;
@@ -777,7 +761,7 @@ __device__ __noinline__ bool rope_role(const Params& p, Smem& sm, Work w) {
     store_rope(k, w.base + kRopeOff + buf * kSlabBytes, lane);
     if (lane == 0) arrive_even(sm.rope_full[buf], w.rank);
     left -= kTile;
-    load_rope(src, 32 * p.kv.kr_r, left, k);
+    load_rope(src, 8 * p.kv.kr_r, left, k);
   }
   return true;
 }
