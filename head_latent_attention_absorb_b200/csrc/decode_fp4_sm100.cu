@@ -20,16 +20,18 @@
 //   bf16 elements are exact down to 2^-31 of it, and the power goes into the row's softmax scale.  The rotary
 //   part stays in bf16 (separate MMAs into the same accumulator).  Probabilities are rounded to fp16.
 // * Shared memory (224 KB): region X holds the key slabs of features 0..255 (three buffers), region Y those of
-//   256..511 (two), the rotary slab (two), query features 384..511 and the rotary query, the probabilities.
+//   256..511 (two), the rotary slab, query features 256..511 and the rotary query, the probabilities.
 //   One of the regions holds the CTA's own half of the features: its slabs serve the scores (K-major) and are the
 //   values of these 64 rows (MN-major).  In the other one the values of the other 64 rows replace the slabs once
 //   the scores are done.  Then X holds the values of the tile's first 64 rows and Y of its last 64, in both CTAs.
-// * TMEM: context 256 columns, scores 64, query features 0..383 192 columns (A operand, in both lane halves).
+// * TMEM: context 256 columns, scores two buffers of 64, query features 0..255 128 columns (A operand, in both
+//   lane halves).
 // * Thirteen warps decode: 16-byte loads of codes one tile ahead in registers (a warp of its
 //   own brings the rows to L2 four tiles ahead), cvt to fp16, one product with the block's scale, stores in the
 //   128-byte-swizzled layout.
-// * MMA order S(t + 1), O(t), S(t + 2), ...: the softmax of tile t runs under S(t + 1), and the tensor pipe
-//   works on O(t - 1) while S(t) is read from TMEM.  The scores start with X, whose third buffer is decoded ahead,
+// * MMA order S(t + 1), O(t), S(t + 2), ...: the softmax of tile t runs under O(t - 1) and S(t + 1).  (With one
+//   score buffer S(t + 1) waited for both CTAs to have read S(t): an arrival at the other CTA takes some hundred
+//   cycles.)  The scores start with X, whose third buffer is decoded ahead,
 //   while Y's are decoded behind O.
 // * Eight softmax warps: a thread has 32 keys of a query row and agrees with the three threads that have the row's
 //   others on the reference of the base-2 exponentials, which moves (and the context is rescaled in TMEM) only when the
@@ -58,18 +60,18 @@ constexpr int kTile = 128, kKeys = 64;           // keys per tile, and of it per
 constexpr int kRows = 128, kMyRows = 64;         // query rows per group, and per CTA
 constexpr int kSlabBytes = 64 * 128;             // 64 rows (keys or query rows) of 64 features
 constexpr int kRegion = 4 * kSlabBytes;          // half of the latent features of 64 keys
-constexpr int kXBufs = 3, kYBufs = 2, kRopeBufs = 2;
-constexpr int kQTmemSlabs = 6;                   // query slabs in TMEM; the other two and the rotary one in shared memory
+constexpr int kXBufs = 3, kYBufs = 2;
+constexpr int kQTmemSlabs = 4;                   // query slabs in TMEM; the other four and the rotary one in shared memory
 constexpr int kYOff = kXBufs * kRegion;
 constexpr int kRopeOff = kYOff + kYBufs * kRegion;
-constexpr int kQOff = kRopeOff + kRopeBufs * kSlabBytes;
-constexpr int kPOff = kQOff + 3 * kSlabBytes;    // probabilities of the first and the last 64 keys
+constexpr int kQOff = kRopeOff + kSlabBytes;
+constexpr int kPOff = kQOff + 5 * kSlabBytes;    // probabilities of the first and the last 64 keys
 constexpr int kSmemOff = kPOff + 2 * kSlabBytes;
-static_assert(kQTmemSlabs * kSlabBytes <= kYOff, "the query is staged in region X");
+static_assert(kQTmemSlabs * kSlabBytes <= kRegion, "the query for TMEM is staged in a buffer of region X");
 static_assert(kMyRows * kDC * 4 <= kRopeOff, "the partial context is staged in the regions");
 constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kXWarp0 = 9, kYWarp0 = 13, kVWarp0 = 17, kRopeWarp = 21, kPrefetchWarp = 22;
-constexpr int kThreads = 32 * 23;
-constexpr uint32_t kTmemCols = 512, kColO = 0, kColS = 256, kColQ = 320;
+constexpr int kThreads = 32 * (kPrefetchWarp + 1);
+constexpr uint32_t kTmemCols = 512, kColO = 0, kColS = 256, kColQ = 384;  // scores: two buffers of 64
 // Probabilities are 2^(z - ref): ref is set kRaise below the largest score so far (log2 units) and moved up
 // only when a score passes it by kRescale.  So they reach 2^15 at most (fp16 ends at 2^16), the sum is at
 // least 2^kRaise, and a probability that fp16's subnormals round (2^-25) is off by 2^-32 of the sum.
@@ -99,8 +101,8 @@ struct Params {
 __device__ __forceinline__ int item_keys(const Params& p, int i) {
   const int len = p.lengths[i / p.groups];
   if (len < p.T || len > p.n_max) return 0;
-  const int last = min(p.R, kRows * (i % p.groups + 1)) - 1;
-  return len - p.T + last / p.n_h + 1;
+  const int g = i % p.groups;
+  return g == p.groups - 1 ? len : len - p.T + (kRows * (g + 1) - 1) / p.n_h + 1;
 }
 __device__ __forceinline__ int item_tiles(const Params& p, int i) { return (item_keys(p, i) + kTile - 1) / kTile; }
 
@@ -118,23 +120,23 @@ struct Piece {
 struct Smem {
   // Waited for in the even CTA only; arrivals from both CTAs.  (The waiting thread reads nothing that they
   // guard, it issues MMAs; an acquire at cluster scope would cost it some hundred cycles a wait.)
-  uint64_t x_full[kXBufs], y_full[kYBufs], rope_full[kRopeBufs], v_full[2], s_empty, p_full;
+  uint64_t x_full[kXBufs], y_full[kYBufs], rope_full, v_full[2], s_empty[2], p_full, q_ready;
   // in each CTA; arrivals from the MMAs
-  uint64_t x_empty[kXBufs], y_empty[kYBufs], rope_empty[kRopeBufs], s_full[2], pv_done, drain;
-  uint64_t q_full;
-  alignas(16) float row_scale[kRows];  // by TMEM lane: softmax scale of the query row, log2 units
+  uint64_t x_empty[kXBufs], y_empty[kYBufs], rope_empty, s_full[2], pv_done, drain;
+  uint64_t q_full, q_placed;
   float share[2][4][kMyRows];          // exchange between the four threads of a row
   Plan plan;
   Piece piece;
   uint32_t tmem_base;
   int abort, never, progress;
 };
-constexpr int kSmemBytes = kSmemOff + (int)sizeof(Smem) + 1024;
+constexpr int kSmemBytes = kSmemOff + (int)sizeof(Smem);
 static_assert(kSmemBytes <= 232448, "shared memory above 227 KB");
 
+// (the kernel checks that the hardware places it on a 1024-byte boundary: there is no room to round it up)
 __device__ __forceinline__ uint8_t* shared_base() {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  return smem_raw;
 }
 
 // Bounded wait that records its own expiry; what follows a first failed try is one shared function, since the
@@ -374,20 +376,20 @@ __device__ __forceinline__ void store_rope(const uint4 (&k)[16], uint32_t dst, i
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// Where slab j of the query lands (8: the rotary one).
-__device__ __forceinline__ uint32_t query_slab(uint32_t base, int j) {
-  return base + (j < kQTmemSlabs ? 0 : kQOff - kQTmemSlabs * kSlabBytes) + j * kSlabBytes;
+// Where slab j of the query lands (8: the rotary one): those for TMEM at `stage`.
+__device__ __forceinline__ uint32_t query_slab(uint32_t base, uint32_t stage, int j) {
+  return j < kQTmemSlabs ? stage + j * kSlabBytes : base + kQOff + (j - kQTmemSlabs) * kSlabBytes;
 }
 
 // One thread: the CTA's 64 query rows of the item as they are (bf16, rows past R as zeros).
-__device__ __noinline__ void fetch_query(const Params& p, Smem& sm, uint32_t base, int b, int row) {
+__device__ __noinline__ void fetch_query(const Params& p, Smem& sm, uint32_t base, uint32_t stage, int b, int row) {
   fence_proxy_async_smem();  // the buffers were read and written by threads before
   const uint64_t pol = policy_evict_first();
   const uint32_t bar = smem_u32(&sm.q_full);
   mbar_arrive_expect_tx(bar, 9 * kSlabBytes);
 #pragma unroll 1
-  for (int j = 0; j < 8; ++j) tma_load_3d(query_slab(base, j), &p.tm_q, bar, 64 * j, row, b, pol);
-  tma_load_3d(query_slab(base, 8), &p.tm_qp, bar, 0, row, b, pol);
+  for (int j = 0; j < 8; ++j) tma_load_3d(query_slab(base, stage, j), &p.tm_q, bar, 64 * j, row, b, pol);
+  tma_load_3d(query_slab(base, stage, 8), &p.tm_qp, bar, 0, row, b, pol);
 }
 
 __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
@@ -396,38 +398,41 @@ __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// The query rows in place, by the softmax warps (the first four, h = 0: slabs 0..3, the others, h = 1: slabs 4..7 and the
-// rotary one), one row per thread and TMEM lane (lanes 64.. repeat the rows): the row's power of two, its latent
-// part to fp16 (in TMEM, or where it is), its rotary part scaled where it is.
-__device__ __noinline__ bool place_query(const Params& p, Smem& sm, uint32_t base, uint32_t tmem, int h, uint32_t parity) {
-  const int lane = 32 * ((threadIdx.x >> 5) & 3) + (threadIdx.x & 31), r = lane & (kMyRows - 1);
+// The query rows in place, by the softmax warps, one row per thread and TMEM lane (lanes 64.. repeat the rows): the
+// row's power of two; the latent part to fp16, slabs 0..3 in TMEM (the first four warps), the others where they are
+// (the other four warps, with the rotary part, which is only scaled).  `scale`: the row's softmax scale, log2 units.
+__device__ __noinline__ bool place_query(const Params& p, Smem& sm, uint32_t base, uint32_t tmem, uint32_t stage,
+                                         uint32_t parity, float* scale) {
+  const int lane = threadIdx.x & (kRows - 1), r = lane & (kMyRows - 1), h = threadIdx.x >> 7, hi = lane >> 6;
   const bool ok = wait_warp(sm, sm.q_full, parity, p.err);
-  auto chunk = [&](int j, int c) { return query_slab(base, j) + r * 128 + ((c ^ (r & 7)) << 4); };
+  auto chunk = [&](int j, int c) { return query_slab(base, stage, j) + r * 128 + ((c ^ (r & 7)) << 4); };
   const float ls = p.kv.latent_scale;
+  // two latent slabs each, the rotary one by the last
+  const int j0 = 4 * h + 2 * hi;
   float m = 0.f;
-  uint32_t big = 0u;
 #pragma unroll 1
-  for (int j = 4 * h; j < 4 + 5 * h; ++j) {
-    if (j == 8) {
-      m = fmaxf(bf16_lo(big), bf16_hi(big)) * ls;
-      big = 0u;
-    }
+  for (int j = j0; j < (h + hi == 2 ? 9 : j0 + 2); ++j) {
+    uint32_t big = 0u;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
       const uint4 u = ld_shared_v4_b32(chunk(j, c));
       big = max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(big, u.x), u.y), u.z), u.w);
     }
+    m = fmaxf(m, fmaxf(bf16_lo(big), bf16_hi(big)) * (j < 8 ? ls : 1.f));
   }
-  m = fmaxf(m, fmaxf(bf16_lo(big), bf16_hi(big)) * (h ? 1.f : ls));
-  sm.share[0][h][r] = m;
+  float(&x)[4][kMyRows] = sm.share[0];
+  x[2 * h + hi][r] = m;
   named_bar_sync(1, 256);
-  m = fmaxf(m, sm.share[0][1 - h][r]);
-  // 2^e that puts the row's largest element into [2^14, 2^15)
+  m = fmaxf(fmaxf(x[0][r], x[1][r]), fmaxf(x[2][r], x[3][r]));
+  // 2^e that puts the largest element into [2^14, 2^15)
   const int e = m > 0.f ? max(-126, min(126, 14 + 127 - (int)(__float_as_uint(m) >> 23))) : 0;
   const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
-  if (h == 0) sm.row_scale[lane] = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23), 1.2e-38f);
+  *scale = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23), 1.2e-38f);
+  // h = 0: slabs 0..3;  h = 1: 4, 5 and 8 by the rows of lanes 0.., 6 and 7 by their repetition
+  const int jn = h == 0 ? 4 : hi == 0 ? 3 : 2;
 #pragma unroll 1
-  for (int j = 4 * h; j < 4 + 5 * h; ++j) {
+  for (int k = 0; k < jn; ++k) {
+    const int j = h == 0 ? k : k == 2 ? 8 : j0 + k;
     const float a = j < 8 ? ls : 1.f;
     uint32_t v[32];
 #pragma unroll
@@ -436,19 +441,19 @@ __device__ __noinline__ bool place_query(const Params& p, Smem& sm, uint32_t bas
       const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float lo = bf16_lo(w[i]) * a * mul, hi = bf16_hi(w[i]) * a * mul;
-        v[4 * c + i] = j < 8 ? pack_f16x2_ieee(lo, hi) : pack_bf16x2(lo, hi);
+        const float lo = bf16_lo(w[i]) * a * mul, up = bf16_hi(w[i]) * a * mul;
+        v[4 * c + i] = j < 8 ? pack_f16x2_ieee(lo, up) : pack_bf16x2(lo, up);
       }
     }
-    if (j < kQTmemSlabs) {
+    if (h == 0) {
       tmem_st32(tmem + ((uint32_t)(lane & 96) << 16) + kColQ + 32 * j, v);
-    } else if (lane < kMyRows) {
+    } else {
 #pragma unroll
       for (int c = 0; c < 8; ++c)
         st_shared_v4_b32(chunk(j, c), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
     }
   }
-  tmem_st_wait();
+  if (h == 0) tmem_st_wait();
   tc_fence_before();
   fence_proxy_async_smem();
   return ok;
@@ -462,6 +467,8 @@ struct Work {
   int begin, b, g, len;
   int rank;
   int slot, c0, pieces;  // as in Piece
+  uint32_t parity;       // pieces before this one, modulo 2
+  uint32_t stage;        // where the query for TMEM is staged: the buffer of region X that is used last
 };
 
 // A 128-byte-swizzled shared-memory descriptor whose address is at + 32 k: the low word counts 16 bytes.
@@ -471,14 +478,13 @@ __device__ __forceinline__ uint64_t step_desc(uint32_t at, int k, uint32_t lbo_b
 }
 
 // One 64-feature slab of the scores, the query slab in TMEM columns q or in shared memory at q.
-__device__ __forceinline__ void slab_ts(uint32_t s, uint32_t q, uint32_t keys, bool first) {
+__device__ __forceinline__ void slab_ts(uint32_t s, uint32_t q, uint32_t keys) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    mma_pair_ts(s, q + 8 * k, step_desc(keys, k), idesc_f16_f32(kRows, kTile, 0, 0), first && k == 0 ? 0u : 1u);
+  for (int k = 0; k < 4; ++k) mma_pair_ts(s, q + 8 * k, step_desc(keys, k), idesc_f16_f32(kRows, kTile, 0, 0), 1u);
 }
-__device__ __forceinline__ void slab_ss(uint32_t s, uint32_t q, uint32_t keys, uint32_t idesc) {
+__device__ __forceinline__ void slab_ss(uint32_t s, uint32_t q, uint32_t keys, uint32_t idesc, bool first) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) mma_pair_ss(s, step_desc(q, k), step_desc(keys, k), idesc, 1u);
+  for (int k = 0; k < 4; ++k) mma_pair_ss(s, step_desc(q, k), step_desc(keys, k), idesc, first && k == 0 ? 0u : 1u);
 }
 // The context from 64 keys: their values at `v`, their probabilities at `pr`; 128 of each CTA's features at a time.
 __device__ __forceinline__ void values(uint32_t o, uint32_t pr, uint32_t v, bool first) {
@@ -491,34 +497,33 @@ __device__ __forceinline__ void values(uint32_t o, uint32_t pr, uint32_t v, bool
 }
 
 // One warp of the even CTA: the pair's MMAs of a piece, issued by one thread: S(t), then O(t - 1).
-__device__ __noinline__ bool mma_role(const Params& p, uint32_t it0, uint32_t n) {
+__device__ __noinline__ bool mma_role(const Params& p, uint32_t it0, uint32_t n, uint32_t parity) {
   uint8_t* smem = shared_base();
   Smem& sm = *reinterpret_cast<Smem*>(smem + kSmemOff);
-  const uint32_t base = smem_u32(smem), tmem = sm.tmem_base, tS = tmem + kColS, tQ = tmem + kColQ, tO = tmem + kColO;
+  const uint32_t base = smem_u32(smem), tmem = sm.tmem_base, tQ = tmem + kColQ, tO = tmem + kColO;
   constexpr uint16_t kBoth = 3;
   bool ok = true;
   if (elect_one()) {
+    ok = wait(sm, sm.q_ready, parity, p.err);
 #pragma unroll 1
-    for (uint32_t t = 0; t <= n; ++t) {
+    for (uint32_t t = 0; t <= n && ok; ++t) {
       if (t < n) {
-        const uint32_t it = it0 + t, xb = it % kXBufs, yb = it % kYBufs, rb = it % kRopeBufs;
-        ok = wait(sm, sm.s_empty, (it & 1u) ^ 1u, p.err) && wait(sm, sm.x_full[xb], (it / kXBufs) & 1u, p.err) &&
-             wait(sm, sm.rope_full[rb], (it / kRopeBufs) & 1u, p.err);
+        const uint32_t it = it0 + t, xb = it % kXBufs, yb = it % kYBufs, tS = tmem + kColS + 64 * (it & 1u);
+        ok = wait(sm, sm.s_empty[it & 1u], ((it >> 1) & 1u) ^ 1u, p.err) && wait(sm, sm.x_full[xb], (it / kXBufs) & 1u, p.err) &&
+             wait(sm, sm.rope_full, it & 1u, p.err);
         if (!ok) break;
         tc_fence_after();
         const uint32_t x = base + xb * kRegion, y = base + kYOff + yb * kRegion;
+        slab_ss(tS, base + kQOff + 4 * kSlabBytes, base + kRopeOff, idesc_bf16_f32(kRows, kTile, 0, 0), true);
+        mma_commit_pair(smem_u32(&sm.rope_empty), kBoth);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) slab_ts(tS, tQ + 32 * j, x + j * kSlabBytes, j == 0);
-        slab_ss(tS, base + kQOff + 2 * kSlabBytes, base + kRopeOff + rb * kSlabBytes, idesc_bf16_f32(kRows, kTile, 0, 0));
-        mma_commit_pair(smem_u32(&sm.rope_empty[rb]), kBoth);
+        for (int j = 0; j < 4; ++j) slab_ts(tS, tQ + 32 * j, x + j * kSlabBytes);
         ok = wait(sm, sm.y_full[yb], (it / kYBufs) & 1u, p.err);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int j = 0; j < 2; ++j) slab_ts(tS, tQ + 128 + 32 * j, y + j * kSlabBytes, false);
-#pragma unroll
-        for (int j = 2; j < 4; ++j)
-          slab_ss(tS, base + kQOff + (j - 2) * kSlabBytes, y + j * kSlabBytes, idesc_f16_f32(kRows, kTile, 0, 0));
+        for (int j = 0; j < 4; ++j)
+          slab_ss(tS, base + kQOff + j * kSlabBytes, y + j * kSlabBytes, idesc_f16_f32(kRows, kTile, 0, 0), false);
         mma_commit_pair(smem_u32(&sm.s_full[it & 1u]), kBoth);
       }
       if (t > 0) {
@@ -538,7 +543,7 @@ __device__ __noinline__ bool mma_role(const Params& p, uint32_t it0, uint32_t n)
 }
 
 // Eight warps, 32 keys of a query row per thread: probabilities, and the piece's result.
-__device__ __noinline__ bool softmax_role(const Params& p, Smem& sm, Work w) {
+__device__ __noinline__ bool softmax_role(const Params& p, Smem& sm, Work w, float sl, bool ok) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, col = warp >> 2;
   const int tl = 32 * quad + lane, r = tl & (kMyRows - 1), half = tl >> 6;  // TMEM lane, row, half of the tile's keys
   const int part = 2 * half + col;                                          // the row's quarter of keys and features
@@ -548,12 +553,10 @@ __device__ __noinline__ bool softmax_role(const Params& p, Smem& sm, Work w) {
   const uint32_t lanes = (uint32_t)(32 * quad) << 16;
   const uint32_t tS = w.tmem + lanes + kColS + 32 * col, tO = w.tmem + lanes + kColO + 128 * col;
   const uint32_t p_row = base + kPOff + half * kSlabBytes + r * 128;
-  const float sl = sm.row_scale[tl];
   // keys that the row, and the group's first row, see
   const int limit = len - p.T + (kRows * g + min(row, rows - 1)) / p.n_h + 1;
   const int all_see = len - p.T + (kRows * g) / p.n_h + 1;
   float ref = -INFINITY, l = 0.f;
-  bool ok = true;
   // The four warps that have the same rows meet once a tile and once more at the end.  A warp whose wait failed
   // still comes to all the meetings.
   uint32_t met = 0;
@@ -562,18 +565,18 @@ __device__ __noinline__ bool softmax_role(const Params& p, Smem& sm, Work w) {
     ++met;
   };
 #pragma unroll 1
-  for (uint32_t t = 0; t < n; ++t) {
+  for (uint32_t t = 0; t < n && ok; ++t) {
     const uint32_t it = it0 + t;
     const int k0 = (w.begin + (int)t) * kTile + 32 * part;
     ok = wait_warp(sm, sm.s_full[it & 1u], (it >> 1) & 1u, p.err);
     if (!ok) break;
     tc_fence_after();
     uint32_t s[32];
-    tmem_ld32(tS, s);
+    tmem_ld32(tS + 64 * (it & 1u), s);
     tmem_ld_wait();
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) arrive_even(sm.s_empty, w.rank);
+    if (lane == 0) arrive_even(sm.s_empty[it & 1u], w.rank);
     if (k0 + 32 > all_see) {
 #pragma unroll
       for (int i = 0; i < 32; ++i)
@@ -711,6 +714,8 @@ __device__ __noinline__ bool latent_role(const Params& p, Smem& sm, Work w) {
     uint64_t &from = values ? sm.s_full[it & 1u] : region ? sm.y_empty[buf] : sm.x_empty[buf],
              &to = values ? sm.v_full[it & 1u] : region ? sm.y_full[buf] : sm.x_full[buf];
     if (!wait_warp(sm, from, values ? (it >> 1) & 1u : ((it / bufs) & 1u) ^ 1u, p.err)) return false;
+    // (the first use of the third buffer: the query has left it)
+    if (region == 0 && !values && t == 2 && !wait_warp(sm, sm.q_placed, w.parity, p.err)) return false;
     store_part(k, slabs + buf * kRegion, j, lane);
     if (lane == 0) arrive_even(to, w.rank);
     if (warp == kXWarp0 && lane == 0) *const_cast<volatile int*>(&sm.progress) = (int)t;
@@ -740,7 +745,7 @@ __device__ __noinline__ void prefetch_role(const Params& p, Smem& sm, Work w) {
   const volatile int* progress = &sm.progress;
   const volatile int* abort = &sm.abort;
 #pragma unroll 1
-  for (int t = kPrefetch; t < (int)w.n; ++t) {
+  for (int t = 1; t < (int)w.n; ++t) {
     while (*progress + kPrefetch < t && !*abort) __nanosleep(100);  // the decode warps' waits are bounded
     prefetch_rows(p, w.b, (w.begin + t) * kTile + kKeys * w.rank, w.len, lane);
   }
@@ -756,10 +761,9 @@ __device__ __noinline__ bool rope_role(const Params& p, Smem& sm, Work w) {
   load_rope(src, 8 * p.kv.kr_r, left, k);
 #pragma unroll 1
   for (uint32_t t = 0; t < w.n; ++t) {
-    const uint32_t it = w.it0 + t, buf = it % kRopeBufs;
-    if (!wait_warp(sm, sm.rope_empty[buf], ((it / kRopeBufs) & 1u) ^ 1u, p.err)) return false;
-    store_rope(k, w.base + kRopeOff + buf * kSlabBytes, lane);
-    if (lane == 0) arrive_even(sm.rope_full[buf], w.rank);
+    if (!wait_warp(sm, sm.rope_empty, ((w.it0 + t) & 1u) ^ 1u, p.err)) return false;
+    store_rope(k, w.base + kRopeOff, lane);
+    if (lane == 0) arrive_even(sm.rope_full, w.rank);
     left -= kTile;
     load_rope(src, 8 * p.kv.kr_r, left, k);
   }
@@ -774,6 +778,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
   const int pair = blockIdx.x >> 1, rank = (int)cluster_ctarank();
 
   griddep_launch_dependents();
+  if (base & 1023u) {
+    if (threadIdx.x == 0) raise_error(p.err, MLA_ERR_CUDA);
+    return;
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kXBufs; ++i) {
       mbar_init(smem_u32(&sm.x_full[i]), 8);
@@ -782,30 +790,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sm.y_full[i]), 8);
       mbar_init(smem_u32(&sm.y_empty[i]), 1);
-      mbar_init(smem_u32(&sm.rope_full[i]), 2);
-      mbar_init(smem_u32(&sm.rope_empty[i]), 1);
       mbar_init(smem_u32(&sm.v_full[i]), 8);
       mbar_init(smem_u32(&sm.s_full[i]), 1);
+      mbar_init(smem_u32(&sm.s_empty[i]), 2 * kSoftmaxWarps);
     }
-    mbar_init(smem_u32(&sm.s_empty), 2 * kSoftmaxWarps);
+    mbar_init(smem_u32(&sm.rope_full), 2);
+    mbar_init(smem_u32(&sm.rope_empty), 1);
     mbar_init(smem_u32(&sm.p_full), 2 * kSoftmaxWarps);
+    mbar_init(smem_u32(&sm.q_ready), 2 * kSoftmaxWarps);
+    mbar_init(smem_u32(&sm.q_placed), kSoftmaxWarps);
+    mbar_init(smem_u32(&sm.q_full), 1);
     mbar_init(smem_u32(&sm.pv_done), 1);
     mbar_init(smem_u32(&sm.drain), 1);
-    mbar_init(smem_u32(&sm.q_full), 1);
-    sm.abort = sm.never = 0;
+    sm.abort = sm.never = sm.progress = 0;
     fence_mbar_init();
+    prefetch_tensormap(&p.tm_q);
+    prefetch_tensormap(&p.tm_qp);
   }
   if (warp == kMmaWarp) {
     tmem_alloc_pair(smem_u32(&sm.tmem_base), kTmemCols);
     tmem_relinquish_pair();
   }
+  __syncwarp();
+  // nothing arrives on the other CTA's barriers before they are there
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   griddep_wait();
   if (warp == 0) {
     make_plan(p, pair, &sm.plan);
     __syncwarp();
     if (lane == 0) next_piece(p, pair, sm.plan, &sm.piece);
+    __syncwarp();
   }
   tc_fence_before();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
@@ -821,59 +838,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
     w.it0 = it0;
     w.begin = sm.piece.begin;
     w.n = (uint32_t)(sm.piece.end - w.begin);
-    w.b = sm.piece.item / p.groups;
-    w.g = sm.piece.item % p.groups;
+    w.b = p.groups == 1 ? sm.piece.item : sm.piece.item / p.groups;
+    w.g = sm.piece.item - w.b * p.groups;
     w.len = p.lengths[w.b];
     w.rank = rank;
     w.slot = sm.piece.slot;
     w.c0 = sm.piece.c0;
     w.pieces = sm.piece.n;
-    if (threadIdx.x == 0) {
-      sm.progress = 0;
-      fetch_query(p, sm, base, w.b, kRows * w.g + kMyRows * rank);
-    }
-    if (warp == kPrefetchWarp)
-      for (int t = 0; t < kPrefetch && t < (int)w.n; ++t)
-        prefetch_rows(p, w.b, (w.begin + t) * kTile + kKeys * rank, w.len, lane);
+    w.parity = pieces++ & 1u;
+    w.stage = base + (it0 + kXBufs - 1) % kXBufs * kRegion;
+    if (threadIdx.x == 0) fetch_query(p, sm, base, w.stage, w.b, kRows * w.g + kMyRows * rank);
     __syncwarp();
-    // (all eight come here in every piece: they meet inside)
-    if (warp < kSoftmaxWarps) dead |= !place_query(p, sm, base, tmem, warp >> 2, pieces & 1u);
-    ++pieces;
-    __syncwarp();
-    cluster_sync();  // the query is in place in both CTAs (in the first piece: and their barriers)
-    tc_fence_after();
-    if (sm.abort) dead = true;
     if (!dead) {
       bool ok = true;
-      if (warp < kSoftmaxWarps)
-        ok = softmax_role(p, sm, w);
-      else if (warp == kMmaWarp)
-        ok = rank != 0 || mma_role(p, it0, w.n);
-      else if (warp < kRopeWarp)
+      if (warp < kSoftmaxWarps) {
+        float scale;
+        ok = place_query(p, sm, base, tmem, w.stage, w.parity, &scale);
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&sm.q_placed));
+          arrive_even(sm.q_ready, rank);
+        }
+        ok = softmax_role(p, sm, w, scale, ok);
+      } else if (warp == kMmaWarp) {
+        ok = rank != 0 || mma_role(p, it0, w.n, w.parity);
+      } else if (warp < kRopeWarp) {
         ok = latent_role(p, sm, w);
-      else if (warp == kRopeWarp)
+      } else if (warp == kRopeWarp) {
         ok = rope_role(p, sm, w);
-      else
+      } else {
         prefetch_role(p, sm, w);
+      }
       dead = !ok;
     }
     __syncwarp();
     it0 += w.n;
-    if (threadIdx.x == 0) next_piece(p, pair, sm.plan, &sm.piece);
+    if (threadIdx.x == 0) {
+      next_piece(p, pair, sm.plan, &sm.piece);
+      sm.progress = 0;
+    }
     __syncthreads();
     tc_fence_after();
     if (sm.abort) dead = true;
   }
-  if (threadIdx.x == 0 && sm.abort && pieces > 0)  // a query still on its way lands before the block leaves
-    mbar_wait(smem_u32(&sm.q_full), (pieces - 1) & 1u, &sm.never, kWaitLimitNs);
-  __syncwarp();
-  if (warp == kMmaWarp && pieces > 0) {
-    if (rank == 0 && elect_one()) mma_commit_pair(smem_u32(&sm.drain), 3);
+  if (sm.abort) {  // what is still on its way, the query and the MMAs, ends before the block leaves
+    if (threadIdx.x == 0 && pieces > 0) mbar_wait(smem_u32(&sm.q_full), (pieces - 1) & 1u, &sm.never, kWaitLimitNs);
     __syncwarp();
-    mbar_wait(smem_u32(&sm.drain), 0, &sm.never, kWaitLimitNs);
-    __syncwarp();
+    if (warp == kMmaWarp && rank == 0) {
+      if (elect_one()) {
+        mma_commit_pair(smem_u32(&sm.drain), 1);
+        mbar_wait(smem_u32(&sm.drain), 0, &sm.never, kWaitLimitNs);
+      }
+      __syncwarp();
+    }
   }
   tc_fence_before();
+  __syncwarp();
   cluster_sync();  // neither CTA leaves while the other may still arrive on its barriers or read its shared memory
   tc_fence_after();
   if (warp == kMmaWarp) tmem_dealloc_pair(tmem, kTmemCols);
