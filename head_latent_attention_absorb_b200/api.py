@@ -7,8 +7,8 @@ All tensors are CUDA tensors.  Strides are read from the tensors, so a packed
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 from typing import Optional, Sequence
 
 import torch
@@ -63,53 +63,92 @@ def _dims(x: Sequence[int]) -> MLADims:
     return x if isinstance(x, MLADims) else MLADims(*x)
 
 
-def _i32(t: torch.Tensor, shape, name: str):
-    if t.dtype != torch.int32 or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+# ---- The cache operators (4-bit cache, attention weights, eviction) are called once or more for every decoded
+# token, where a few microseconds on the host count.  Their checks take the common case first.
+def _fast_dims(x: Sequence[int]) -> MLADims:
+    if isinstance(x, MLADims):
+        return x
+    d = _DIMS.get(x) if type(x) is tuple else None
+    if d is None:
+        d = MLADims(*x)
+        if len(_DIMS) < 256:
+            _DIMS[tuple(x)] = d
+    return d
+
+
+_DIMS: dict = {}
+_FN: dict = {}
+
+
+def _fn(name: str):
+    f = _FN.get(name)
+    if f is None:
+        f = _FN[name] = getattr(lib(), name)
+    return f
+
+
+def _i32(t: torch.Tensor, shape: tuple, name: str):
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous int32 {list(shape)} tensor")
 
 
-def _shape(t: torch.Tensor, shape, dtype: torch.dtype, name: str):
-    if t.dtype != dtype:
+def _shape(t: torch.Tensor, shape: tuple, dtype: torch.dtype, name: str):
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    if t.shape[-1] > 1:
+    if t.stride(-1) != 1 and shape[-1] > 1:
         _rows(t, name)
 
 
-def _on_device(*tensors) -> torch.device:
-    """The one CUDA device that all the tensors (None: absent) live on."""
-    ts = [t for t in tensors if t is not None]
-    for t in ts:
-        if not t.is_cuda:
-            raise ValueError("expected a CUDA tensor")
-        if t.device != ts[0].device:
-            raise ValueError(f"tensors on two devices: {ts[0].device} and {t.device}")
-    return ts[0].device
+def _on_device(*tensors) -> int:
+    """Index of the one CUDA device that all the tensors (None: absent) live on."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d != dev:
+                if d < 0:
+                    raise ValueError("expected a CUDA tensor")
+                if dev is not None:
+                    raise ValueError(f"tensors on two devices: cuda:{dev} and cuda:{d}")
+                dev = d
+    return dev
 
 
-@contextlib.contextmanager
-def _entered(stream):
-    with torch.cuda.stream(stream):
-        yield
+class _Entered:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
 
 
-def _launch_on(stream, device: torch.device):
+_HERE = _Entered()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+
+
+def _launch_on(stream, device: int):
     """(context, handle) of a call: inside the context the tensors' device is current, and so is the
     stream, so that what the call allocates belongs to the stream that uses it."""
-    cur = torch.cuda.current_stream(device)
+    cur = _raw_stream(device)
+    handle = cur if stream is None else getattr(stream, "cuda_stream", stream)
+    if handle == cur and device == torch.cuda.current_device():
+        return _HERE, cur
     if stream is None:
-        stream = cur
+        stream = torch.cuda.current_stream(device)
     elif not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(stream, device=device)
-    if stream.cuda_stream == cur.cuda_stream and device.index == torch.cuda.current_device():
-        return contextlib.nullcontext(), cur.cuda_stream
-    return _entered(stream), stream.cuda_stream
+        stream = torch.cuda.ExternalStream(stream, device=torch.device("cuda", device))
+    return torch.cuda.stream(stream), handle
 
 
 def _flag(dev_err: Optional[torch.Tensor]):
-    if dev_err is not None and (dev_err.dtype != torch.int32 or dev_err.numel() < 1):
+    if dev_err is not None and (dev_err.dtype is not torch.int32 or dev_err.numel() < 1):
         raise TypeError("dev_err must be an int32 tensor")
+
+
+def _at(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
 def _fp4_planes(d: MLADims, c4: torch.Tensor, kv_scale: torch.Tensor, k_r: Optional[torch.Tensor],
@@ -125,29 +164,30 @@ def _fp4_planes(d: MLADims, c4: torch.Tensor, kv_scale: torch.Tensor, k_r: Optio
     return B, n_max
 
 
-def _token_rows(q: torch.Tensor, name: str) -> torch.Tensor:
-    """[B, T, n_h, w] as [B * T, n_h, w] without a copy."""
-    if q.dim() == 3:
-        return q
-    try:
-        return q.view(-1, q.shape[2], q.shape[3])
-    except RuntimeError:
-        raise ValueError(f"{name}: the tokens of consecutive sequences must be evenly strided") from None
+def _token_stride(q: torch.Tensor, name: str) -> int:
+    """Stride of the evenly strided rows (b, t, h) of a [B, n_h, w] or [B, T, n_h, w] tensor."""
+    if q.is_contiguous():
+        return q.shape[-1]
+    if q.dim() == 4:
+        try:
+            q = q.view(-1, q.shape[2], q.shape[3])
+        except RuntimeError:
+            raise ValueError(f"{name}: the tokens of consecutive sequences must be evenly strided") from None
+    return _headrows(q, name)
 
 
-def _queries(d: MLADims, q_tilde: torch.Tensor, q_pe: torch.Tensor, B: int, n_max: int, lengths: torch.Tensor):
-    """Query tensors [B, n_h, .] or [B, T, n_h, .] as rows; returns (T, q_tilde, ldqt, q_pe, ldqp)."""
-    if q_tilde.dim() not in (3, 4):
+def _queries(d: MLADims, q_tilde: torch.Tensor, q_pe: torch.Tensor, B: int, lengths: torch.Tensor):
+    """Query tensors [B, n_h, .] or [B, T, n_h, .]; returns (T, row stride of q_tilde, of q_pe)."""
+    shape = q_tilde.shape
+    if len(shape) not in (3, 4):
         raise ValueError("q_tilde must be [B, n_h, d_c] or [B, T, n_h, d_c]")
-    lead = tuple(q_tilde.shape[:-2])
-    T = 1 if len(lead) == 1 else lead[1]
-    _shape(q_tilde, (*lead, d.n_h, d.d_c), q_tilde.dtype, "q_tilde")
-    _shape(q_pe, (*lead, d.n_h, d.d_r), q_tilde.dtype, "q_pe")
+    lead, dtype = tuple(shape[:-2]), q_tilde.dtype
+    _shape(q_tilde, (*lead, d.n_h, d.d_c), dtype, "q_tilde")
+    _shape(q_pe, (*lead, d.n_h, d.d_r), dtype, "q_pe")
     if lead[0] != B:
         raise ValueError(f"q_tilde holds {lead[0]} sequences, the cache {B}")
     _i32(lengths, (B,), "lengths")
-    qt, qp = _token_rows(q_tilde, "q_tilde"), _token_rows(q_pe, "q_pe")
-    return T, qt, _headrows(qt, "q_tilde"), qp, _headrows(qp, "q_pe")
+    return 1 if len(lead) == 1 else lead[1], _token_stride(q_tilde, "q_tilde"), _token_stride(q_pe, "q_pe")
 
 
 def mla_absorb_q(dims, q_nope: torch.Tensor, w_kv_b: torch.Tensor, q_tilde: Optional[torch.Tensor] = None,
@@ -485,7 +525,7 @@ def mla_cache_append_fp4(dims, kv_a: torch.Tensor, positions: torch.Tensor, c4: 
     (None: the position); counts int32 [B], tokens of each sequence (None: all T).  c4 uint8
     [B, n_max, d_c / 2], kv_scale uint8 [B, n_max, d_c / 16] and k_r [B, n_max, d_r] may be views of one
     packed row.  latent_scale: a power of two, the same for every call on the cache."""
-    d = _dims(dims)
+    d = _fast_dims(dims)
     B, n_max = _fp4_planes(d, c4, kv_scale, k_r, kv_a.dtype)
     if kv_a.dim() not in (2, 3):
         raise ValueError("kv_a must be [B, d_c + d_r] or [B, T, d_c + d_r]")
@@ -503,11 +543,11 @@ def mla_cache_append_fp4(dims, kv_a: torch.Tensor, positions: torch.Tensor, c4: 
     dev = _on_device(kv_a, positions, c4, kv_scale, k_r, rows, counts, gain, dev_err)
     on, st = _launch_on(stream, dev)
     with on:
-        check(lib().mla_cache_append_fp4(
-            d, _dt(kv_a), B, T, _ptr(x), x.stride(0), x.stride(1) if T > 1 else d.d_c + d.d_r, _ptr(gain), float(eps),
-            float(rope_base), float(latent_scale), _ptr(positions), _ptr(rows), _ptr(counts), n_max,
-            _ptr(c4), c4.stride(0), c4.stride(1), _ptr(kv_scale), kv_scale.stride(0), kv_scale.stride(1),
-            _ptr(k_r), k_r.stride(0), k_r.stride(1), _ptr(dev_err), st), "mla_cache_append_fp4")
+        check(_fn("mla_cache_append_fp4")(
+            d, _dt(kv_a), B, T, _at(x), x.stride(0), x.stride(1) if T > 1 else d.d_c + d.d_r, _at(gain), float(eps),
+            float(rope_base), float(latent_scale), _at(positions), _at(rows), _at(counts), n_max,
+            _at(c4), c4.stride(0), c4.stride(1), _at(kv_scale), kv_scale.stride(0), kv_scale.stride(1),
+            _at(k_r), k_r.stride(0), k_r.stride(1), _at(dev_err), st), "mla_cache_append_fp4")
 
 
 def mla_cache_read_fp4(dims, c4: torch.Tensor, kv_scale: torch.Tensor, n: int, first: Optional[torch.Tensor] = None,
@@ -516,7 +556,7 @@ def mla_cache_read_fp4(dims, c4: torch.Tensor, kv_scale: torch.Tensor, n: int, f
                        dev_err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values of n latent rows per sequence of a 4-bit cache, from row first[b] on (int32 [B]; None: 0):
     out [B, n, d_c], zeros from counts[b] on (int32 [B]; None: n)."""
-    d = _dims(dims)
+    d = _fast_dims(dims)
     B, n_max = _fp4_planes(d, c4, kv_scale, None, None)
     if out is not None:
         _shape(out, (B, n, d.d_c), out.dtype, "out")
@@ -531,15 +571,21 @@ def mla_cache_read_fp4(dims, c4: torch.Tensor, kv_scale: torch.Tensor, n: int, f
     with on:
         if out is None:
             out = torch.empty((B, n, d.d_c), dtype=dtype, device=dev)
-        check(lib().mla_cache_read_fp4(
-            d, code, B, n, _ptr(first), _ptr(counts), n_max, _ptr(c4), c4.stride(0), c4.stride(1),
-            _ptr(kv_scale), kv_scale.stride(0), kv_scale.stride(1), float(latent_scale), _ptr(out), out.stride(0),
-            out.stride(1) if n > 1 else d.d_c, _ptr(dev_err), st), "mla_cache_read_fp4")
+        check(_fn("mla_cache_read_fp4")(
+            d, code, B, n, _at(first), _at(counts), n_max, _at(c4), c4.stride(0), c4.stride(1),
+            _at(kv_scale), kv_scale.stride(0), kv_scale.stride(1), float(latent_scale), _at(out), out.stride(0),
+            out.stride(1) if n > 1 else d.d_c, _at(dev_err), st), "mla_cache_read_fp4")
     return out
 
 
 def mla_decode_fp4kv_workspace_size(dims, dtype: torch.dtype, B: int, T: int, n_max: int) -> int:
+    """Bytes of workspace on the current device; 0 for arguments that the call would reject."""
     return int(lib().mla_decode_fp4kv_workspace_size(_dims(dims), _dtc(dtype), B, T, n_max))
+
+
+@functools.lru_cache(maxsize=1024)
+def _fp4kv_workspace(device: int, n_h: int, d_c: int, d_r: int, dtype: torch.dtype, B: int, T: int, n_max: int) -> int:
+    return mla_decode_fp4kv_workspace_size((n_h, d_c, d_r, 1, 1), dtype, B, T, n_max)
 
 
 def mla_decode_absorb_fp4kv(dims, q_tilde: torch.Tensor, q_pe: torch.Tensor, c4: torch.Tensor, kv_scale: torch.Tensor,
@@ -551,9 +597,9 @@ def mla_decode_absorb_fp4kv(dims, q_tilde: torch.Tensor, q_pe: torch.Tensor, c4:
     sequence (q_tilde [B, n_h, d_c], q_pe [B, n_h, d_r]) or T ([B, T, n_h, .], the last T cached rows of each
     sequence being those tokens).  Any n_h <= 128 in bf16.  Returns ctx of q_tilde's shape; lse float32
     [B, n_h] or [B, T, n_h]."""
-    d = _dims(dims)
+    d = _fast_dims(dims)
     B, n_max = _fp4_planes(d, c4, kv_scale, k_r, q_tilde.dtype)
-    T, qt, ldqt, qp, ldqp = _queries(d, q_tilde, q_pe, B, n_max, lengths)
+    T, ldqt, ldqp = _queries(d, q_tilde, q_pe, B, lengths)
     if ctx is not None:
         _shape(ctx, q_tilde.shape, q_tilde.dtype, "ctx")
     if lse is not None:
@@ -567,13 +613,13 @@ def mla_decode_absorb_fp4kv(dims, q_tilde: torch.Tensor, q_pe: torch.Tensor, c4:
         if ctx is None:
             ctx = torch.empty(q_tilde.shape, dtype=q_tilde.dtype, device=dev)
         if workspace is None:
-            nbytes = mla_decode_fp4kv_workspace_size(d, q_tilde.dtype, B, T, n_max)
+            nbytes = _fp4kv_workspace(dev, d.n_h, d.d_c, d.d_r, q_tilde.dtype, B, T, n_max)
             workspace = torch.empty((max(nbytes, 16),), dtype=torch.uint8, device=dev)
-        check(lib().mla_decode_absorb_fp4kv(
-            d, _dt(q_tilde), B, T, _ptr(qt), ldqt, _ptr(qp), ldqp, _ptr(c4), c4.stride(0), c4.stride(1),
-            _ptr(kv_scale), kv_scale.stride(0), kv_scale.stride(1), _ptr(k_r), k_r.stride(0), k_r.stride(1),
-            float(latent_scale), n_max, _ptr(lengths), float(scale), _ptr(ctx), _ptr(lse), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _ptr(dev_err), st),
+        check(_fn("mla_decode_absorb_fp4kv")(
+            d, _dt(q_tilde), B, T, _at(q_tilde), ldqt, _at(q_pe), ldqp, _at(c4), c4.stride(0), c4.stride(1),
+            _at(kv_scale), kv_scale.stride(0), kv_scale.stride(1), _at(k_r), k_r.stride(0), k_r.stride(1),
+            float(latent_scale), n_max, _at(lengths), float(scale), _at(ctx), _at(lse), _at(workspace),
+            workspace.numel() * workspace.element_size(), _at(dev_err), st),
             "mla_decode_absorb_fp4kv")
     return ctx
 
@@ -596,13 +642,13 @@ def mla_cache_weights(dims, q_tilde: torch.Tensor, q_pe: torch.Tensor, c_kv: tor
     tokens, added to decay * acc (float32 [B, n_max]; the step's own T rows start from nothing).  Queries
     [B, n_h, .] or [B, T, n_h, .]; lse is the decode's.  Returns out [B, n_max], which may be acc; entries
     at and behind lengths[b] are left as they were (zeros when out is allocated here)."""
-    d = _dims(dims)
+    d = _fast_dims(dims)
     if c_kv.dim() != 3:
         raise ValueError("c_kv must be [B, n_max, d_c]")
     B, n_max = c_kv.shape[0], c_kv.shape[1]
     _shape(c_kv, (B, n_max, d.d_c), q_tilde.dtype, "c_kv")
     _shape(k_r, (B, n_max, d.d_r), q_tilde.dtype, "k_r")
-    T, qt, ldqt, qp, ldqp = _queries(d, q_tilde, q_pe, B, n_max, lengths)
+    T, ldqt, ldqp = _queries(d, q_tilde, q_pe, B, lengths)
     _shape(lse, q_tilde.shape[:-1], torch.float32, "lse")
     if not lse.is_contiguous():
         raise ValueError("lse must be contiguous")
@@ -613,10 +659,10 @@ def mla_cache_weights(dims, q_tilde: torch.Tensor, q_pe: torch.Tensor, c_kv: tor
     with on:
         if out is None:
             out = torch.zeros((B, n_max), dtype=torch.float32, device=dev)
-        check(lib().mla_cache_weights(
-            d, _dt(q_tilde), B, T, _ptr(qt), ldqt, _ptr(qp), ldqp, _ptr(c_kv), c_kv.stride(0), c_kv.stride(1),
-            _ptr(k_r), k_r.stride(0), k_r.stride(1), n_max, _ptr(lengths), float(scale), _ptr(lse), _ptr(acc),
-            _bstride(acc, n_max), float(decay), _ptr(out), _bstride(out, n_max), _ptr(dev_err),
+        check(_fn("mla_cache_weights")(
+            d, _dt(q_tilde), B, T, _at(q_tilde), ldqt, _at(q_pe), ldqp, _at(c_kv), c_kv.stride(0), c_kv.stride(1),
+            _at(k_r), k_r.stride(0), k_r.stride(1), n_max, _at(lengths), float(scale), _at(lse), _at(acc),
+            _bstride(acc, n_max), float(decay), _at(out), _bstride(out, n_max), _at(dev_err),
             st), "mla_cache_weights")
     return out
 
@@ -627,9 +673,9 @@ def mla_cache_weights_fp4kv(dims, q_tilde: torch.Tensor, q_pe: torch.Tensor, c4:
                             out: Optional[torch.Tensor] = None, dev_err: Optional[torch.Tensor] = None,
                             stream=None) -> torch.Tensor:
     """mla_cache_weights over a 4-bit latent cache (planes as in mla_cache_append_fp4)."""
-    d = _dims(dims)
+    d = _fast_dims(dims)
     B, n_max = _fp4_planes(d, c4, kv_scale, k_r, q_tilde.dtype)
-    T, qt, ldqt, qp, ldqp = _queries(d, q_tilde, q_pe, B, n_max, lengths)
+    T, ldqt, ldqp = _queries(d, q_tilde, q_pe, B, lengths)
     _shape(lse, q_tilde.shape[:-1], torch.float32, "lse")
     if not lse.is_contiguous():
         raise ValueError("lse must be contiguous")
@@ -640,11 +686,11 @@ def mla_cache_weights_fp4kv(dims, q_tilde: torch.Tensor, q_pe: torch.Tensor, c4:
     with on:
         if out is None:
             out = torch.zeros((B, n_max), dtype=torch.float32, device=dev)
-        check(lib().mla_cache_weights_fp4kv(
-            d, _dt(q_tilde), B, T, _ptr(qt), ldqt, _ptr(qp), ldqp, _ptr(c4), c4.stride(0), c4.stride(1),
-            _ptr(kv_scale), kv_scale.stride(0), kv_scale.stride(1), _ptr(k_r), k_r.stride(0), k_r.stride(1),
-            float(latent_scale), n_max, _ptr(lengths), float(scale), _ptr(lse), _ptr(acc), _bstride(acc, n_max),
-            float(decay), _ptr(out), _bstride(out, n_max), _ptr(dev_err), st),
+        check(_fn("mla_cache_weights_fp4kv")(
+            d, _dt(q_tilde), B, T, _at(q_tilde), ldqt, _at(q_pe), ldqp, _at(c4), c4.stride(0), c4.stride(1),
+            _at(kv_scale), kv_scale.stride(0), kv_scale.stride(1), _at(k_r), k_r.stride(0), k_r.stride(1),
+            float(latent_scale), n_max, _at(lengths), float(scale), _at(lse), _at(acc), _bstride(acc, n_max),
+            float(decay), _at(out), _bstride(out, n_max), _at(dev_err), st),
             "mla_cache_weights_fp4kv")
     return out
 
@@ -687,9 +733,9 @@ def mla_cache_evict(planes: Sequence[torch.Tensor], acc: torch.Tensor, lengths: 
             new_lengths = torch.empty((B,), dtype=torch.int32, device=dev)
         if row_map is None:
             row_map = torch.empty((B, max(keep, 0)), dtype=torch.int32, device=dev)
-        check(lib().mla_cache_evict(B, n_max, rows, len(planes), _ptr(acc), _bstride(acc, n_max), _ptr(lengths),
-                                    int(keep), int(sink), int(recent), _ptr(new_lengths), _ptr(row_map),
-                                    _ptr(dev_err), st), "mla_cache_evict")
+        check(_fn("mla_cache_evict")(B, n_max, rows, len(planes), _at(acc), _bstride(acc, n_max), _at(lengths),
+                                    int(keep), int(sink), int(recent), _at(new_lengths), _at(row_map),
+                                    _at(dev_err), st), "mla_cache_evict")
     return new_lengths, row_map
 
 

@@ -158,6 +158,31 @@ struct EvictArgs {
   int32_t* err;
 };
 
+// The current device's index (below kMaxDevices) and multiprocessors, looked up once per device.
+constexpr int kMaxDevices = 64;
+inline int current_device() {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  return dev >= 0 && dev < kMaxDevices ? dev : 0;
+}
+inline int sm_count() {
+  static int cache[kMaxDevices] = {};
+  const int dev = current_device();
+  if (cache[dev] == 0) {
+    int n = 0;
+    cache[dev] = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0 ? n : 148;
+  }
+  return cache[dev];
+}
+// Raises a kernel's dynamic shared memory limit, once per device; `allowed` is the kernel's own record.
+inline cudaError_t allow_smem(const void* kernel, int bytes, int (&allowed)[kMaxDevices]) {
+  const int dev = current_device();
+  if (allowed[dev] >= bytes) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) allowed[dev] = bytes;
+  return e;
+}
+
 // Launch with programmatic stream serialization: the kernel may start while the preceding kernel
 // in the stream is still running, and synchronises with it through griddepcontrol.wait before it
 // touches that kernel's data (every kernel of this library does).

@@ -951,12 +951,7 @@ bool query_map(CUtensorMap* m, const void* base, int width, int R, int B, int64_
   const uint32_t box[3] = {64, kMyRows, 1};
   return make_tensor_map_bf16(m, base, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
-int max_pairs() {
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms > 1 ? sms / 2 : 1;
-}
+int max_pairs() { return sm_count() > 1 ? sm_count() / 2 : 1; }
 // Pairs that this shape can keep busy at most
 int shape_pairs(int pairs, int n_h, int B, int T, int n_max) {
   const int64_t groups = ((int64_t)n_h * T + kRows - 1) / kRows, tiles = groups * B * ((n_max + kTile - 1) / kTile);
@@ -964,10 +959,9 @@ int shape_pairs(int pairs, int n_h, int B, int T, int n_max) {
 }
 // Pairs that are resident at once (a GPC with an odd number of SMs leaves one over): one wave.  Per device.
 int resident_pairs() {
-  static int cache[64] = {};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev >= 0 && dev < 64 && cache[dev] > 0) return cache[dev];
+  static int cache[kMaxDevices] = {};
+  const int dev = current_device();
+  if (cache[dev] > 0) return cache[dev];
   int pairs = max_pairs(), active = 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs);
@@ -976,7 +970,7 @@ int resident_pairs() {
   if (cudaOccupancyMaxActiveClusters(&active, decode_kernel, &cfg) == cudaSuccess && active > 0 && active < pairs)
     pairs = active;
   cudaGetLastError();  // a failed query leaves no sticky state
-  if (dev >= 0 && dev < 64) cache[dev] = pairs;
+  cache[dev] = pairs;
   return pairs;
 }
 size_t table_bytes(int n_h, int B, int T) { return (size_t)B * (((size_t)n_h * T + kRows - 1) / kRows) * sizeof(int4); }
@@ -1000,7 +994,8 @@ cudaError_t decode_fp4_tc_launch(const Fp4DecodeArgs& a, void* ws, cudaStream_t 
   p.groups = (p.R + kRows - 1) / kRows;
   if (!query_map(&p.tm_q, a.q_tilde, kDC, p.R, a.B, a.ldqt) || !query_map(&p.tm_qp, a.q_pe, kDR, p.R, a.B, a.ldqp))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  static int allowed[kMaxDevices];
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(decode_kernel), kSmemBytes, allowed);
   if (e != cudaSuccess) return e;
   p.pairs = shape_pairs(resident_pairs(), a.n_h, a.B, a.T, a.n_max);
   p.scale_log2 = a.scale * kLog2e;

@@ -218,7 +218,8 @@ int evict_max_rows() { return kMaxRows; }
 
 cudaError_t evict_launch(const EvictArgs& a, cudaStream_t st) {
   const size_t smem = select_smem_bytes(a.n_max);
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static int allowed[kMaxDevices];
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(evict_select_kernel), (int)smem, allowed);
   if (e != cudaSuccess) return e;
   evict_select_kernel<<<a.B, kSelThreads, smem, st>>>(a);
   e = cudaGetLastError();

@@ -358,7 +358,8 @@ bool make_cache_map(CUtensorMap* m, const void* base, int width, int n_max, int 
 
 template <bool kFp4>
 cudaError_t launch(const Params& p, int grid, cudaStream_t st) {
-  const cudaError_t e = cudaFuncSetAttribute(weights_kernel<kFp4>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  static int allowed[kMaxDevices];
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(weights_kernel<kFp4>), kSmemBytes, allowed);
   if (e != cudaSuccess) return e;
   return launch_pdl(weights_kernel<kFp4>, dim3(grid), dim3(kFp4 ? kThreadsFp4 : kThreadsBf16), kSmemBytes, st, p);
 }
@@ -382,9 +383,7 @@ cudaError_t weights_tc_launch(const WeightsArgs& a, cudaStream_t st) {
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.lse = a.lse; p.acc = a.acc; p.acc_b = a.acc_b; p.decay = a.decay;
   p.out = a.out; p.out_b = a.out_b; p.err = a.err;
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int sms = sm_count();
   const int64_t tiles = (int64_t)a.B * ((a.n_max + kTile - 1) / kTile);
   const int grid = (int)(tiles < sms ? tiles : sms);
   return fp4 ? launch<true>(p, grid, st) : launch<false>(p, grid, st);
