@@ -28,6 +28,7 @@ namespace mla {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kMaxPairs = 64;  // rotary pairs: d_r <= 128
 constexpr float kDelta = 1.f / 524288.f;  // 2^-19
 
 __device__ __forceinline__ double warp_sum_f64(double v) {
@@ -124,19 +125,21 @@ __device__ __noinline__ void quantise_exact(const float (&x)[16], const float* g
   }
 }
 
+// Turns per position of each rotary pair, base^(-2j / d_r) / (2 pi), by the host: in the kernel the fp64
+// logarithm and exponentials took longer than a token's rows.
+struct RotaryTurns {
+  double turn[kMaxPairs];
+};
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads) append_fp4_kernel(AppendFp4Args a) {
+__global__ void __launch_bounds__(kThreads) append_fp4_kernel(const __grid_constant__ AppendFp4Args a,
+                                                              const __grid_constant__ RotaryTurns rot) {
   sm100::griddep_launch_dependents();
   sm100::griddep_wait();
   const int lane = threadIdx.x & 31;
   const int64_t n_rows = (int64_t)a.B * a.T;
   const int64_t stride = (int64_t)gridDim.x * (kThreads / 32);
   const int blocks = a.d_c / fp4::kBlock;
-  // turns per position of the lane's rotary pairs (lane, lane + 32)
-  double turn[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-    turn[k] = exp(-(2.0 * (lane + 32 * k) / a.d_r) * log((double)a.rope_base)) * 0.15915494309189533577;  // 1 / (2 pi)
   for (int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); w < n_rows; w += stride) {
     const int b = (int)(w / a.T), i = (int)(w % a.T);
     if (a.counts != nullptr) {
@@ -224,7 +227,7 @@ __global__ void __launch_bounds__(kThreads) append_fp4_kernel(AppendFp4Args a) {
     for (int k = 0; k < 2; ++k) {
       const int j = lane + 32 * k;
       if (j >= a.d_r / 2) continue;
-      const double t = (double)pos * turn[k];
+      const double t = (double)pos * rot.turn[j];
       float s, c;
       sincospif(2.f * (float)(t - rint(t)), &s, &c);
       k_dst[2 * j] = from_f32<T>(k0[k] * c - k1[k] * s);
@@ -298,14 +301,25 @@ __global__ void __launch_bounds__(256) read_fp4_kernel(ReadFp4Args a) {
 
 template <typename T>
 cudaError_t cache_append_fp4_launch(const AppendFp4Args& a, cudaStream_t st) {
-  const int64_t ctas = ((int64_t)a.B * a.T + kThreads / 32 - 1) / (kThreads / 32);
-  return launch_pdl(append_fp4_kernel<T>, dim3((unsigned)(ctas < 148 * 16 ? ctas : 148 * 16)), dim3(kThreads), 0, st, a);
+  // the last table made by this thread: a program appends with one base and width
+  static thread_local float base = 0.f;
+  static thread_local int d_r = 0;
+  static thread_local RotaryTurns rot;
+  if (base != a.rope_base || d_r != a.d_r) {
+    for (int j = 0; j < kMaxPairs; ++j)
+      rot.turn[j] = exp(-(2.0 * j / a.d_r) * log((double)a.rope_base)) * 0.15915494309189533577;  // 1 / (2 pi)
+    base = a.rope_base;
+    d_r = a.d_r;
+  }
+  const int64_t ctas = ((int64_t)a.B * a.T + kThreads / 32 - 1) / (kThreads / 32), most = 16 * sm_count();
+  return launch_pdl(append_fp4_kernel<T>, dim3((unsigned)(ctas < most ? ctas : most)), dim3(kThreads), 0, st, a, rot);
 }
 
 template <typename T>
 cudaError_t cache_read_fp4_launch(const ReadFp4Args& a, cudaStream_t st) {
   const int64_t ctas = ((int64_t)a.B * a.n * (a.d_c / fp4::kBlock) + 255) / 256;
-  return launch_pdl(read_fp4_kernel<T>, dim3((unsigned)(ctas < 148 * 8 ? ctas : 148 * 8)), dim3(256), 0, st, a);
+  const int64_t most = 8 * sm_count();
+  return launch_pdl(read_fp4_kernel<T>, dim3((unsigned)(ctas < most ? ctas : most)), dim3(256), 0, st, a);
 }
 
 template cudaError_t cache_append_fp4_launch<float>(const AppendFp4Args&, cudaStream_t);
