@@ -14,9 +14,10 @@
 // fall on the side that the formula puts it on.  The fp32 pass carries a relative error below
 // 32 * 2^-24 = 2^-19 (sum of up to 32 squares per lane and five exchanges, halved by the square root:
 // 19; reciprocal root 4; two products, the scale's reciprocal and the product with it 5).  It rounds
-// each quotient twice, moved down and up by 2^-19; where the two disagree (about one row in 150), or
-// where the sum of squares leaves fp32's safe range, the warp redoes the row in fp64.  fp64 results
-// reach the fp32 converters through round-to-odd, so the second rounding cannot undo the first.
+// each quotient twice, moved down and up by 2^-19; where the two disagree (about one row in 160), or
+// where the sum of squares leaves fp32's safe range, the warp redoes the row in fp64: the scale reaches the
+// fp32 converter through round-to-odd, so the second rounding cannot undo the first, and the codes come from
+// comparisons with the borders (quotients took most of the kernel's time on prompts).
 #include <math.h>
 
 #include "common.cuh"
@@ -44,23 +45,49 @@ __device__ __forceinline__ float to_odd(double v) {
   return f;
 }
 
-// 16 consecutive elements as fp32 (bf16 rows are 16-byte aligned, fp32 rows element-aligned).
-__device__ __forceinline__ void load16(const float* p, float (&x)[16]) {
+// A block of 16 consecutive elements (bf16 rows are 16-byte aligned, fp32 rows element-aligned) and a rotary pair,
+// as loaded and as fp32.
+template <typename T> struct Raw;
+template <> struct Raw<float> {
+  float x[16], k[2];
+};
+template <> struct Raw<__nv_bfloat16> {
+  uint4 x[2];
+  uint32_t k;
+};
+__device__ __forceinline__ void load16(const float* p, Raw<float>& r) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = p[i];
+  for (int i = 0; i < 16; ++i) r.x[i] = p[i];
 }
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&x)[16]) {
-  const uint4* v = reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, Raw<__nv_bfloat16>& r) {
+  r.x[0] = reinterpret_cast<const uint4*>(p)[0];
+  r.x[1] = reinterpret_cast<const uint4*>(p)[1];
+}
+__device__ __forceinline__ void load2(const float* p, Raw<float>& r) {
+  r.k[0] = p[0];
+  r.k[1] = p[1];
+}
+__device__ __forceinline__ void load2(const __nv_bfloat16* p, Raw<__nv_bfloat16>& r) {
+  r.k = *reinterpret_cast<const uint32_t*>(p);
+}
+__device__ __forceinline__ void widen(const Raw<float>& r, float (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = r.x[i];
+}
+__device__ __forceinline__ void widen(const Raw<__nv_bfloat16>& r, float (&x)[16]) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const uint4 u = v[k];
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const uint32_t w[4] = {r.x[k].x, r.x[k].y, r.x[k].z, r.x[k].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       x[8 * k + 2 * i] = __uint_as_float(w[i] << 16);
       x[8 * k + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
+}
+__device__ __forceinline__ float2 pair_of(const Raw<float>& r) { return make_float2(r.k[0], r.k[1]); }
+__device__ __forceinline__ float2 pair_of(const Raw<__nv_bfloat16>& r) {
+  return make_float2(__uint_as_float(r.k << 16), __uint_as_float(r.k & 0xffff0000u));
 }
 
 // NaN-keeping maximum of magnitudes.
@@ -71,13 +98,12 @@ __device__ __forceinline__ float max_abs(float m, float v) {
 }
 
 // One block in fp32; returns false when a rounding is too close to call.
-__device__ __forceinline__ bool quantise_fast(const float (&x)[16], const float* g, float mul, uint32_t (&code)[2],
+__device__ __forceinline__ bool quantise_fast(const float (&x)[16], const float (&g)[16], float mul, uint32_t (&code)[2],
                                               uint32_t& s8) {
   float y[16], m = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    y[i] = x[i] * mul;
-    if (g != nullptr) y[i] *= __ldg(g + i);
+    y[i] = x[i] * mul * g[i];
     m = max_abs(m, y[i]);
   }
   const float q = m * (1.f / 6.f);
@@ -97,31 +123,48 @@ __device__ __forceinline__ bool quantise_fast(const float (&x)[16], const float*
   return ok;
 }
 
-// One block in fp64.
-__device__ __noinline__ void quantise_exact(const float (&x)[16], const float* g, double mul, double unscale,
-                                            uint32_t (&code)[2], uint32_t& s8) {
-  double m = 0.0;
-  bool nan = false;
-  for (int i = 0; i < 16; ++i) {
-    double y = (double)x[i] * mul;
-    if (g != nullptr) y *= (double)g[i];
-    y *= unscale;
-    nan |= y != y;
-    m = fmax(m, fabs(y));
-  }
-  const float q = nan ? nanf("") : to_odd(m / 6.0);
-  s8 = fp4::to_scales(q, q) & 0xffu;
-  const double s = (double)fp4::scale_value(s8);
-  code[0] = code[1] = 0u;
-  if (!(s > 0.0)) return;
-  for (int i = 0; i < 16; i += 2) {
-    float r[2];
-    for (int k = 0; k < 2; ++k) {
-      double y = (double)x[i + k] * mul;
-      if (g != nullptr) y *= (double)g[i + k];
-      r[k] = to_odd(y * unscale / s);
+// A lane's blocks of a row in fp64, from the row itself: out of line, and without the fast path's registers.
+template <typename T, int NB>
+__device__ __noinline__ void quantise_exact(const AppendFp4Args& a, const T* row, uint8_t* c_dst, uint8_t* s_dst) {
+  const int lane = threadIdx.x & 31, blocks = a.d_c / fp4::kBlock;
+  double s64 = 0.0;
+  for (int k = 0; k < NB; ++k)
+    if (lane + 32 * k < blocks)
+      for (int j = 0; j < 16; ++j) {
+        const double v = (double)to_f32(row[16 * (lane + 32 * k) + j]);
+        s64 = fma(v, v, s64);
+      }
+  const double mul = 1.0 / sqrt(warp_sum_f64(s64) / a.d_c + (double)a.eps), unscale = 1.0 / (double)a.latent_scale;
+  for (int k = 0; k < NB; ++k) {
+    const int blk = lane + 32 * k;
+    if (blk >= blocks) break;
+    const T* x = row + 16 * blk;
+    const float* g = a.gain != nullptr ? a.gain + 16 * blk : nullptr;
+    double m = 0.0;
+    bool nan = false;
+    for (int i = 0; i < 16; ++i) {
+      const double y = (double)to_f32(x[i]) * mul * (g != nullptr ? (double)g[i] : 1.0) * unscale;
+      nan |= y != y;
+      m = fmax(m, fabs(y));
     }
-    code[i >> 3] |= fp4::to_codes(r[0], r[1]) << (4 * (i & 7));
+    const float q = nan ? nanf("") : to_odd(m / 6.0);
+    const uint32_t s8 = fp4::to_scales(q, q) & 0xffu;
+    const double s = (double)fp4::scale_value(s8);
+    s_dst[blk] = (uint8_t)s8;
+    // a code counts the borders that |y| has passed; a tie goes to the even code.  Border times scale is exact.
+    double border[7];
+    for (int e = 0; e < 7; ++e) border[e] = s * (e < 4 ? 0.25 + 0.5 * e : e == 4 ? 2.5 : e == 5 ? 3.5 : 5.0);
+    for (int i = 0; i < 16; i += 2) {
+      uint32_t byte = 0u;
+      for (int n = 0; n < 2; ++n) {
+        const double y = (double)to_f32(x[i + n]) * mul * (g != nullptr ? (double)g[i + n] : 1.0) * unscale, v = fabs(y);
+        uint32_t code = y < 0.0 ? 8u : 0u;
+        for (int e = 0; e < 7; ++e) code += (e & 1) ? v >= border[e] : v > border[e];
+        if (!(s > 0.0)) code = 0u;  // a zero or NaN scale
+        byte |= code << (4 * n);
+      }
+      c_dst[8 * blk + i / 2] = (uint8_t)byte;
+    }
   }
 }
 
@@ -131,107 +174,110 @@ struct RotaryTurns {
   double turn[kMaxPairs];
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) append_fp4_kernel(const __grid_constant__ AppendFp4Args a,
+// NB blocks of 16 features and NB rotary pairs per lane.
+template <typename T, int NB>
+__global__ void __launch_bounds__(kThreads, NB == 1 ? 6 : 3) append_fp4_kernel(const __grid_constant__ AppendFp4Args a,
                                                               const __grid_constant__ RotaryTurns rot) {
   sm100::griddep_launch_dependents();
   sm100::griddep_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t n_rows = (int64_t)a.B * a.T;
-  const int64_t stride = (int64_t)gridDim.x * (kThreads / 32);
+  const uint32_t n_rows = (uint32_t)a.B * (uint32_t)a.T, stride = gridDim.x * (kThreads / 32);
   const int blocks = a.d_c / fp4::kBlock;
-  for (int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); w < n_rows; w += stride) {
-    const int b = (int)(w / a.T), i = (int)(w % a.T);
-    if (a.counts != nullptr) {
-      const int n = a.counts[b];
-      if (n < 0 || n > a.T) {
-        if (lane == 0 && i == 0) raise_error(a.err, MLA_ERR_LENGTH);
-        continue;
-      }
-      if (i >= n) continue;
+  // a lane's blocks are the same in every row: their gains stay in registers (read again for every token, 64 bytes
+  // apart, they took more L1 lookups than the rows)
+  float g[NB][16];
+#pragma unroll
+  for (int k = 0; k < NB; ++k)
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      g[k][j] = a.gain != nullptr && lane + 32 * k < blocks ? __ldg(a.gain + 16 * (lane + 32 * k) + j) : 1.f;
+  // the next token's row and indices are on their way while a token is worked on
+  struct Token {
+    Raw<T> raw[NB];
+    const T* row;
+    int b, i, pos, dst, n;
+  };
+  auto fetch = [&](uint32_t w, Token& t) {
+    t.b = a.T == 1 ? (int)w : (int)(w / (uint32_t)a.T);
+    t.i = (int)(w - (uint32_t)t.b * (uint32_t)a.T);
+    t.pos = a.positions[t.b];
+    t.dst = a.rows != nullptr ? a.rows[t.b] : t.pos;
+    t.n = a.counts != nullptr ? a.counts[t.b] : a.T;
+    t.row = static_cast<const T*>(a.kv_a) + t.b * a.lda_b + t.i * a.lda;
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const int at = lane + 32 * k;
+      if (at < blocks) load16(t.row + at * fp4::kBlock, t.raw[k]);
+      if (at < a.d_r / 2) load2(t.row + a.d_c + 2 * at, t.raw[k]);
     }
-    const int p0 = a.positions[b];
-    const int64_t pos = (int64_t)p0 + i;
-    const int64_t dst = (a.rows != nullptr ? (int64_t)a.rows[b] : (int64_t)p0) + i;
-    if (p0 < 0 || dst < 0 || dst >= a.n_max) {  // would land outside the cache: report, write nothing
+  };
+  Token next;
+  const uint32_t first = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (first < n_rows) fetch(first, next);
+  for (uint32_t w = first; w < n_rows; w += stride) {
+    const Token t = next;
+    if (n_rows - w > stride) fetch(w + stride, next);
+    const int b = t.b, i = t.i;
+    const int64_t pos = (int64_t)t.pos + i, dst = (int64_t)t.dst + i;
+    if (t.n < 0 || t.n > a.T) {
+      if (lane == 0 && i == 0) raise_error(a.err, MLA_ERR_LENGTH);
+      continue;
+    }
+    if (i >= t.n) continue;
+    if (t.pos < 0 || dst < 0 || dst >= a.n_max) {  // would land outside the cache: report, write nothing
       if (lane == 0) raise_error(a.err, MLA_ERR_INDEX);
       continue;
     }
-    const T* row = static_cast<const T*>(a.kv_a) + b * a.lda_b + i * a.lda;
-    float x[2][16];
+    float x[NB][16];
     float ss = 0.f;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int blk = lane + 32 * k;
-      if (blk < blocks) {
-        load16(row + blk * fp4::kBlock, x[k]);
+    for (int k = 0; k < NB; ++k)
+      if (lane + 32 * k < blocks) {
+        widen(t.raw[k], x[k]);
 #pragma unroll
         for (int j = 0; j < 16; ++j) ss = fmaf(x[k][j], x[k][j], ss);
       }
-    }
-    // the rotary key's loads overlap the norm
-    const T* key = row + a.d_c;
-    float k0[2], k1[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int j = lane + 32 * k;
-      if (j < a.d_r / 2) {
-        k0[k] = to_f32(key[2 * j]);
-        k1[k] = to_f32(key[2 * j + 1]);
-      }
-    }
     ss = warp_sum(ss);
     const float inv = rsqrtf(ss / (float)a.d_c + a.eps) * (1.f / a.latent_scale);
-    uint32_t code[2][2], s8[2];
+    uint32_t code[NB][2], s8[NB];
     bool ok = ss > 1e-30f && ss < 1e36f;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < NB; ++k) {
       const int blk = lane + 32 * k;
       if (blk < blocks)
-        ok &= quantise_fast(x[k], a.gain != nullptr ? a.gain + blk * fp4::kBlock : nullptr, inv, code[k], s8[k]);
-    }
-    if (!__all_sync(0xffffffffu, ok)) {
-      double s64 = 0.0;
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (lane + 32 * k < blocks)
-          for (int j = 0; j < 16; ++j) s64 = fma((double)x[k][j], (double)x[k][j], s64);
-      s64 = warp_sum_f64(s64);
-      const double mul = 1.0 / sqrt(s64 / a.d_c + (double)a.eps);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int blk = lane + 32 * k;
-        if (blk < blocks)
-          quantise_exact(x[k], a.gain != nullptr ? a.gain + blk * fp4::kBlock : nullptr, mul,
-                         1.0 / (double)a.latent_scale, code[k], s8[k]);
-      }
+        ok &= quantise_fast(x[k], g[k], inv, code[k], s8[k]);
     }
     uint8_t* c_dst = a.c4 + b * a.c4_b + dst * a.c4_r;
     uint8_t* s_dst = a.sc + b * a.sc_b + dst * a.sc_r;
+    if (!__all_sync(0xffffffffu, ok)) {
+      quantise_exact<T, NB>(a, t.row, c_dst, s_dst);
+    } else {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int blk = lane + 32 * k;
-      if (blk >= blocks) continue;
-      if constexpr (sizeof(T) == 2) {  // bf16 caches are 16-byte aligned
-        *reinterpret_cast<uint2*>(c_dst + 8 * blk) = make_uint2(code[k][0], code[k][1]);
-      } else {
+      for (int k = 0; k < NB; ++k) {
+        const int blk = lane + 32 * k;
+        if (blk >= blocks) continue;
+        if constexpr (sizeof(T) == 2) {  // bf16 caches are 16-byte aligned
+          *reinterpret_cast<uint2*>(c_dst + 8 * blk) = make_uint2(code[k][0], code[k][1]);
+        } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) c_dst[8 * blk + j] = (uint8_t)(code[k][j >> 2] >> (8 * (j & 3)));
+          for (int j = 0; j < 8; ++j) c_dst[8 * blk + j] = (uint8_t)(code[k][j >> 2] >> (8 * (j & 3)));
+        }
+        s_dst[blk] = (uint8_t)s8[k];
       }
-      s_dst[blk] = (uint8_t)s8[k];
     }
     // rotary key: the angle in turns, reduced in fp64 (at position 65535 an fp32 product is off by
     // 4e-3 rad), then sin and cos of at most half a turn in fp32
     T* k_dst = static_cast<T*>(a.k_r) + b * a.kr_b + dst * a.kr_r;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < NB; ++k) {
       const int j = lane + 32 * k;
       if (j >= a.d_r / 2) continue;
-      const double t = (double)pos * rot.turn[j];
+      const double turns = (double)pos * rot.turn[j];
+      const float2 y = pair_of(t.raw[k]);
       float s, c;
-      sincospif(2.f * (float)(t - rint(t)), &s, &c);
-      k_dst[2 * j] = from_f32<T>(k0[k] * c - k1[k] * s);
-      k_dst[2 * j + 1] = from_f32<T>(k0[k] * s + k1[k] * c);
+      sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
+      k_dst[2 * j] = from_f32<T>(y.x * c - y.y * s);
+      k_dst[2 * j + 1] = from_f32<T>(y.x * s + y.y * c);
     }
   }
 }
@@ -311,8 +357,11 @@ cudaError_t cache_append_fp4_launch(const AppendFp4Args& a, cudaStream_t st) {
     base = a.rope_base;
     d_r = a.d_r;
   }
-  const int64_t ctas = ((int64_t)a.B * a.T + kThreads / 32 - 1) / (kThreads / 32), most = 16 * sm_count();
-  return launch_pdl(append_fp4_kernel<T>, dim3((unsigned)(ctas < most ? ctas : most)), dim3(kThreads), 0, st, a, rot);
+  const int64_t ctas = ((int64_t)a.B * a.T + kThreads / 32 - 1) / (kThreads / 32), most = 6 * sm_count();
+  const dim3 grid((unsigned)(ctas < most ? ctas : most));
+  // the usual widths leave a lane one block and one pair, and half the registers of two
+  if (a.d_c <= 512 && a.d_r <= 64) return launch_pdl(append_fp4_kernel<T, 1>, grid, dim3(kThreads), 0, st, a, rot);
+  return launch_pdl(append_fp4_kernel<T, 2>, grid, dim3(kThreads), 0, st, a, rot);
 }
 
 template <typename T>

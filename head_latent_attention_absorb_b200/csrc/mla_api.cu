@@ -564,6 +564,7 @@ mla_status mla_cache_append_fp4(mla_dims dims, mla_dtype dtype, int32_t B, int32
   g_msg[0] = 0;
   MLA_TRY(check_cache_dims(dims, dtype, true));
   if (B <= 0 || T <= 0 || n_max <= 0) return fail(MLA_ERR_INVALID_ARG, "B, T and n_max must be positive");
+  if ((int64_t)B * T > INT32_MAX) return fail(MLA_ERR_UNSUPPORTED, "B * T must stay below 2^31");
   if (!kv_a || !positions || !k_r) return fail(MLA_ERR_INVALID_ARG, "NULL pointer");
   if (dims.d_r % 2 != 0) return fail(MLA_ERR_INVALID_ARG, "d_r must be even (rotary pairs)");
   if (lda < (int64_t)dims.d_c + dims.d_r || lda_b < 0)
