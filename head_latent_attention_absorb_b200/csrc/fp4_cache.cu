@@ -14,8 +14,8 @@
 // fall on the side that the formula puts it on.  The fp32 pass carries a relative error below
 // 32 * 2^-24 = 2^-19 (sum of up to 32 squares per lane and five exchanges, halved by the square root:
 // 19; reciprocal root 4; two products, the scale's reciprocal and the product with it 5).  It rounds
-// each quotient twice, moved down and up by 2^-19; where the two disagree (about one row in 160), or
-// where the sum of squares leaves fp32's safe range, the warp redoes the row in fp64: the scale reaches the
+// each quotient twice, moved down and up by 2^-19; where the two disagree (in about one row of 160), or
+// where the sum of squares leaves fp32's safe range, the warp redoes the block in fp64: the scale reaches the
 // fp32 converter through round-to-odd, so the second rounding cannot undo the first, and the codes come from
 // comparisons with the borders (quotients took most of the kernel's time on prompts).
 #include <math.h>
@@ -90,6 +90,14 @@ __device__ __forceinline__ float2 pair_of(const Raw<__nv_bfloat16>& r) {
   return make_float2(__uint_as_float(r.k << 16), __uint_as_float(r.k & 0xffff0000u));
 }
 
+__device__ __forceinline__ void store2(float* p, float a, float b) {
+  p[0] = a;
+  p[1] = b;
+}
+__device__ __forceinline__ void store2(__nv_bfloat16* p, float a, float b) {
+  *reinterpret_cast<uint32_t*>(p) = sm100::pack_bf16x2(a, b);
+}
+
 // NaN-keeping maximum of magnitudes.
 __device__ __forceinline__ float max_abs(float m, float v) {
   float r;
@@ -98,12 +106,13 @@ __device__ __forceinline__ float max_abs(float m, float v) {
 }
 
 // One block in fp32; returns false when a rounding is too close to call.
-__device__ __forceinline__ bool quantise_fast(const float (&x)[16], const float (&g)[16], float mul, uint32_t (&code)[2],
+__device__ __forceinline__ bool quantise_fast(const float (&x)[16], const float* g, float mul, uint32_t (&code)[2],
                                               uint32_t& s8) {
   float y[16], m = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    y[i] = x[i] * mul * g[i];
+    y[i] = x[i] * mul;
+    if (g != nullptr) y[i] *= g[32 * i];
     m = max_abs(m, y[i]);
   }
   const float q = m * (1.f / 6.f);
@@ -123,49 +132,39 @@ __device__ __forceinline__ bool quantise_fast(const float (&x)[16], const float 
   return ok;
 }
 
-// A lane's blocks of a row in fp64, from the row itself: out of line, and without the fast path's registers.
+// The blocks of a row whose bits are set in `redo` (bit l of word k: block l + 32 k), in fp64, 16 lanes to a block.
 template <typename T, int NB>
-__device__ __noinline__ void quantise_exact(const AppendFp4Args& a, const T* row, uint8_t* c_dst, uint8_t* s_dst) {
-  const int lane = threadIdx.x & 31, blocks = a.d_c / fp4::kBlock;
+__device__ __noinline__ void quantise_exact(const AppendFp4Args& a, const T* row, const uint32_t (&redo)[NB], uint8_t* c_dst,
+                                            uint8_t* s_dst) {
+  const int lane = threadIdx.x & 31, e = lane & 15;
   double s64 = 0.0;
-  for (int k = 0; k < NB; ++k)
-    if (lane + 32 * k < blocks)
-      for (int j = 0; j < 16; ++j) {
-        const double v = (double)to_f32(row[16 * (lane + 32 * k) + j]);
-        s64 = fma(v, v, s64);
-      }
-  const double mul = 1.0 / sqrt(warp_sum_f64(s64) / a.d_c + (double)a.eps), unscale = 1.0 / (double)a.latent_scale;
-  for (int k = 0; k < NB; ++k) {
-    const int blk = lane + 32 * k;
-    if (blk >= blocks) break;
-    const T* x = row + 16 * blk;
-    const float* g = a.gain != nullptr ? a.gain + 16 * blk : nullptr;
-    double m = 0.0;
-    bool nan = false;
-    for (int i = 0; i < 16; ++i) {
-      const double y = (double)to_f32(x[i]) * mul * (g != nullptr ? (double)g[i] : 1.0) * unscale;
-      nan |= y != y;
-      m = fmax(m, fabs(y));
-    }
-    const float q = nan ? nanf("") : to_odd(m / 6.0);
-    const uint32_t s8 = fp4::to_scales(q, q) & 0xffu;
-    const double s = (double)fp4::scale_value(s8);
-    s_dst[blk] = (uint8_t)s8;
-    // a code counts the borders that |y| has passed; a tie goes to the even code.  Border times scale is exact.
-    double border[7];
-    for (int e = 0; e < 7; ++e) border[e] = s * (e < 4 ? 0.25 + 0.5 * e : e == 4 ? 2.5 : e == 5 ? 3.5 : 5.0);
-    for (int i = 0; i < 16; i += 2) {
-      uint32_t byte = 0u;
-      for (int n = 0; n < 2; ++n) {
-        const double y = (double)to_f32(x[i + n]) * mul * (g != nullptr ? (double)g[i + n] : 1.0) * unscale, v = fabs(y);
-        uint32_t code = y < 0.0 ? 8u : 0u;
-        for (int e = 0; e < 7; ++e) code += (e & 1) ? v >= border[e] : v > border[e];
-        if (!(s > 0.0)) code = 0u;  // a zero or NaN scale
-        byte |= code << (4 * n);
-      }
-      c_dst[8 * blk + i / 2] = (uint8_t)byte;
-    }
+  for (int f = lane; f < a.d_c; f += 32) {
+    const double v = (double)to_f32(row[f]);
+    s64 = fma(v, v, s64);
   }
+  const double mul = 1.0 / sqrt(warp_sum_f64(s64) / a.d_c + (double)a.eps), unscale = 1.0 / (double)a.latent_scale;
+  for (int k = 0; k < NB; ++k)
+    for (uint32_t left = redo[k]; left != 0u; left &= left - 1) {
+      const int blk = 32 * k + __ffs(left) - 1, f = 16 * blk + e;
+      double y = (double)to_f32(row[f]) * mul;
+      if (a.gain != nullptr) y *= (double)a.gain[f];
+      y *= unscale;
+      double m = fabs(y);
+      for (int o = 8; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const bool nan = __any_sync(0xffffffffu, y != y);
+      const float q = nan ? nanf("") : to_odd(m / 6.0);
+      const uint32_t s8 = fp4::to_scales(q, q) & 0xffu;
+      const double s = (double)fp4::scale_value(s8), v = fabs(y);
+      // a code counts the borders that |y| has passed; a tie goes to the even code.  Border times scale is exact.
+      uint32_t code = 0u;
+      if (s > 0.0) {  // (a zero or NaN scale: all codes zero)
+        code = (v > 0.25 * s) + (v >= 0.75 * s) + (v > 1.25 * s) + (v >= 1.75 * s) + (v > 2.5 * s) + (v >= 3.5 * s) + (v > 5.0 * s);
+        code |= y < 0.0 ? 8u : 0u;
+      }
+      const uint32_t high = __shfl_down_sync(0xffffffffu, code, 1);
+      if (lane < 16 && (lane & 1) == 0) c_dst[8 * blk + lane / 2] = (uint8_t)(code | high << 4);
+      if (lane == 0) s_dst[blk] = (uint8_t)s8;
+    }
 }
 
 // Turns per position of each rotary pair, base^(-2j / d_r) / (2 pi), by the host: in the kernel the fp64
@@ -176,21 +175,20 @@ struct RotaryTurns {
 
 // NB blocks of 16 features and NB rotary pairs per lane.
 template <typename T, int NB>
-__global__ void __launch_bounds__(kThreads, NB == 1 ? 6 : 3) append_fp4_kernel(const __grid_constant__ AppendFp4Args a,
+__global__ void __launch_bounds__(kThreads, NB == 1 ? 8 : 4) append_fp4_kernel(const __grid_constant__ AppendFp4Args a,
                                                               const __grid_constant__ RotaryTurns rot) {
   sm100::griddep_launch_dependents();
   sm100::griddep_wait();
   const int lane = threadIdx.x & 31;
   const uint32_t n_rows = (uint32_t)a.B * (uint32_t)a.T, stride = gridDim.x * (kThreads / 32);
   const int blocks = a.d_c / fp4::kBlock;
-  // a lane's blocks are the same in every row: their gains stay in registers (read again for every token, 64 bytes
-  // apart, they took more L1 lookups than the rows)
-  float g[NB][16];
-#pragma unroll
-  for (int k = 0; k < NB; ++k)
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      g[k][j] = a.gain != nullptr && lane + 32 * k < blocks ? __ldg(a.gain + 16 * (lane + 32 * k) + j) : 1.f;
+  // the gains by lane and element: read from global memory for every token, 64 bytes apart, they took more L1
+  // lookups than the rows, and in registers they cost a third of the resident warps
+  __shared__ float gain[NB][16][32];
+  if (a.gain != nullptr) {
+    for (int f = threadIdx.x; f < a.d_c; f += kThreads) gain[f >> 9][f & 15][(f >> 4) & 31] = a.gain[f];
+    __syncthreads();
+  }
   // the next token's row and indices are on their way while a token is worked on
   struct Token {
     Raw<T> raw[NB];
@@ -240,31 +238,30 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 6 : 3) append_fp4_kernel(c
     ss = warp_sum(ss);
     const float inv = rsqrtf(ss / (float)a.d_c + a.eps) * (1.f / a.latent_scale);
     uint32_t code[NB][2], s8[NB];
-    bool ok = ss > 1e-30f && ss < 1e36f;
+    const bool safe = ss > 1e-30f && ss < 1e36f;
+    uint8_t* c_dst = a.c4 + b * a.c4_b + dst * a.c4_r;
+    uint8_t* s_dst = a.sc + b * a.sc_b + dst * a.sc_r;
+    uint32_t redo[NB], any = 0u;
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
       const int blk = lane + 32 * k;
-      if (blk < blocks)
-        ok &= quantise_fast(x[k], g[k], inv, code[k], s8[k]);
-    }
-    uint8_t* c_dst = a.c4 + b * a.c4_b + dst * a.c4_r;
-    uint8_t* s_dst = a.sc + b * a.sc_b + dst * a.sc_r;
-    if (!__all_sync(0xffffffffu, ok)) {
-      quantise_exact<T, NB>(a, t.row, c_dst, s_dst);
-    } else {
+      bool ok = true;
+      if (blk < blocks) {
+        ok = quantise_fast(x[k], a.gain != nullptr ? &gain[k][0][lane] : nullptr, inv, code[k], s8[k]) && safe;
+        if (ok) {
+          if constexpr (sizeof(T) == 2) {  // bf16 caches are 16-byte aligned
+            *reinterpret_cast<uint2*>(c_dst + 8 * blk) = make_uint2(code[k][0], code[k][1]);
+          } else {
 #pragma unroll
-      for (int k = 0; k < NB; ++k) {
-        const int blk = lane + 32 * k;
-        if (blk >= blocks) continue;
-        if constexpr (sizeof(T) == 2) {  // bf16 caches are 16-byte aligned
-          *reinterpret_cast<uint2*>(c_dst + 8 * blk) = make_uint2(code[k][0], code[k][1]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) c_dst[8 * blk + j] = (uint8_t)(code[k][j >> 2] >> (8 * (j & 3)));
+            for (int j = 0; j < 8; ++j) c_dst[8 * blk + j] = (uint8_t)(code[k][j >> 2] >> (8 * (j & 3)));
+          }
+          s_dst[blk] = (uint8_t)s8[k];
         }
-        s_dst[blk] = (uint8_t)s8[k];
       }
+      redo[k] = __ballot_sync(0xffffffffu, !ok);
+      any |= redo[k];
     }
+    if (any != 0u) quantise_exact<T, NB>(a, t.row, redo, c_dst, s_dst);
     // rotary key: the angle in turns, reduced in fp64 (at position 65535 an fp32 product is off by
     // 4e-3 rad), then sin and cos of at most half a turn in fp32
     T* k_dst = static_cast<T*>(a.k_r) + b * a.kr_b + dst * a.kr_r;
@@ -276,8 +273,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 6 : 3) append_fp4_kernel(c
       const float2 y = pair_of(t.raw[k]);
       float s, c;
       sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
-      k_dst[2 * j] = from_f32<T>(y.x * c - y.y * s);
-      k_dst[2 * j + 1] = from_f32<T>(y.x * s + y.y * c);
+      store2(k_dst + 2 * j, y.x * c - y.y * s, y.x * s + y.y * c);
     }
   }
 }
@@ -357,7 +353,7 @@ cudaError_t cache_append_fp4_launch(const AppendFp4Args& a, cudaStream_t st) {
     base = a.rope_base;
     d_r = a.d_r;
   }
-  const int64_t ctas = ((int64_t)a.B * a.T + kThreads / 32 - 1) / (kThreads / 32), most = 6 * sm_count();
+  const int64_t ctas = ((int64_t)a.B * a.T + kThreads / 32 - 1) / (kThreads / 32), most = 8 * sm_count();
   const dim3 grid((unsigned)(ctas < most ? ctas : most));
   // the usual widths leave a lane one block and one pair, and half the registers of two
   if (a.d_c <= 512 && a.d_r <= 64) return launch_pdl(append_fp4_kernel<T, 1>, grid, dim3(kThreads), 0, st, a, rot);
