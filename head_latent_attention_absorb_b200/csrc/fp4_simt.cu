@@ -18,6 +18,8 @@ namespace mla {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kAhead = 4;      // rows that a warp of the decode works on at once
+constexpr int kRowsSplit = 16;  // rows of a split while there are few of them
 
 // The lane's blocks of latent row t of sequence b (kFp4: decoded; otherwise in the element type).
 template <typename T, int NB, bool kFp4>
@@ -54,21 +56,37 @@ __device__ __forceinline__ void load_row(const QueryArgs& a, int b, int t, int l
   }
 }
 
-// The lane's share of q~ . c_t + q_pe . k^R_t of query row r, summed over the warp.
+// A lane's features of query row r.
 template <typename T, int NB>
-__device__ __forceinline__ float score(const QueryArgs& a, int64_t r, const T* k_row, int lane,
+struct Query {
+  float c[NB][16], pe[4];  // d_r <= 128
+  __device__ __forceinline__ void load(const QueryArgs& a, int64_t r, int lane) {
+    const T* q = static_cast<const T*>(a.q_tilde) + r * a.ldqt;
+    const T* qp = static_cast<const T*>(a.q_pe) + r * a.ldqp;
+#pragma unroll
+    for (int k = 0; k < NB; ++k)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int f = 16 * (lane + 32 * k) + i;
+        c[k][i] = f < a.d_c ? to_f32(q[f]) : 0.f;
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pe[i] = lane + 32 * i < a.d_r ? to_f32(qp[lane + 32 * i]) : 0.f;
+  }
+};
+
+// scale (q~ . c_t + q_pe . k^R_t), summed over the warp.  (load_row leaves zeros past d_c.)
+template <typename T, int NB>
+__device__ __forceinline__ float score(const QueryArgs& a, const Query<T, NB>& q, const T* k_row, int lane,
                                        const float (&c)[NB][16]) {
-  const T* q = static_cast<const T*>(a.q_tilde) + r * a.ldqt;
-  const T* qp = static_cast<const T*>(a.q_pe) + r * a.ldqp;
   float dot = 0.f;
 #pragma unroll
   for (int k = 0; k < NB; ++k)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int f = 16 * (lane + 32 * k) + i;
-      if (f < a.d_c) dot = fmaf(to_f32(q[f]), c[k][i], dot);
-    }
-  for (int f = lane; f < a.d_r; f += 32) dot = fmaf(to_f32(qp[f]), to_f32(k_row[f]), dot);
+    for (int i = 0; i < 16; ++i) dot = fmaf(q.c[k][i], c[k][i], dot);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (lane + 32 * i < a.d_r) dot = fmaf(q.pe[i], to_f32(k_row[lane + 32 * i]), dot);
   return warp_sum(dot) * a.scale;
 }
 
@@ -92,19 +110,42 @@ __global__ void __launch_bounds__(32 * kWarps) decode_fp4_simt(Fp4DecodeArgs a, 
   for (int k = 0; k < NB; ++k)
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[k][i] = 0.f;
+  Query<T, NB> query;
+  query.load(a, r, lane);
   float m = -INFINITY, l = 0.f;
-  for (int t = t0; t < t1; ++t) {
-    float c[NB][16];
-    load_row<T, NB, true>(a, b, t, lane, c);
-    const float z = score<T, NB>(a, r, static_cast<const T*>(a.kv.k_r) + b * a.kv.kr_b + t * a.kv.kr_r, lane, c);
-    const float m_new = fmaxf(m, z);
-    const float corr = m_new > -INFINITY ? expf(m - m_new) : 1.f;
-    const float p = m_new > -INFINITY ? expf(z - m_new) : (z != z ? z : 0.f);
-    l = fmaf(l, corr, p);
+  // four rows at a time: their loads and sums overlap, and the running maximum is settled once
+  for (int t = t0; t < t1; t += kAhead) {
+    float c[kAhead][NB][16], z[kAhead];
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) load_row<T, NB, true>(a, b, min(t + e, t1 - 1), lane, c[e]);
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+      const int row = min(t + e, t1 - 1);
+      z[e] = score<T, NB>(a, query, static_cast<const T*>(a.kv.k_r) + b * a.kv.kr_b + row * a.kv.kr_r, lane, c[e]);
+    }
+    float m_new = m;
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e)
+      if (t + e < t1) m_new = fmaxf(m_new, z[e]);
+    const bool none = m_new == -INFINITY;  // nothing to weigh yet (NaN scores pass through below)
+    const float corr = none ? 1.f : expf(m - m_new);
+    l *= corr;
+    float p[kAhead];
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+      p[e] = t + e >= t1 ? 0.f : none ? (z[e] != z[e] ? z[e] : 0.f) : expf(z[e] - m_new);
+      l += p[e];
+    }
 #pragma unroll
     for (int k = 0; k < NB; ++k)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) acc[k][i] = fmaf(acc[k][i], corr, p * c[k][i]);
+      for (int i = 0; i < 16; ++i) {
+        float v = acc[k][i] * corr;
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e)
+          if (t + e < t1) v = fmaf(p[e], c[e][k][i], v);
+        acc[k][i] = v;
+      }
     m = m_new;
   }
   const bool whole = n_splits == 1;
@@ -169,7 +210,9 @@ __global__ void __launch_bounds__(32 * kWarps) weights_simt(WeightsArgs a) {
     for (int h = 0; h < a.n_h; ++h) {
       const int64_t r = ((int64_t)b * a.T + s) * a.n_h + h;
       const float lse = a.lse[r];
-      const float z = score<T, NB>(a, r, k_row, lane, c);
+      Query<T, NB> query;
+      query.load(a, r, lane);
+      const float z = score<T, NB>(a, query, k_row, lane, c);
       if (lse != -INFINITY) w += expf(z - lse);  // a row without a softmax gave no weight
     }
   if (lane != 0) return;
@@ -181,8 +224,9 @@ __global__ void __launch_bounds__(32 * kWarps) weights_simt(WeightsArgs a) {
 }  // namespace
 
 int decode_fp4_simt_splits(int B, int n_max) {
-  // enough (head group, query, split) blocks to cover the GPU a few times over
-  const int by_rows = (n_max + 255) / 256, want = (4 * 148 + B - 1) / B;
+  // a warp's rows are a chain of loads and sums, about 2 us for four of them: short splits while the GPU has room
+  // for more of them, then enough (head group, query, split) blocks to cover it a few times over
+  const int by_rows = (n_max + kRowsSplit - 1) / kRowsSplit, want = (4 * 148 + B - 1) / B;
   const int s = by_rows < want ? by_rows : want;
   return s < 1 ? 1 : s > 64 ? 64 : s;
 }
