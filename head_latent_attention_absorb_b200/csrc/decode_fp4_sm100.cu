@@ -26,8 +26,7 @@
 //   the scores are done.  Then X holds the values of the tile's first 64 rows and Y of its last 64, in both CTAs.
 // * TMEM: context 256 columns, scores two buffers of 64, query features 0..255 128 columns (A operand, in both
 //   lane halves).
-// * Thirteen warps decode: 16-byte loads of codes one tile ahead in registers (a warp of its
-//   own brings the rows to L2 four tiles ahead), cvt to fp16, one product with the block's scale, stores in the
+// * Thirteen warps decode: 16-byte loads of codes one tile ahead in registers, cvt to fp16, one product with the block's scale, stores in the
 //   128-byte-swizzled layout.
 // * MMA order S(t + 1), O(t), S(t + 2), ...: the softmax of tile t runs under O(t - 1) and S(t + 1).  (With one
 //   score buffer S(t + 1) waited for both CTAs to have read S(t): an arrival at the other CTA takes some hundred
@@ -69,22 +68,21 @@ constexpr int kPOff = kQOff + 5 * kSlabBytes;    // probabilities of the first a
 constexpr int kSmemOff = kPOff + 2 * kSlabBytes;
 static_assert(kQTmemSlabs * kSlabBytes <= kRegion, "the query for TMEM is staged in a buffer of region X");
 static_assert(kMyRows * kDC * 4 <= kRopeOff, "the partial context is staged in the regions");
-constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kXWarp0 = 9, kYWarp0 = 13, kVWarp0 = 17, kRopeWarp = 21, kPrefetchWarp = 22;
-constexpr int kThreads = 32 * (kPrefetchWarp + 1);
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kXWarp0 = 9, kYWarp0 = 13, kVWarp0 = 17, kRopeWarp = 21;
+constexpr int kThreads = 32 * (kRopeWarp + 1);
 constexpr uint32_t kTmemCols = 512, kColO = 0, kColS = 256, kColQ = 384;  // scores: two buffers of 64
 // Probabilities are 2^(z - ref): ref is set kRaise below the largest score so far (log2 units) and moved up
 // only when a score passes it by kRescale.  So they reach 2^15 at most (fp16 ends at 2^16), the sum is at
 // least 2^kRaise, and a probability that fp16's subnormals round (2^-25) is off by 2^-32 of the sum.
 constexpr float kRaise = 7.f, kRescale = 15.f;
-constexpr int kPrefetch = 4;                     // tiles that L2 is ahead of the decode warps
 constexpr int kPlanRegs = 3;                     // items per lane that the chunk search holds (more than the pairs)
 constexpr int kSwitchTiles = 3;                  // what a second piece costs a CTA, in tiles
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-struct Params {
-  CUtensorMap tm_q;   // (d_c, R, B) query rows, box (64, 64, 1), 128-byte swizzle: rows past R read as zeros
-  CUtensorMap tm_qp;  // (d_r, R, B), same box
+// The roles read their arguments from shared memory: handed to functions that are not inlined, a reference to the
+// kernel's parameters becomes loads through L1, some hundred cycles each.
+struct Args {
   CacheView kv;
   const int32_t* lengths;
   int B, T, n_h, n_max, R, groups, pairs;
@@ -96,25 +94,34 @@ struct Params {
   float* ws_o;    // [slots][4 quarters of the features][min(R, 128)][128], 16-byte chunk j of row r at (j + r) % 32
   int32_t* err;
 };
+struct Params {
+  CUtensorMap tm_q;   // (d_c, R, B) query rows, box (64, 64, 1), 128-byte swizzle: rows past R read as zeros
+  CUtensorMap tm_qp;  // (d_r, R, B), same box
+  Args a;
+};
 
 // An item is a group of up to 128 query rows of one sequence.  Keys its last row sees, 0 for a bad length.
-__device__ __forceinline__ int item_keys(const Params& p, int i) {
-  const int len = p.lengths[i / p.groups];
+__device__ __forceinline__ int item_keys(const Args& p, int b, int g) {
+  const int len = p.lengths[b];
   if (len < p.T || len > p.n_max) return 0;
-  const int g = i % p.groups;
   return g == p.groups - 1 ? len : len - p.T + (kRows * (g + 1) - 1) / p.n_h + 1;
 }
-__device__ __forceinline__ int item_tiles(const Params& p, int i) { return (item_keys(p, i) + kTile - 1) / kTile; }
+__device__ __noinline__ int item_tiles(const Args& p, int i) {
+  const int b = p.groups == 1 ? i : i / p.groups;
+  return (item_keys(p, b, i - b * p.groups) + kTile - 1) / kTile;
+}
 
 // A CTA pair's share: pieces of items.
 struct Plan {
-  long long lo, hi, tb, total;  // tiles [lo, hi) of all items' tiles laid end to end; first tile of `item`
-  int item, chunk, c0, n;       // chunk > 0: one piece, the (pair - c0)-th of item's n chunks
-  int nc;                       // pairs that have work
+  int lo, hi, tb;          // tiles [lo, hi) of all items' tiles laid end to end; first tile of `item`
+  int item, chunk, c0, n;  // chunk > 0: one piece, the (pair - c0)-th of item's n chunks
+  int nc, q, rem;          // pairs that have work; total tiles = q nc + rem
 };
 struct Piece {
-  int item, begin, end, tiles;  // item < 0: none left
-  int slot, c0, n;              // where its partial goes; first pair and number of the item's pieces
+  int item;              // < 0: none left
+  int b, g, len;         // its sequence, group of query rows, and the sequence's length
+  int begin, n;          // first tile, tiles
+  int slot, c0, pieces;  // where its partial goes; first pair and number of the item's pieces
 };
 
 struct Smem {
@@ -125,10 +132,11 @@ struct Smem {
   uint64_t x_empty[kXBufs], y_empty[kYBufs], rope_empty, s_full[2], pv_done, drain;
   uint64_t q_full, q_placed;
   float share[2][4][kMyRows];          // exchange between the four threads of a row
+  Args args;
   Plan plan;
-  Piece piece;
+  Piece piece[2];  // the one at hand, the next one
   uint32_t tmem_base;
-  int abort, never, progress;
+  int abort, never;
 };
 constexpr int kSmemBytes = kSmemOff + (int)sizeof(Smem);
 static_assert(kSmemBytes <= 232448, "shared memory above 227 KB");
@@ -162,21 +170,53 @@ __device__ __forceinline__ void arrive_even(uint64_t& bar, uint32_t rank) {
     mbar_arrive_remote_cta(mapa(smem_u32(&bar), 0));
 }
 
-// total c / nc, in 32 bits where they hold the product.
-__device__ __forceinline__ long long share(long long total, int c, int nc) {
-  return total < (1 << 22) ? (long long)((uint32_t)total * (uint32_t)c / (uint32_t)nc) : total * c / nc;
-}
-// The pair that holds tile t: ((t + 1) nc - 1) / total.
-__device__ __forceinline__ int holder(long long t, long long total, int nc) {
-  return total < (1 << 22) ? (int)(((uint32_t)(t + 1) * (uint32_t)nc - 1u) / (uint32_t)total)
-                           : (int)(((t + 1) * nc - 1) / total);
+// First tile of pair c's share: floor(total c / nc).  (The launch refuses totals of 2^31 tiles.)
+__device__ __forceinline__ int share(const Plan& s, int c) { return s.q * c + s.rem * c / s.nc; }
+// The pair whose share holds tile t.
+__device__ __forceinline__ int holder(const Plan& s, int t) {
+  int c = t / (s.q + 1);
+  while (c + 1 < s.nc && share(s, c + 1) <= t) ++c;
+  return c;
 }
 
-// One warp: the share of pair c.
-__device__ __noinline__ void make_plan(const Params& p, int c, Plan* out) {
+// One thread: the next piece of pair c.
+__device__ __noinline__ void next_piece(const Args& p, int c, Plan& s, Piece& r) {
+  const int items = p.B * p.groups;
+  r.item = -1;
+  if (s.chunk > 0) {
+    if (s.item >= items) return;
+    r.item = s.item;
+    r.begin = (c - s.c0) * s.chunk;
+    r.n = min(s.chunk, item_tiles(p, s.item) - r.begin);
+    r.slot = 2 * c;
+    r.c0 = s.c0;
+    r.pieces = s.n;
+    s.item = items;
+  } else {
+#pragma unroll 1
+    for (; r.item < 0 && s.item < items && s.lo < s.hi; ++s.item) {
+      const int nt = item_tiles(p, s.item), tb = s.tb;
+      s.tb += nt;
+      if (s.tb <= s.lo) continue;
+      r.item = s.item;
+      r.begin = s.lo - tb;
+      r.n = min(s.hi, s.tb) - s.lo;
+      r.c0 = holder(s, tb);
+      r.pieces = holder(s, tb + nt - 1) - r.c0 + 1;
+      r.slot = 2 * c + (share(s, c) < tb ? 1 : 0);  // a pair's first and its later pieces
+      s.lo += r.n;
+    }
+    if (r.item < 0) return;
+  }
+  r.b = p.groups == 1 ? r.item : r.item / p.groups;
+  r.g = r.item - r.b * p.groups;
+  r.len = p.lengths[r.b];
+}
+
+// One warp: the share of pair c and its first piece.
+__device__ __noinline__ void make_plan(const Args& p, int c, Plan* out, Piece* piece) {
   const int lane = threadIdx.x & 31, items = p.B * p.groups;
-  long long total = 0;
-  int longest = 0, nonempty = 0, nt[kPlanRegs];
+  int total = 0, longest = 0, nonempty = 0, nt[kPlanRegs];
   bool bad = false;
 #pragma unroll
   for (int k = 0; k < kPlanRegs; ++k) nt[k] = 0;
@@ -191,111 +231,71 @@ __device__ __noinline__ void make_plan(const Params& p, int c, Plan* out) {
     longest = max(longest, n);
     nonempty += n > 0;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  total = __reduce_add_sync(0xffffffffu, total);
   longest = __reduce_max_sync(0xffffffffu, longest);
   nonempty = __reduce_add_sync(0xffffffffu, nonempty);
   if (__any_sync(0xffffffffu, bad) && c == 0 && lane == 0) raise_error(p.err, MLA_ERR_LENGTH);
   Plan r;
-  r.total = total;
-  r.nc = (int)(total < p.pairs ? total : p.pairs);
+  r.nc = min(total, p.pairs);
+  r.q = r.nc > 0 ? total / r.nc : 0;
+  r.rem = total - r.q * r.nc;
   r.lo = r.hi = r.tb = 0;
   r.item = items;
   r.chunk = r.c0 = r.n = 0;
-  if (c >= r.nc) {
-    if (lane == 0) *out = r;
-    return;
-  }
-  // the smallest chunk whose chunks fit the pairs, if that is little above the even share
-  const int even = (int)share(total + r.nc - 1, 1, r.nc);
-  if (items <= 32 * kPlanRegs && nonempty <= r.nc && longest < (1 << 22)) {
+  if (c < r.nc) {
+    // the smallest chunk whose chunks fit the pairs, if that is little above the even share
+    const int even = r.q + (r.rem > 0);
+    if (items <= 32 * kPlanRegs && nonempty <= r.nc && longest < (1 << 22)) {
 #pragma unroll 1
-    for (int size = even; size <= even + kSwitchTiles; ++size) {
-      const float inv = 1.f / (float)size;
-      int n = 0;
+      for (int size = even; size <= even + kSwitchTiles; ++size) {
+        const float inv = 1.f / (float)size;
+        int n = 0;
 #pragma unroll
-      for (int k = 0; k < kPlanRegs; ++k) {
-        // ceil(nt / size): the float quotient is within one of the exact one
-        int q = (int)((float)nt[k] * inv);
-        q += (q * size < nt[k]) + ((q + 1) * size < nt[k]) - ((q - 1) * size >= nt[k] && q > 0);
-        n += q;
+        for (int k = 0; k < kPlanRegs; ++k) {
+          // ceil(nt / size): the float quotient is within one of the exact one
+          int q = (int)((float)nt[k] * inv);
+          q += (q * size < nt[k]) + ((q + 1) * size < nt[k]) - ((q - 1) * size >= nt[k] && q > 0);
+          n += q;
+        }
+        if ((int)__reduce_add_sync(0xffffffffu, n) <= r.nc) {
+          r.chunk = size;
+          break;
+        }
       }
-      if ((int)__reduce_add_sync(0xffffffffu, n) <= r.nc) {
-        r.chunk = size;
+    }
+    if (r.chunk == 0) {
+      r.lo = share(r, c);
+      r.hi = share(r, c + 1);
+    }
+    int base = 0;  // chunks or tiles before item i0
+    const int at = r.chunk > 0 ? c : r.lo;
+#pragma unroll 1
+    for (int i0 = 0; i0 < items; i0 += 32) {
+      int n = i0 == 0 ? nt[0] : i0 + lane < items ? item_tiles(p, i0 + lane) : 0;
+      if (r.chunk > 0) n = (n + r.chunk - 1) / r.chunk;
+      int sum = n;
+#pragma unroll 1
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, base + sum > at);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        r.item = i0 + l;
+        r.tb = base + __shfl_sync(0xffffffffu, sum - n, l);
+        r.n = __shfl_sync(0xffffffffu, n, l);
         break;
       }
+      base += __shfl_sync(0xffffffffu, sum, 31);
     }
+    r.c0 = r.tb;  // chunk plan: the item's first chunk is its first pair's
   }
-  if (r.chunk == 0) {
-    r.lo = share(total, c, r.nc);
-    r.hi = share(total, c + 1, r.nc);
-  }
-  long long base = 0;  // chunks or tiles before item i0
-  const long long at = r.chunk > 0 ? c : r.lo;
-#pragma unroll 1
-  for (int i0 = 0; i0 < items; i0 += 32) {
-    const int tiles = i0 + lane < items ? item_tiles(p, i0 + lane) : 0;
-    const int n = r.chunk > 0 ? (tiles + r.chunk - 1) / r.chunk : tiles;
-    int sum = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += v;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, base + sum > at);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      r.item = i0 + l;
-      r.tb = base + __shfl_sync(0xffffffffu, sum - n, l);
-      r.n = __shfl_sync(0xffffffffu, n, l);
-      break;
-    }
-    base += __shfl_sync(0xffffffffu, sum, 31);
-  }
-  r.c0 = (int)r.tb;  // chunk plan: the item's first chunk is its first pair's
-  if (lane == 0) *out = r;
-}
-
-// One thread: the next piece of pair c.
-__device__ __noinline__ void next_piece(const Params& p, int c, Plan& s, Piece* out) {
-  Piece r;
-  r.item = -1;
-  r.begin = r.end = r.tiles = r.slot = r.c0 = r.n = 0;
-  const int items = p.B * p.groups;
-  if (s.chunk > 0) {
-    if (s.item < items) {
-      r.item = s.item;
-      r.tiles = item_tiles(p, s.item);
-      r.begin = (c - s.c0) * s.chunk;
-      r.end = min(r.begin + s.chunk, r.tiles);
-      r.slot = 2 * c;
-      r.c0 = s.c0;
-      r.n = s.n;
-      s.item = items;
-    }
+  if (lane == 0) {
     *out = r;
-    return;
+    next_piece(p, c, *out, *piece);
   }
-  for (; s.item < items && s.lo < s.hi; ++s.item) {
-    const int nt = item_tiles(p, s.item);
-    if (s.tb + nt > s.lo) {
-      const long long end = s.hi < s.tb + nt ? s.hi : s.tb + nt;
-      r.item = s.item;
-      r.tiles = nt;
-      r.begin = (int)(s.lo - s.tb);
-      r.end = (int)(end - s.tb);
-      r.c0 = holder(s.tb, s.total, s.nc);
-      r.n = holder(s.tb + nt - 1, s.total, s.nc) - r.c0 + 1;
-      r.slot = 2 * c + (share(s.total, c, s.nc) < s.tb ? 1 : 0);  // a pair's first and its later pieces
-      s.lo = end;
-      s.tb += nt;
-      ++s.item;
-      *out = r;
-      return;
-    }
-    s.tb += nt;
-  }
-  *out = r;
+  __syncwarp();
 }
 
 // A decode warp has 16 of 64 keys and one half of the latent features, 128 bytes of codes: eight lanes cover a
@@ -315,7 +315,7 @@ struct PartSource {
 };
 __device__ __forceinline__ int part_row(int lane) { return ((lane >> 3) + ((lane & 7) >> 1)) & 3; }
 // From key `first` on, half `region` of the features, by warp j of four
-__device__ __forceinline__ PartSource part_source(const Params& p, int b, int len, int first, int region, int j, int lane) {
+__device__ __forceinline__ PartSource part_source(const Args& p, int b, int len, int first, int region, int j, int lane) {
   const int64_t t = (int64_t)first + 16 * j + part_row(lane);
   return {p.kv.c4 + b * p.kv.c4_b + t * p.kv.c4_r + 128 * region + 16 * (lane & 7),
           p.kv.sc + b * p.kv.sc_b + t * p.kv.sc_r + 16 * region + 2 * (lane & 7), 4 * p.kv.c4_r, 4 * p.kv.sc_r,
@@ -382,14 +382,14 @@ __device__ __forceinline__ uint32_t query_slab(uint32_t base, uint32_t stage, in
 }
 
 // One thread: the CTA's 64 query rows of the item as they are (bf16, rows past R as zeros).
-__device__ __noinline__ void fetch_query(const Params& p, Smem& sm, uint32_t base, uint32_t stage, int b, int row) {
+__device__ __noinline__ void fetch_query(const CUtensorMap* maps, Smem& sm, uint32_t base, uint32_t stage, int b, int row) {
   fence_proxy_async_smem();  // the buffers were read and written by threads before
   const uint64_t pol = policy_evict_first();
   const uint32_t bar = smem_u32(&sm.q_full);
   mbar_arrive_expect_tx(bar, 9 * kSlabBytes);
 #pragma unroll 1
-  for (int j = 0; j < 8; ++j) tma_load_3d(query_slab(base, stage, j), &p.tm_q, bar, 64 * j, row, b, pol);
-  tma_load_3d(query_slab(base, stage, 8), &p.tm_qp, bar, 0, row, b, pol);
+  for (int j = 0; j < 8; ++j) tma_load_3d(query_slab(base, stage, j), maps, bar, 64 * j, row, b, pol);
+  tma_load_3d(query_slab(base, stage, 8), maps + 1, bar, 0, row, b, pol);
 }
 
 __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
@@ -401,8 +401,9 @@ __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
 // The query rows in place, by the softmax warps, one row per thread and TMEM lane (lanes 64.. repeat the rows): the
 // row's power of two; the latent part to fp16, slabs 0..3 in TMEM (the first four warps), the others where they are
 // (the other four warps, with the rotary part, which is only scaled).  `scale`: the row's softmax scale, log2 units.
-__device__ __noinline__ bool place_query(const Params& p, Smem& sm, uint32_t base, uint32_t tmem, uint32_t stage,
+__device__ __noinline__ bool place_query(Smem& sm, uint32_t base, uint32_t tmem, uint32_t stage,
                                          uint32_t parity, float* scale) {
+  const Args& p = sm.args;
   const int lane = threadIdx.x & (kRows - 1), r = lane & (kMyRows - 1), h = threadIdx.x >> 7, hi = lane >> 6;
   const bool ok = wait_warp(sm, sm.q_full, parity, p.err);
   auto chunk = [&](int j, int c) { return query_slab(base, stage, j) + r * 128 + ((c ^ (r & 7)) << 4); };
@@ -424,33 +425,34 @@ __device__ __noinline__ bool place_query(const Params& p, Smem& sm, uint32_t bas
   x[2 * h + hi][r] = m;
   named_bar_sync(1, 256);
   m = fmaxf(fmaxf(x[0][r], x[1][r]), fmaxf(x[2][r], x[3][r]));
-  // 2^e that puts the largest element into [2^14, 2^15)
-  const int e = m > 0.f ? max(-126, min(126, 14 + 127 - (int)(__float_as_uint(m) >> 23))) : 0;
-  const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
+  // 2^e that puts the largest element into [2^14, 2^15); the latent part takes 2^e times latent_scale
+  const int le = (int)(__float_as_uint(ls) >> 23) - 127;
+  const int e = m > 0.f ? max(max(-126, -126 - le), min(min(126, 126 - le), 14 + 127 - (int)(__float_as_uint(m) >> 23))) : 0;
   *scale = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23), 1.2e-38f);
+  const float mul_pe = __uint_as_float((uint32_t)(127 + e) << 23), mul_lat = __uint_as_float((uint32_t)(127 + e + le) << 23);
   // h = 0: slabs 0..3;  h = 1: 4, 5 and 8 by the rows of lanes 0.., 6 and 7 by their repetition
   const int jn = h == 0 ? 4 : hi == 0 ? 3 : 2;
 #pragma unroll 1
   for (int k = 0; k < jn; ++k) {
     const int j = h == 0 ? k : k == 2 ? 8 : j0 + k;
-    const float a = j < 8 ? ls : 1.f;
-    uint32_t v[32];
+#pragma unroll 1
+    for (int c = 0; c < 8; c += 2) {
+      uint32_t v[8];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const uint4 u = ld_shared_v4_b32(chunk(j, c));
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      for (int d = 0; d < 2; ++d) {
+        const uint4 u = ld_shared_v4_b32(chunk(j, c + d));
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float lo = bf16_lo(w[i]) * a * mul, up = bf16_hi(w[i]) * a * mul;
-        v[4 * c + i] = j < 8 ? pack_f16x2_ieee(lo, up) : pack_bf16x2(lo, up);
+        for (int i = 0; i < 4; ++i)
+          v[4 * d + i] = j < 8 ? pack_f16x2_ieee(bf16_lo(w[i]) * mul_lat, bf16_hi(w[i]) * mul_lat)
+                               : pack_bf16x2(bf16_lo(w[i]) * mul_pe, bf16_hi(w[i]) * mul_pe);
       }
-    }
-    if (h == 0) {
-      tmem_st32(tmem + ((uint32_t)(lane & 96) << 16) + kColQ + 32 * j, v);
-    } else {
-#pragma unroll
-      for (int c = 0; c < 8; ++c)
-        st_shared_v4_b32(chunk(j, c), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+      if (h == 0) {
+        tmem_st8(tmem + ((uint32_t)(lane & 96) << 16) + kColQ + 32 * j + 4 * c, v);
+      } else {
+        st_shared_v4_b32(chunk(j, c), v[0], v[1], v[2], v[3]);
+        st_shared_v4_b32(chunk(j, c + 1), v[4], v[5], v[6], v[7]);
+      }
     }
   }
   if (h == 0) tmem_st_wait();
@@ -459,17 +461,8 @@ __device__ __noinline__ bool place_query(const Params& p, Smem& sm, uint32_t bas
   return ok;
 }
 
-// What a role needs to know of the piece at hand.  The roles are functions of their own so that each has the
-// registers to itself: inlined together they spill.
-struct Work {
-  uint32_t base, tmem;   // shared memory, TMEM
-  uint32_t it0, n;       // tiles of the earlier pieces, tiles of this one
-  int begin, b, g, len;
-  int rank;
-  int slot, c0, pieces;  // as in Piece
-  uint32_t parity;       // pieces before this one, modulo 2
-  uint32_t stage;        // where the query for TMEM is staged: the buffer of region X that is used last
-};
+// The roles are functions of their own so that each has the registers to itself (inlined together they spill), and
+// read the piece at hand from shared memory.
 
 // A 128-byte-swizzled shared-memory descriptor whose address is at + 32 k: the low word counts 16 bytes.
 __device__ __forceinline__ uint64_t step_desc(uint32_t at, int k, uint32_t lbo_bytes = 16) {
@@ -497,9 +490,10 @@ __device__ __forceinline__ void values(uint32_t o, uint32_t pr, uint32_t v, bool
 }
 
 // One warp of the even CTA: the pair's MMAs of a piece, issued by one thread: S(t), then O(t - 1).
-__device__ __noinline__ bool mma_role(const Params& p, uint32_t it0, uint32_t n, uint32_t parity) {
+__device__ __noinline__ bool mma_role(uint32_t it0, uint32_t n, uint32_t parity) {
   uint8_t* smem = shared_base();
   Smem& sm = *reinterpret_cast<Smem*>(smem + kSmemOff);
+  const Args& p = sm.args;
   const uint32_t base = smem_u32(smem), tmem = sm.tmem_base, tQ = tmem + kColQ, tO = tmem + kColO;
   constexpr uint16_t kBoth = 3;
   bool ok = true;
@@ -543,15 +537,16 @@ __device__ __noinline__ bool mma_role(const Params& p, uint32_t it0, uint32_t n,
 }
 
 // Eight warps, 32 keys of a query row per thread: probabilities, and the piece's result.
-__device__ __noinline__ bool softmax_role(const Params& p, Smem& sm, Work w, float sl, bool ok) {
+__device__ __noinline__ bool softmax_role(Smem& sm, const Piece& w, uint32_t it0, float sl, bool ok) {
+  const Args& p = sm.args;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, col = warp >> 2;
   const int tl = 32 * quad + lane, r = tl & (kMyRows - 1), half = tl >> 6;  // TMEM lane, row, half of the tile's keys
   const int part = 2 * half + col;                                          // the row's quarter of keys and features
-  const uint32_t base = w.base, n = w.n, it0 = w.it0;
-  const int b = w.b, g = w.g, len = w.len;
-  const int row = kMyRows * w.rank + r, rows = min(p.R - kRows * g, kRows);  // row of the group, rows that it has
+  const uint32_t base = smem_u32(&sm) - kSmemOff, tmem = sm.tmem_base, n = w.n, rank = cluster_ctarank();
+  const int g = w.g, len = w.len;
+  const int row = kMyRows * (int)rank + r, rows = min(p.R - kRows * g, kRows);  // row of the group, rows that it has
   const uint32_t lanes = (uint32_t)(32 * quad) << 16;
-  const uint32_t tS = w.tmem + lanes + kColS + 32 * col, tO = w.tmem + lanes + kColO + 128 * col;
+  const uint32_t tS = tmem + lanes + kColS + 32 * col, tO = tmem + lanes + kColO + 128 * col;
   const uint32_t p_row = base + kPOff + half * kSlabBytes + r * 128;
   // keys that the row, and the group's first row, see
   const int limit = len - p.T + (kRows * g + min(row, rows - 1)) / p.n_h + 1;
@@ -576,7 +571,7 @@ __device__ __noinline__ bool softmax_role(const Params& p, Smem& sm, Work w, flo
     tmem_ld_wait();
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) arrive_even(sm.s_empty[it & 1u], w.rank);
+    if (lane == 0) arrive_even(sm.s_empty[it & 1u], rank);
     if (k0 + 32 > all_see) {
 #pragma unroll
       for (int i = 0; i < 32; ++i)
@@ -631,7 +626,7 @@ __device__ __noinline__ bool softmax_role(const Params& p, Smem& sm, Work w, flo
       st_shared_v4_b32(p_row + (((4 * col + c) ^ (r & 7)) << 4), s[4 * c], s[4 * c + 1], s[4 * c + 2], s[4 * c + 3]);
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) arrive_even(sm.p_full, w.rank);
+    if (lane == 0) arrive_even(sm.p_full, rank);
   }
   if (ok) {  // the row's sum (the last tile used the other buffer)
     float(&x)[4][kMyRows] = sm.share[(it0 + n) & 1u];
@@ -646,8 +641,8 @@ __device__ __noinline__ bool softmax_role(const Params& p, Smem& sm, Work w, flo
     // The thread has the row's features [128 part, 128 part + 128).  They go through the idle regions, 16-byte
     // chunks rotated by the row so that neither the row-wise writes nor the copies out conflict.
     tc_fence_after();
-    const int64_t out_row = (int64_t)b * p.R + kRows * g + kMyRows * w.rank;  // the CTA's first query row
-    const int first = 32 * (quad & 1), mine = min(32, rows - kMyRows * w.rank - first);  // the warp's rows of it
+    const int64_t out_row = (int64_t)w.b * p.R + kRows * g + kMyRows * (int)rank;  // the CTA's first query row
+    const int first = 32 * (quad & 1), mine = min(32, rows - kMyRows * (int)rank - first);  // the warp's rows of it
     const bool whole = w.pieces == 1;
     const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) * p.kv.latent_scale : 1.f;
     const uint32_t src = base + warp * (32 * 512), dst = src + lane * 512;
@@ -682,88 +677,66 @@ __device__ __noinline__ bool softmax_role(const Params& p, Smem& sm, Work w, flo
         p.lse[out_row + r] = l == 0.f ? -INFINITY : ref * kLn2 + logf(l);
     } else {
       if (lane == 0 && mine > 0) {
-        const int64_t at = (4 * (int64_t)w.slot + part) * min(p.R, kRows) + kMyRows * w.rank + first;
+        const int64_t at = (4 * (int64_t)w.slot + part) * min(p.R, kRows) + kMyRows * (int)rank + first;
         bulk_store_s2g(p.ws_o + at * 128, src, mine * 512);
         bulk_group_commit();
         bulk_group_wait_read_all();
       }
       if (part == 0 && row < rows) p.ws_ml[(int64_t)w.slot * kRows + row] = make_float2(ref, l);
     }
-    if (threadIdx.x == 0 && w.rank == 0 && w.begin == 0) p.table[w.b * p.groups + w.g] = make_int4(w.slot, w.c0, w.pieces, 0);
+    if (threadIdx.x == 0 && rank == 0 && w.begin == 0) p.table[w.item] = make_int4(w.slot, w.c0, w.pieces, 0);
     tc_fence_before();
     fence_proxy_async_smem();
   }
   return ok;
 }
 
-// One warp: 16 keys of every tile, loaded one tile ahead (from L2: another warp prefetches).  Four warps have the
+// One warp: 16 keys of every tile, loaded one tile ahead.  Four warps have the
 // CTA's keys in region X, four in region Y, and four replace the slabs of the half that is not the CTA's by
 // values of the other CTA's keys once the tile's scores are done.
-__device__ __noinline__ bool latent_role(const Params& p, Smem& sm, Work w) {
+__device__ __noinline__ bool latent_role(Smem& sm, const Piece& w, uint32_t it0, uint32_t parity) {
+  const Args& p = sm.args;
+  const uint32_t base = smem_u32(&sm) - kSmemOff, n = w.n;
+  const int rank = (int)cluster_ctarank();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool values = warp >= kVWarp0;
-  const int region = values ? 1 - w.rank : warp >= kYWarp0 ? 1 : 0, j = (warp - kXWarp0) & 3;
-  const uint32_t bufs = region ? kYBufs : kXBufs, slabs = w.base + (region ? kYOff : 0);
-  PartSource src = part_source(p, w.b, w.len, w.begin * kTile + kKeys * (values ? 1 - w.rank : w.rank),
-                               values ? w.rank : region, j, lane);
+  const int region = values ? 1 - rank : warp >= kYWarp0 ? 1 : 0, j = (warp - kXWarp0) & 3;
+  const uint32_t bufs = region ? kYBufs : kXBufs, slabs = base + (region ? kYOff : 0);
+  PartSource src = part_source(p, w.b, w.len, w.begin * kTile + kKeys * (values ? 1 - rank : rank),
+                               values ? rank : region, j, lane);
   Part k;
   load_part(src, k);
 #pragma unroll 1
-  for (uint32_t t = 0; t < w.n; ++t) {
-    const uint32_t it = w.it0 + t, buf = it % bufs;
+  for (uint32_t t = 0; t < n; ++t) {
+    const uint32_t it = it0 + t, buf = it % bufs;
     uint64_t &from = values ? sm.s_full[it & 1u] : region ? sm.y_empty[buf] : sm.x_empty[buf],
              &to = values ? sm.v_full[it & 1u] : region ? sm.y_full[buf] : sm.x_full[buf];
     if (!wait_warp(sm, from, values ? (it >> 1) & 1u : ((it / bufs) & 1u) ^ 1u, p.err)) return false;
     // (the first use of the third buffer: the query has left it)
-    if (region == 0 && !values && t == 2 && !wait_warp(sm, sm.q_placed, w.parity, p.err)) return false;
+    if (region == 0 && !values && t == 2 && !wait_warp(sm, sm.q_placed, parity, p.err)) return false;
     store_part(k, slabs + buf * kRegion, j, lane);
-    if (lane == 0) arrive_even(to, w.rank);
-    if (warp == kXWarp0 && lane == 0) *const_cast<volatile int*>(&sm.progress) = (int)t;
+    if (lane == 0) arrive_even(to, rank);
     load_part(src, k);
   }
   return true;
 }
 
-__device__ __forceinline__ void prefetch_l2(const void* a) { asm volatile("prefetch.global.L2 [%0];" ::"l"(a)); }
-// One warp: 64 cached rows into L2.
-__device__ __forceinline__ void prefetch_rows(const Params& p, int b, int first, int len, int lane) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t t = (int64_t)first + 32 * i + lane;
-    if (t >= len) return;
-    const uint8_t* c = p.kv.c4 + b * p.kv.c4_b + t * p.kv.c4_r;
-    prefetch_l2(c);
-    prefetch_l2(c + 128);
-    prefetch_l2(p.kv.sc + b * p.kv.sc_b + t * p.kv.sc_r);
-    prefetch_l2(static_cast<const __nv_bfloat16*>(p.kv.k_r) + b * p.kv.kr_b + t * p.kv.kr_r);
-  }
-}
-
-// One warp: the tiles' way into L2, kPrefetch tiles ahead of the decode warps.
-__device__ __noinline__ void prefetch_role(const Params& p, Smem& sm, Work w) {
-  const int lane = threadIdx.x & 31;
-  const volatile int* progress = &sm.progress;
-  const volatile int* abort = &sm.abort;
-#pragma unroll 1
-  for (int t = 1; t < (int)w.n; ++t) {
-    while (*progress + kPrefetch < t && !*abort) __nanosleep(100);  // the decode warps' waits are bounded
-    prefetch_rows(p, w.b, (w.begin + t) * kTile + kKeys * w.rank, w.len, lane);
-  }
-}
-
 // One warp: the rotary slab of every tile.
-__device__ __noinline__ bool rope_role(const Params& p, Smem& sm, Work w) {
-  const int lane = threadIdx.x & 31, keys = w.begin * kTile + kKeys * w.rank;
+__device__ __noinline__ bool rope_role(Smem& sm, const Piece& w, uint32_t it0) {
+  const Args& p = sm.args;
+  const uint32_t base = smem_u32(&sm) - kSmemOff, n = w.n;
+  const int rank = (int)cluster_ctarank();
+  const int lane = threadIdx.x & 31, keys = w.begin * kTile + kKeys * rank;
   const uint8_t* src = reinterpret_cast<const uint8_t*>(static_cast<const __nv_bfloat16*>(p.kv.k_r) + w.b * p.kv.kr_b +
                                                         ((int64_t)keys + (lane >> 3)) * p.kv.kr_r) + 16 * (lane & 7);
   int left = w.len - keys - (lane >> 3);
   uint4 k[16];
   load_rope(src, 8 * p.kv.kr_r, left, k);
 #pragma unroll 1
-  for (uint32_t t = 0; t < w.n; ++t) {
-    if (!wait_warp(sm, sm.rope_empty, ((w.it0 + t) & 1u) ^ 1u, p.err)) return false;
-    store_rope(k, w.base + kRopeOff, lane);
-    if (lane == 0) arrive_even(sm.rope_full, w.rank);
+  for (uint32_t t = 0; t < n; ++t) {
+    if (!wait_warp(sm, sm.rope_empty, ((it0 + t) & 1u) ^ 1u, p.err)) return false;
+    store_rope(k, base + kRopeOff, lane);
+    if (lane == 0) arrive_even(sm.rope_full, rank);
     left -= kTile;
     load_rope(src, 8 * p.kv.kr_r, left, k);
   }
@@ -779,7 +752,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
 
   griddep_launch_dependents();
   if (base & 1023u) {
-    if (threadIdx.x == 0) raise_error(p.err, MLA_ERR_CUDA);
+    if (threadIdx.x == 0) raise_error(p.a.err, MLA_ERR_CUDA);
     return;
   }
   if (threadIdx.x == 0) {
@@ -802,7 +775,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
     mbar_init(smem_u32(&sm.q_full), 1);
     mbar_init(smem_u32(&sm.pv_done), 1);
     mbar_init(smem_u32(&sm.drain), 1);
-    sm.abort = sm.never = sm.progress = 0;
+    sm.abort = sm.never = 0;
     fence_mbar_init();
     prefetch_tensormap(&p.tm_q);
     prefetch_tensormap(&p.tm_qp);
@@ -816,67 +789,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   griddep_wait();
   if (warp == 0) {
-    make_plan(p, pair, &sm.plan);
+    static_assert(sizeof(Args) % 4 == 0, "copied by words");
+    for (int i = lane; i < (int)sizeof(Args) / 4; i += 32)
+      reinterpret_cast<uint32_t*>(&sm.args)[i] = reinterpret_cast<const uint32_t*>(&p.a)[i];
     __syncwarp();
-    if (lane == 0) next_piece(p, pair, sm.plan, &sm.piece);
-    __syncwarp();
+    make_plan(sm.args, pair, &sm.plan, &sm.piece[0]);
   }
   tc_fence_before();
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sm.tmem_base;
 
   // it0: tiles of the earlier pieces.  Both CTAs walk the same pieces, and all warps take every barrier of every
   // piece, also after a failed wait.
   uint32_t it0 = 0, pieces = 0;
   bool dead = false;
-  while (sm.piece.item >= 0) {
-    Work w;
-    w.base = base;
-    w.tmem = tmem;
-    w.it0 = it0;
-    w.begin = sm.piece.begin;
-    w.n = (uint32_t)(sm.piece.end - w.begin);
-    w.b = p.groups == 1 ? sm.piece.item : sm.piece.item / p.groups;
-    w.g = sm.piece.item - w.b * p.groups;
-    w.len = p.lengths[w.b];
-    w.rank = rank;
-    w.slot = sm.piece.slot;
-    w.c0 = sm.piece.c0;
-    w.pieces = sm.piece.n;
-    w.parity = pieces++ & 1u;
-    w.stage = base + (it0 + kXBufs - 1) % kXBufs * kRegion;
-    if (threadIdx.x == 0) fetch_query(p, sm, base, w.stage, w.b, kRows * w.g + kMyRows * rank);
+  while (true) {
+    const uint32_t parity = pieces & 1u;
+    const Piece& w = sm.piece[parity];
+    if (w.item < 0) break;
+    ++pieces;
+    // the query for TMEM is staged in the buffer of region X that is used last
+    const uint32_t stage = base + (it0 + kXBufs - 1) % kXBufs * kRegion;
+    if (threadIdx.x == 0) fetch_query(&p.tm_q, sm, base, stage, w.b, kRows * w.g + kMyRows * rank);
     __syncwarp();
     if (!dead) {
       bool ok = true;
       if (warp < kSoftmaxWarps) {
         float scale;
-        ok = place_query(p, sm, base, tmem, w.stage, w.parity, &scale);
+        ok = place_query(sm, base, sm.tmem_base, stage, parity, &scale);
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(smem_u32(&sm.q_placed));
           arrive_even(sm.q_ready, rank);
         }
-        ok = softmax_role(p, sm, w, scale, ok);
+        ok = softmax_role(sm, w, it0, scale, ok);
       } else if (warp == kMmaWarp) {
-        ok = rank != 0 || mma_role(p, it0, w.n, w.parity);
+        ok = rank != 0 || mma_role(it0, w.n, parity);
       } else if (warp < kRopeWarp) {
-        ok = latent_role(p, sm, w);
-      } else if (warp == kRopeWarp) {
-        ok = rope_role(p, sm, w);
+        ok = latent_role(sm, w, it0, parity);
       } else {
-        prefetch_role(p, sm, w);
+        ok = rope_role(sm, w, it0);
       }
       dead = !ok;
     }
     __syncwarp();
     it0 += w.n;
-    if (threadIdx.x == 0) {
-      next_piece(p, pair, sm.plan, &sm.piece);
-      sm.progress = 0;
-    }
+    if (threadIdx.x == 0) next_piece(sm.args, pair, sm.plan, sm.piece[parity ^ 1u]);
     __syncthreads();
     tc_fence_after();
     if (sm.abort) dead = true;
@@ -896,21 +855,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
   __syncwarp();
   cluster_sync();  // neither CTA leaves while the other may still arrive on its barriers or read its shared memory
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc_pair(tmem, kTmemCols);
+  if (warp == kMmaWarp) tmem_dealloc_pair(sm.tmem_base, kTmemCols);
 }
 
 // Joins the partials of items that were cut: one warp per query row and latent half, in slot order.  Rows of
 // sequences with a bad length become zeros.
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args p) {
   griddep_launch_dependents();
   griddep_wait();
-  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int w = blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31, hf = (int)(w & 1);
-  const int64_t row = w >> 1;
-  if (row >= (int64_t)p.B * p.R) return;
-  const int b = (int)(row / p.R), r = (int)(row % p.R), g = r / kRows, i = r % kRows;
-  uint4* dst = reinterpret_cast<uint4*>(p.ctx + row * kDC + 256 * hf);
-  if (item_keys(p, b * p.groups + g) == 0) {
+  const int row = w >> 1;
+  if (row >= p.B * p.R) return;  // (at most 65535 query groups of 128 rows)
+  const int b = row / p.R, r = row - b * p.R, g = r / kRows, i = r % kRows;
+  uint4* dst = reinterpret_cast<uint4*>(p.ctx + (int64_t)row * kDC + 256 * hf);
+  if (item_keys(p, b, g) == 0) {
     dst[lane] = make_uint4(0u, 0u, 0u, 0u);
     if (hf == 0 && lane == 0 && p.lse != nullptr) p.lse[row] = -INFINITY;
     return;
@@ -986,13 +945,14 @@ size_t decode_fp4_tc_workspace(int n_h, int B, int T, int n_max) {
 
 cudaError_t decode_fp4_tc_launch(const Fp4DecodeArgs& a, void* ws, cudaStream_t st) {
   using namespace decode_fp4;
-  Params p{};
+  Params params{};
+  Args& p = params.a;
   p.kv = a.kv;
   p.lengths = a.lengths;
   p.B = a.B; p.T = a.T; p.n_h = a.n_h; p.n_max = a.n_max;
   p.R = a.T * a.n_h;
   p.groups = (p.R + kRows - 1) / kRows;
-  if (!query_map(&p.tm_q, a.q_tilde, kDC, p.R, a.B, a.ldqt) || !query_map(&p.tm_qp, a.q_pe, kDR, p.R, a.B, a.ldqp))
+  if (!query_map(&params.tm_q, a.q_tilde, kDC, p.R, a.B, a.ldqt) || !query_map(&params.tm_qp, a.q_pe, kDR, p.R, a.B, a.ldqp))
     return cudaErrorInvalidValue;
   static int allowed[kMaxDevices];
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(decode_kernel), kSmemBytes, allowed);
@@ -1008,7 +968,7 @@ cudaError_t decode_fp4_tc_launch(const Fp4DecodeArgs& a, void* ws, cudaStream_t 
   w += ml_bytes(p.pairs);
   p.ws_o = reinterpret_cast<float*>(w);
   p.err = a.err;
-  e = launch_pdl(decode_kernel, dim3(2 * p.pairs), dim3(kThreads), kSmemBytes, st, p);
+  e = launch_pdl(decode_kernel, dim3(2 * p.pairs), dim3(kThreads), kSmemBytes, st, params);
   if (e != cudaSuccess) return e;
   const int64_t warps = (int64_t)p.B * p.R * 2;
   return launch_pdl(join_kernel, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st, p);

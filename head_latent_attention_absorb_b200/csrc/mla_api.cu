@@ -641,6 +641,8 @@ mla_status mla_decode_absorb_fp4kv(mla_dims dims, mla_dtype dtype, int32_t B, in
                         scale));
   MLA_TRY(check_fp4(dims, dtype, c4, c4_bstride, c4_rstride, kv_scale, sc_bstride, sc_rstride, latent_scale));
   if (!ctx_out) return fail(MLA_ERR_INVALID_ARG, "NULL pointer");
+  if (((int64_t)dims.n_h * T + 127) / 128 * B * (((int64_t)n_max + 127) / 128) > INT32_MAX)
+    return fail(MLA_ERR_UNSUPPORTED, "more than 2^31 tiles of 128 query rows and 128 cached rows");
   MLA_TRY(check_bf16_ptr(dtype, ctx_out, "ctx_out"));
   const size_t need = mla_decode_fp4kv_workspace_size(dims, dtype, B, T, n_max);
   if (!workspace || ws_bytes < need)
