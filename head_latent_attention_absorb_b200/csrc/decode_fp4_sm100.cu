@@ -68,7 +68,8 @@ constexpr int kPOff = kQOff + 5 * kSlabBytes;    // probabilities of the first a
 constexpr int kSmemOff = kPOff + 2 * kSlabBytes;
 static_assert(kQTmemSlabs * kSlabBytes <= kRegion, "the query for TMEM is staged in a buffer of region X");
 static_assert(kMyRows * kDC * 4 <= kRopeOff, "the partial context is staged in the regions");
-constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kXWarp0 = 9, kYWarp0 = 13, kVWarp0 = 17, kRopeWarp = 21;
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kKWarp0 = 9, kVWarp0 = 17, kRopeWarp = 21;
+constexpr int kKWarps = 8, kVWarps = 4;
 constexpr int kThreads = 32 * (kRopeWarp + 1);
 constexpr uint32_t kTmemCols = 512, kColO = 0, kColS = 256, kColQ = 384;  // scores: two buffers of 64
 // Probabilities are 2^(z - ref): ref is set kRaise below the largest score so far (log2 units) and moved up
@@ -298,14 +299,15 @@ __device__ __noinline__ void make_plan(const Args& p, int c, Plan* out, Piece* p
   __syncwarp();
 }
 
-// A decode warp has 16 of 64 keys and one half of the latent features, 128 bytes of codes: eight lanes cover a
+// A decode warp has 4 G of 64 keys and one half of the latent features, 128 bytes of codes, at a time: eight lanes cover a
 // key's, so an instruction reads four keys in about six cache lines (one key per lane pair, 64 features each,
 // needed sixteen, and the L1 lookups then bounded the kernel).  Lane l has 32 features, of slab (l & 7) / 2, and
-// of the keys 4 i + r, i = 0..3, the r that makes the eight lanes of a store phase hit distinct banks: the four
+// of the keys 4 i + r, i < G, the r that makes the eight lanes of a store phase hit distinct banks: the four
 // slabs take four different rows.
+template <int G>
 struct Part {
-  uint4 code[4];
-  uint32_t scale[4];
+  uint4 code[G];
+  uint32_t scale[G];
 };
 struct PartSource {
   const uint8_t* code;
@@ -314,34 +316,38 @@ struct PartSource {
   int left;               // keys from the lane's first one on that are in the sequence
 };
 __device__ __forceinline__ int part_row(int lane) { return ((lane >> 3) + ((lane & 7) >> 1)) & 3; }
-// From key `first` on, half `region` of the features, by warp j of four
-__device__ __forceinline__ PartSource part_source(const Args& p, int b, int len, int first, int region, int j, int lane) {
-  const int64_t t = (int64_t)first + 16 * j + part_row(lane);
+// From key `first` on, half `region` of the features
+__device__ __forceinline__ PartSource part_source(const Args& p, int b, int len, int first, int region, int lane) {
+  const int64_t t = (int64_t)first + part_row(lane);
   return {p.kv.c4 + b * p.kv.c4_b + t * p.kv.c4_r + 128 * region + 16 * (lane & 7),
           p.kv.sc + b * p.kv.sc_b + t * p.kv.sc_r + 16 * region + 2 * (lane & 7), 4 * p.kv.c4_r, 4 * p.kv.sc_r,
           (int)(len - t)};
 }
-// Loads the source's keys and moves on to the next tile's.
-__device__ __forceinline__ void load_part(PartSource& s, Part& k) {
+// Loads the source's keys; those of the other half of the features, too, lie `half` halves away.
+template <int G>
+__device__ __forceinline__ void load_part(const PartSource& s, int half, Part<G>& k) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < G; ++i) {
     k.code[i] = make_uint4(0u, 0u, 0u, 0u);
     k.scale[i] = 0u;
     if (4 * i < s.left) {  // rows behind the sequence may hold anything, or not exist
-      k.code[i] = __ldg(reinterpret_cast<const uint4*>(s.code + i * s.code4));
-      k.scale[i] = __ldg(reinterpret_cast<const uint16_t*>(s.scale + i * s.scale4));
+      k.code[i] = __ldg(reinterpret_cast<const uint4*>(s.code + i * s.code4 + 128 * half));
+      k.scale[i] = __ldg(reinterpret_cast<const uint16_t*>(s.scale + i * s.scale4 + 16 * half));
     }
   }
+}
+__device__ __forceinline__ void next_tile(PartSource& s) {
   s.code += kTile / 4 * s.code4;
   s.scale += kTile / 4 * s.scale4;
   s.left -= kTile;
 }
-// Decodes into the region at `dst`.
-__device__ __forceinline__ void store_part(const Part& k, uint32_t dst, int j, int lane) {
+// Decodes into the region at `dst`, keys 4 G j on.
+template <int G>
+__device__ __forceinline__ void store_part(const Part<G>& k, uint32_t dst, int j, int lane) {
   const int half = lane & 1, r = part_row(lane);
-  dst += ((lane & 7) >> 1) * kSlabBytes + (16 * j + r) * 128;
+  dst += ((lane & 7) >> 1) * kSlabBytes + (4 * G * j + r) * 128;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < G; ++i) {
     const uint32_t s2 = fp4::scales_to_f16(k.scale[i]);
     const uint32_t s[2] = {__byte_perm(s2, s2, 0x1010), __byte_perm(s2, s2, 0x3232)};
     const uint32_t words[4] = {k.code[i].x, k.code[i].y, k.code[i].z, k.code[i].w};
@@ -435,24 +441,28 @@ __device__ __noinline__ bool place_query(Smem& sm, uint32_t base, uint32_t tmem,
 #pragma unroll 1
   for (int k = 0; k < jn; ++k) {
     const int j = h == 0 ? k : k == 2 ? 8 : j0 + k;
-#pragma unroll 1
-    for (int c = 0; c < 8; c += 2) {
-      uint32_t v[8];
+    uint32_t v[32];
 #pragma unroll
-      for (int d = 0; d < 2; ++d) {
-        const uint4 u = ld_shared_v4_b32(chunk(j, c + d));
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    for (int c = 0; c < 8; ++c) {
+      const uint4 u = ld_shared_v4_b32(chunk(j, c));
+      v[4 * c] = u.x;
+      v[4 * c + 1] = u.y;
+      v[4 * c + 2] = u.z;
+      v[4 * c + 3] = u.w;
+    }
+    if (j < 8) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          v[4 * d + i] = j < 8 ? pack_f16x2_ieee(bf16_lo(w[i]) * mul_lat, bf16_hi(w[i]) * mul_lat)
-                               : pack_bf16x2(bf16_lo(w[i]) * mul_pe, bf16_hi(w[i]) * mul_pe);
-      }
-      if (h == 0) {
-        tmem_st8(tmem + ((uint32_t)(lane & 96) << 16) + kColQ + 32 * j + 4 * c, v);
-      } else {
-        st_shared_v4_b32(chunk(j, c), v[0], v[1], v[2], v[3]);
-        st_shared_v4_b32(chunk(j, c + 1), v[4], v[5], v[6], v[7]);
-      }
+      for (int i = 0; i < 32; ++i) v[i] = pack_f16x2_ieee(bf16_lo(v[i]) * mul_lat, bf16_hi(v[i]) * mul_lat);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = pack_bf16x2(bf16_lo(v[i]) * mul_pe, bf16_hi(v[i]) * mul_pe);
+    }
+    if (h == 0) {
+      tmem_st32(tmem + ((uint32_t)(lane & 96) << 16) + kColQ + 32 * j, v);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        st_shared_v4_b32(chunk(j, c), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
     }
   }
   if (h == 0) tmem_st_wait();
@@ -691,32 +701,51 @@ __device__ __noinline__ bool softmax_role(Smem& sm, const Piece& w, uint32_t it0
   return ok;
 }
 
-// One warp: 16 keys of every tile, loaded one tile ahead.  Four warps have the
-// CTA's keys in region X, four in region Y, and four replace the slabs of the half that is not the CTA's by
-// values of the other CTA's keys once the tile's scores are done.
-__device__ __noinline__ bool latent_role(Smem& sm, const Piece& w, uint32_t it0, uint32_t parity) {
+// One of eight warps: eight of the CTA's keys of every tile, loaded one tile ahead; first the half in region X, then,
+// when the values of two tiles before have been used, the one in region Y.
+__device__ __noinline__ bool key_role(Smem& sm, const Piece& w, uint32_t it0, uint32_t parity) {
   const Args& p = sm.args;
-  const uint32_t base = smem_u32(&sm) - kSmemOff, n = w.n;
-  const int rank = (int)cluster_ctarank();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool values = warp >= kVWarp0;
-  const int region = values ? 1 - rank : warp >= kYWarp0 ? 1 : 0, j = (warp - kXWarp0) & 3;
-  const uint32_t bufs = region ? kYBufs : kXBufs, slabs = base + (region ? kYOff : 0);
-  PartSource src = part_source(p, w.b, w.len, w.begin * kTile + kKeys * (values ? 1 - rank : rank),
-                               values ? rank : region, j, lane);
-  Part k;
-  load_part(src, k);
+  const uint32_t base = smem_u32(&sm) - kSmemOff, n = w.n, rank = cluster_ctarank();
+  const int lane = threadIdx.x & 31, j = (threadIdx.x >> 5) - kKWarp0;
+  PartSource src = part_source(p, w.b, w.len, w.begin * kTile + kKeys * (int)rank + 8 * j, 0, lane);
+  Part<2> x, y;
+  load_part(src, 0, x);
+  load_part(src, 1, y);
 #pragma unroll 1
   for (uint32_t t = 0; t < n; ++t) {
-    const uint32_t it = it0 + t, buf = it % bufs;
-    uint64_t &from = values ? sm.s_full[it & 1u] : region ? sm.y_empty[buf] : sm.x_empty[buf],
-             &to = values ? sm.v_full[it & 1u] : region ? sm.y_full[buf] : sm.x_full[buf];
-    if (!wait_warp(sm, from, values ? (it >> 1) & 1u : ((it / bufs) & 1u) ^ 1u, p.err)) return false;
+    const uint32_t it = it0 + t, xb = it % kXBufs, yb = it % kYBufs;
+    if (!wait_warp(sm, sm.x_empty[xb], ((it / kXBufs) & 1u) ^ 1u, p.err)) return false;
     // (the first use of the third buffer: the query has left it)
-    if (region == 0 && !values && t == 2 && !wait_warp(sm, sm.q_placed, parity, p.err)) return false;
-    store_part(k, slabs + buf * kRegion, j, lane);
-    if (lane == 0) arrive_even(to, rank);
-    load_part(src, k);
+    if (t == 2 && !wait_warp(sm, sm.q_placed, parity, p.err)) return false;
+    store_part(x, base + xb * kRegion, j, lane);
+    if (lane == 0) arrive_even(sm.x_full[xb], rank);
+    next_tile(src);
+    load_part(src, 0, x);
+    if (!wait_warp(sm, sm.y_empty[yb], ((it / kYBufs) & 1u) ^ 1u, p.err)) return false;
+    store_part(y, base + kYOff + yb * kRegion, j, lane);
+    if (lane == 0) arrive_even(sm.y_full[yb], rank);
+    load_part(src, 1, y);
+  }
+  return true;
+}
+
+// One of four warps: of every tile, the values of 16 of the other CTA's keys replace slabs of the half that is not
+// this CTA's, once the tile's scores are done.
+__device__ __noinline__ bool value_role(Smem& sm, const Piece& w, uint32_t it0) {
+  const Args& p = sm.args;
+  const uint32_t base = smem_u32(&sm) - kSmemOff, n = w.n, rank = cluster_ctarank();
+  const int lane = threadIdx.x & 31, j = (threadIdx.x >> 5) - kVWarp0;
+  PartSource src = part_source(p, w.b, w.len, w.begin * kTile + kKeys * (1 - (int)rank) + 16 * j, (int)rank, lane);
+  Part<4> v;
+  load_part(src, 0, v);
+#pragma unroll 1
+  for (uint32_t t = 0; t < n; ++t) {
+    const uint32_t it = it0 + t;
+    if (!wait_warp(sm, sm.s_full[it & 1u], (it >> 1) & 1u, p.err)) return false;
+    store_part(v, base + (rank == 0 ? kYOff + it % kYBufs * kRegion : it % kXBufs * kRegion), j, lane);
+    if (lane == 0) arrive_even(sm.v_full[it & 1u], rank);
+    next_tile(src);
+    load_part(src, 0, v);
   }
   return true;
 }
@@ -757,13 +786,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kXBufs; ++i) {
-      mbar_init(smem_u32(&sm.x_full[i]), 8);
+      mbar_init(smem_u32(&sm.x_full[i]), 2 * kKWarps);
       mbar_init(smem_u32(&sm.x_empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&sm.y_full[i]), 8);
+      mbar_init(smem_u32(&sm.y_full[i]), 2 * kKWarps);
       mbar_init(smem_u32(&sm.y_empty[i]), 1);
-      mbar_init(smem_u32(&sm.v_full[i]), 8);
+      mbar_init(smem_u32(&sm.v_full[i]), 2 * kVWarps);
       mbar_init(smem_u32(&sm.s_full[i]), 1);
       mbar_init(smem_u32(&sm.s_empty[i]), 2 * kSoftmaxWarps);
     }
@@ -813,7 +842,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
     const uint32_t stage = base + (it0 + kXBufs - 1) % kXBufs * kRegion;
     if (threadIdx.x == 0) fetch_query(&p.tm_q, sm, base, stage, w.b, kRows * w.g + kMyRows * rank);
     __syncwarp();
-    if (!dead) {
+    if (dead) {
+      if (warp == kRopeWarp && lane == 0) next_piece(sm.args, pair, sm.plan, sm.piece[parity ^ 1u]);
+    } else {
       bool ok = true;
       if (warp < kSoftmaxWarps) {
         float scale;
@@ -827,15 +858,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) decode_
       } else if (warp == kMmaWarp) {
         ok = rank != 0 || mma_role(it0, w.n, parity);
       } else if (warp < kRopeWarp) {
-        ok = latent_role(sm, w, it0, parity);
+        ok = warp < kVWarp0 ? key_role(sm, w, it0, parity) : value_role(sm, w, it0);
       } else {
+        if (lane == 0) next_piece(sm.args, pair, sm.plan, sm.piece[parity ^ 1u]);
+        __syncwarp();
         ok = rope_role(sm, w, it0);
       }
       dead = !ok;
     }
     __syncwarp();
     it0 += w.n;
-    if (threadIdx.x == 0) next_piece(sm.args, pair, sm.plan, sm.piece[parity ^ 1u]);
     __syncthreads();
     tc_fence_after();
     if (sm.abort) dead = true;
