@@ -159,6 +159,14 @@ __device__ __noinline__ bool wait_more(Smem& sm, uint32_t bar, uint32_t parity, 
 __device__ __forceinline__ bool wait(Smem& sm, uint64_t& bar, uint32_t parity, int32_t* err) {
   return mbar_try_wait(smem_u32(&bar), parity) || wait_more(sm, smem_u32(&bar), parity, err);
 }
+// The MMA thread polls before it lets the hardware put it to sleep: waking up takes some hundred cycles, and one
+// polling thread costs the others little.
+__device__ __forceinline__ bool wait_awake(Smem& sm, uint64_t& bar, uint32_t parity, int32_t* err) {
+#pragma unroll 1
+  for (int i = 0; i < 256; ++i)
+    if (mbar_test(smem_u32(&bar), parity)) return true;
+  return wait_more(sm, smem_u32(&bar), parity, err);
+}
 // All lanes wait; the warp goes on only if all of them saw the phase complete.
 __device__ __forceinline__ bool wait_warp(Smem& sm, uint64_t& bar, uint32_t parity, int32_t* err) {
   return __all_sync(0xffffffffu, wait(sm, bar, parity, err));
@@ -508,13 +516,13 @@ __device__ __noinline__ bool mma_role(uint32_t it0, uint32_t n, uint32_t parity)
   constexpr uint16_t kBoth = 3;
   bool ok = true;
   if (elect_one()) {
-    ok = wait(sm, sm.q_ready, parity, p.err);
+    ok = wait_awake(sm, sm.q_ready, parity, p.err);
 #pragma unroll 1
     for (uint32_t t = 0; t <= n && ok; ++t) {
       if (t < n) {
         const uint32_t it = it0 + t, xb = it % kXBufs, yb = it % kYBufs, tS = tmem + kColS + 64 * (it & 1u);
-        ok = wait(sm, sm.s_empty[it & 1u], ((it >> 1) & 1u) ^ 1u, p.err) && wait(sm, sm.x_full[xb], (it / kXBufs) & 1u, p.err) &&
-             wait(sm, sm.rope_full, it & 1u, p.err);
+        ok = wait_awake(sm, sm.s_empty[it & 1u], ((it >> 1) & 1u) ^ 1u, p.err) && wait_awake(sm, sm.x_full[xb], (it / kXBufs) & 1u, p.err) &&
+             wait_awake(sm, sm.rope_full, it & 1u, p.err);
         if (!ok) break;
         tc_fence_after();
         const uint32_t x = base + xb * kRegion, y = base + kYOff + yb * kRegion;
@@ -522,7 +530,7 @@ __device__ __noinline__ bool mma_role(uint32_t it0, uint32_t n, uint32_t parity)
         mma_commit_pair(smem_u32(&sm.rope_empty), kBoth);
 #pragma unroll
         for (int j = 0; j < 4; ++j) slab_ts(tS, tQ + 32 * j, x + j * kSlabBytes);
-        ok = wait(sm, sm.y_full[yb], (it / kYBufs) & 1u, p.err);
+        ok = wait_awake(sm, sm.y_full[yb], (it / kYBufs) & 1u, p.err);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
@@ -532,7 +540,7 @@ __device__ __noinline__ bool mma_role(uint32_t it0, uint32_t n, uint32_t parity)
       }
       if (t > 0) {
         const uint32_t it = it0 + t - 1, xb = it % kXBufs, yb = it % kYBufs;
-        ok = wait(sm, sm.v_full[it & 1u], (it >> 1) & 1u, p.err) && wait(sm, sm.p_full, it & 1u, p.err);
+        ok = wait_awake(sm, sm.v_full[it & 1u], (it >> 1) & 1u, p.err) && wait_awake(sm, sm.p_full, it & 1u, p.err);
         if (!ok) break;
         tc_fence_after();
         values(tO, base + kPOff + kSlabBytes, base + kYOff + yb * kRegion, t == 1);
