@@ -76,6 +76,7 @@ def _fast_dims(x: Sequence[int]) -> MLADims:
     return d
 
 
+_PLANES = _capi.MLARows * _capi.MAX_PLANES
 _DIMS: dict = {}
 _FN: dict = {}
 
@@ -92,13 +93,16 @@ def _i32(t: torch.Tensor, shape: tuple, name: str):
         raise TypeError(f"{name} must be a contiguous int32 {list(shape)} tensor")
 
 
-def _shape(t: torch.Tensor, shape: tuple, dtype: torch.dtype, name: str):
+def _shape(t: torch.Tensor, shape: tuple, dtype: torch.dtype, name: str) -> tuple:
+    """Checks a tensor with contiguous rows; its strides."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    if t.stride(-1) != 1 and shape[-1] > 1:
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
         _rows(t, name)
+    return st
 
 
 def _on_device(*tensors) -> int:
@@ -153,15 +157,17 @@ def _at(t: Optional[torch.Tensor]) -> Optional[int]:
 
 def _fp4_planes(d: MLADims, c4: torch.Tensor, kv_scale: torch.Tensor, k_r: Optional[torch.Tensor],
                 dtype: Optional[torch.dtype]):
-    """Shapes of a 4-bit cache; returns (B, n_max)."""
-    if c4.dim() != 3:
+    """Shapes of a 4-bit cache; returns (B, n_max, batch and row strides of c4, of kv_scale, of k_r)."""
+    shape = c4.shape
+    if len(shape) != 3:
         raise ValueError("c4 must be [B, n_max, d_c / 2]")
-    B, n_max = c4.shape[0], c4.shape[1]
-    _shape(c4, (B, n_max, d.d_c // 2), torch.uint8, "c4")
-    _shape(kv_scale, (B, n_max, d.d_c // 16), torch.uint8, "kv_scale")
-    if k_r is not None:
-        _shape(k_r, (B, n_max, d.d_r), dtype, "k_r")
-    return B, n_max
+    B, n_max, d_c = shape[0], shape[1], d.d_c
+    a = _shape(c4, (B, n_max, d_c // 2), torch.uint8, "c4")
+    b = _shape(kv_scale, (B, n_max, d_c // 16), torch.uint8, "kv_scale")
+    if k_r is None:
+        return B, n_max, a[0], a[1], b[0], b[1], 0, 0
+    c = _shape(k_r, (B, n_max, d.d_r), dtype, "k_r")
+    return B, n_max, a[0], a[1], b[0], b[1], c[0], c[1]
 
 
 def _token_stride(q: torch.Tensor, name: str) -> int:
@@ -526,17 +532,24 @@ def mla_cache_append_fp4(dims, kv_a: torch.Tensor, positions: torch.Tensor, c4: 
     [B, n_max, d_c / 2], kv_scale uint8 [B, n_max, d_c / 16] and k_r [B, n_max, d_r] may be views of one
     packed row.  latent_scale: a power of two, the same for every call on the cache."""
     d = _fast_dims(dims)
-    B, n_max = _fp4_planes(d, c4, kv_scale, k_r, kv_a.dtype)
-    if kv_a.dim() not in (2, 3):
+    dtype = kv_a.dtype
+    B, n_max, c4b, c4r, scb, scr, krb, krr = _fp4_planes(d, c4, kv_scale, k_r, dtype)
+    width = d.d_c + d.d_r
+    if kv_a.dim() == 3:
+        T = kv_a.shape[1]
+        lda = _shape(kv_a, (B, T, width), dtype, "kv_a")
+        lda_b, lda = lda[0], lda[1] if T > 1 else width
+    elif kv_a.dim() == 2:
+        T = 1
+        lda_b, lda = _shape(kv_a, (B, width), dtype, "kv_a")[0], width
+    else:
         raise ValueError("kv_a must be [B, d_c + d_r] or [B, T, d_c + d_r]")
-    T = kv_a.shape[1] if kv_a.dim() == 3 else 1
-    x = kv_a if kv_a.dim() == 3 else kv_a.unsqueeze(1)
-    _shape(x, (B, T, d.d_c + d.d_r), kv_a.dtype, "kv_a")
-    _i32(positions, (B,), "positions")
+    index = (B,)
+    _i32(positions, index, "positions")
     if rows is not None:
-        _i32(rows, (B,), "rows")
+        _i32(rows, index, "rows")
     if counts is not None:
-        _i32(counts, (B,), "counts")
+        _i32(counts, index, "counts")
     if gain is not None:
         _shape(gain, (d.d_c,), torch.float32, "gain")
     _flag(dev_err)
@@ -544,10 +557,9 @@ def mla_cache_append_fp4(dims, kv_a: torch.Tensor, positions: torch.Tensor, c4: 
     on, st = _launch_on(stream, dev)
     with on:
         check(_fn("mla_cache_append_fp4")(
-            d, _dt(kv_a), B, T, _at(x), x.stride(0), x.stride(1) if T > 1 else d.d_c + d.d_r, _at(gain), float(eps),
-            float(rope_base), float(latent_scale), _at(positions), _at(rows), _at(counts), n_max,
-            _at(c4), c4.stride(0), c4.stride(1), _at(kv_scale), kv_scale.stride(0), kv_scale.stride(1),
-            _at(k_r), k_r.stride(0), k_r.stride(1), _at(dev_err), st), "mla_cache_append_fp4")
+            d, _dtc(dtype), B, T, kv_a.data_ptr(), lda_b, lda, _at(gain), eps, rope_base, latent_scale,
+            positions.data_ptr(), _at(rows), _at(counts), n_max, c4.data_ptr(), c4b, c4r, kv_scale.data_ptr(), scb, scr,
+            k_r.data_ptr(), krb, krr, _at(dev_err), st), "mla_cache_append_fp4")
 
 
 def mla_cache_read_fp4(dims, c4: torch.Tensor, kv_scale: torch.Tensor, n: int, first: Optional[torch.Tensor] = None,
@@ -557,10 +569,12 @@ def mla_cache_read_fp4(dims, c4: torch.Tensor, kv_scale: torch.Tensor, n: int, f
     """The values of n latent rows per sequence of a 4-bit cache, from row first[b] on (int32 [B]; None: 0):
     out [B, n, d_c], zeros from counts[b] on (int32 [B]; None: n)."""
     d = _fast_dims(dims)
-    B, n_max = _fp4_planes(d, c4, kv_scale, None, None)
+    B, n_max, c4b, c4r, scb, scr, _, _ = _fp4_planes(d, c4, kv_scale, None, None)
+    shape = (B, n, d.d_c)
     if out is not None:
-        _shape(out, (B, n, d.d_c), out.dtype, "out")
-    code = _dtc(dtype if out is None else out.dtype)
+        dtype = out.dtype
+        strides = _shape(out, shape, dtype, "out")
+    code = _dtc(dtype)
     if first is not None:
         _i32(first, (B,), "first")
     if counts is not None:
@@ -570,11 +584,12 @@ def mla_cache_read_fp4(dims, c4: torch.Tensor, kv_scale: torch.Tensor, n: int, f
     on, st = _launch_on(stream, dev)
     with on:
         if out is None:
-            out = torch.empty((B, n, d.d_c), dtype=dtype, device=dev)
+            out = torch.empty(shape, dtype=dtype, device=dev)
+            strides = (n * d.d_c, d.d_c, 1)
         check(_fn("mla_cache_read_fp4")(
-            d, code, B, n, _at(first), _at(counts), n_max, _at(c4), c4.stride(0), c4.stride(1),
-            _at(kv_scale), kv_scale.stride(0), kv_scale.stride(1), float(latent_scale), _at(out), out.stride(0),
-            out.stride(1) if n > 1 else d.d_c, _at(dev_err), st), "mla_cache_read_fp4")
+            d, code, B, n, _at(first), _at(counts), n_max, c4.data_ptr(), c4b, c4r, kv_scale.data_ptr(), scb, scr,
+            latent_scale, out.data_ptr(), strides[0], strides[1] if n > 1 else d.d_c, _at(dev_err), st),
+            "mla_cache_read_fp4")
     return out
 
 
@@ -598,40 +613,41 @@ def mla_decode_absorb_fp4kv(dims, q_tilde: torch.Tensor, q_pe: torch.Tensor, c4:
     sequence being those tokens).  Any n_h <= 128 in bf16.  Returns ctx of q_tilde's shape; lse float32
     [B, n_h] or [B, T, n_h]."""
     d = _fast_dims(dims)
-    B, n_max = _fp4_planes(d, c4, kv_scale, k_r, q_tilde.dtype)
+    dtype = q_tilde.dtype
+    B, n_max, c4b, c4r, scb, scr, krb, krr = _fp4_planes(d, c4, kv_scale, k_r, dtype)
     T, ldqt, ldqp = _queries(d, q_tilde, q_pe, B, lengths)
     if ctx is not None:
-        _shape(ctx, q_tilde.shape, q_tilde.dtype, "ctx")
+        _shape(ctx, q_tilde.shape, dtype, "ctx")
+        if not ctx.is_contiguous():
+            raise ValueError("ctx and lse must be contiguous")
     if lse is not None:
         _shape(lse, q_tilde.shape[:-1], torch.float32, "lse")
-    if (ctx is not None and not ctx.is_contiguous()) or (lse is not None and not lse.is_contiguous()):
-        raise ValueError("ctx and lse must be contiguous")
+        if not lse.is_contiguous():
+            raise ValueError("ctx and lse must be contiguous")
     _flag(dev_err)
     dev = _on_device(q_tilde, q_pe, c4, kv_scale, k_r, lengths, ctx, lse, workspace, dev_err)
     on, st = _launch_on(stream, dev)
     with on:
         if ctx is None:
-            ctx = torch.empty(q_tilde.shape, dtype=q_tilde.dtype, device=dev)
+            ctx = torch.empty(q_tilde.shape, dtype=dtype, device=dev)
         if workspace is None:
-            nbytes = _fp4kv_workspace(dev, d.n_h, d.d_c, d.d_r, q_tilde.dtype, B, T, n_max)
-            workspace = torch.empty((max(nbytes, 16),), dtype=torch.uint8, device=dev)
+            nbytes = max(_fp4kv_workspace(dev, d.n_h, d.d_c, d.d_r, dtype, B, T, n_max), 16)
+            workspace = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
+        else:
+            nbytes = workspace.numel() * workspace.element_size()
         check(_fn("mla_decode_absorb_fp4kv")(
-            d, _dt(q_tilde), B, T, _at(q_tilde), ldqt, _at(q_pe), ldqp, _at(c4), c4.stride(0), c4.stride(1),
-            _at(kv_scale), kv_scale.stride(0), kv_scale.stride(1), _at(k_r), k_r.stride(0), k_r.stride(1),
-            float(latent_scale), n_max, _at(lengths), float(scale), _at(ctx), _at(lse), _at(workspace),
-            workspace.numel() * workspace.element_size(), _at(dev_err), st),
-            "mla_decode_absorb_fp4kv")
+            d, _dtc(dtype), B, T, q_tilde.data_ptr(), ldqt, q_pe.data_ptr(), ldqp, c4.data_ptr(), c4b, c4r,
+            kv_scale.data_ptr(), scb, scr, k_r.data_ptr(), krb, krr, latent_scale, n_max, lengths.data_ptr(), scale,
+            ctx.data_ptr(), _at(lse), workspace.data_ptr(), nbytes, _at(dev_err), st), "mla_decode_absorb_fp4kv")
     return ctx
 
 
-def _weight_arrays(acc: Optional[torch.Tensor], out: Optional[torch.Tensor], B: int, n_max: int):
-    for t, name in ((acc, "acc"), (out, "out")):
-        if t is not None:
-            _shape(t, (B, n_max), torch.float32, name)
-
-
-def _bstride(t: Optional[torch.Tensor], n_max: int) -> int:
-    return n_max if t is None or t.shape[0] == 1 else t.stride(0)
+def _weight_array(t: Optional[torch.Tensor], shape: tuple, name: str) -> int:
+    """Batch stride of acc or out."""
+    if t is None:
+        return shape[1]
+    st = _shape(t, shape, torch.float32, name)
+    return st[0] if shape[0] > 1 else shape[1]
 
 
 def mla_cache_weights(dims, q_tilde: torch.Tensor, q_pe: torch.Tensor, c_kv: torch.Tensor, k_r: torch.Tensor,
@@ -645,25 +661,26 @@ def mla_cache_weights(dims, q_tilde: torch.Tensor, q_pe: torch.Tensor, c_kv: tor
     d = _fast_dims(dims)
     if c_kv.dim() != 3:
         raise ValueError("c_kv must be [B, n_max, d_c]")
+    dtype = q_tilde.dtype
     B, n_max = c_kv.shape[0], c_kv.shape[1]
-    _shape(c_kv, (B, n_max, d.d_c), q_tilde.dtype, "c_kv")
-    _shape(k_r, (B, n_max, d.d_r), q_tilde.dtype, "k_r")
+    ckv = _shape(c_kv, (B, n_max, d.d_c), dtype, "c_kv")
+    kr = _shape(k_r, (B, n_max, d.d_r), dtype, "k_r")
     T, ldqt, ldqp = _queries(d, q_tilde, q_pe, B, lengths)
     _shape(lse, q_tilde.shape[:-1], torch.float32, "lse")
     if not lse.is_contiguous():
         raise ValueError("lse must be contiguous")
-    _weight_arrays(acc, out, B, n_max)
+    rows = (B, n_max)
+    acc_b, out_b = _weight_array(acc, rows, "acc"), _weight_array(out, rows, "out")
     _flag(dev_err)
     dev = _on_device(q_tilde, q_pe, c_kv, k_r, lengths, lse, acc, out, dev_err)
     on, st = _launch_on(stream, dev)
     with on:
         if out is None:
-            out = torch.zeros((B, n_max), dtype=torch.float32, device=dev)
+            out = torch.zeros(rows, dtype=torch.float32, device=dev)
         check(_fn("mla_cache_weights")(
-            d, _dt(q_tilde), B, T, _at(q_tilde), ldqt, _at(q_pe), ldqp, _at(c_kv), c_kv.stride(0), c_kv.stride(1),
-            _at(k_r), k_r.stride(0), k_r.stride(1), n_max, _at(lengths), float(scale), _at(lse), _at(acc),
-            _bstride(acc, n_max), float(decay), _at(out), _bstride(out, n_max), _at(dev_err),
-            st), "mla_cache_weights")
+            d, _dtc(dtype), B, T, q_tilde.data_ptr(), ldqt, q_pe.data_ptr(), ldqp, c_kv.data_ptr(), ckv[0], ckv[1],
+            k_r.data_ptr(), kr[0], kr[1], n_max, lengths.data_ptr(), scale, lse.data_ptr(), _at(acc), acc_b, decay,
+            out.data_ptr(), out_b, _at(dev_err), st), "mla_cache_weights")
     return out
 
 
@@ -674,23 +691,24 @@ def mla_cache_weights_fp4kv(dims, q_tilde: torch.Tensor, q_pe: torch.Tensor, c4:
                             stream=None) -> torch.Tensor:
     """mla_cache_weights over a 4-bit latent cache (planes as in mla_cache_append_fp4)."""
     d = _fast_dims(dims)
-    B, n_max = _fp4_planes(d, c4, kv_scale, k_r, q_tilde.dtype)
+    dtype = q_tilde.dtype
+    B, n_max, c4b, c4r, scb, scr, krb, krr = _fp4_planes(d, c4, kv_scale, k_r, dtype)
     T, ldqt, ldqp = _queries(d, q_tilde, q_pe, B, lengths)
     _shape(lse, q_tilde.shape[:-1], torch.float32, "lse")
     if not lse.is_contiguous():
         raise ValueError("lse must be contiguous")
-    _weight_arrays(acc, out, B, n_max)
+    rows = (B, n_max)
+    acc_b, out_b = _weight_array(acc, rows, "acc"), _weight_array(out, rows, "out")
     _flag(dev_err)
     dev = _on_device(q_tilde, q_pe, c4, kv_scale, k_r, lengths, lse, acc, out, dev_err)
     on, st = _launch_on(stream, dev)
     with on:
         if out is None:
-            out = torch.zeros((B, n_max), dtype=torch.float32, device=dev)
+            out = torch.zeros(rows, dtype=torch.float32, device=dev)
         check(_fn("mla_cache_weights_fp4kv")(
-            d, _dt(q_tilde), B, T, _at(q_tilde), ldqt, _at(q_pe), ldqp, _at(c4), c4.stride(0), c4.stride(1),
-            _at(kv_scale), kv_scale.stride(0), kv_scale.stride(1), _at(k_r), k_r.stride(0), k_r.stride(1),
-            float(latent_scale), n_max, _at(lengths), float(scale), _at(lse), _at(acc), _bstride(acc, n_max),
-            float(decay), _at(out), _bstride(out, n_max), _at(dev_err), st),
+            d, _dtc(dtype), B, T, q_tilde.data_ptr(), ldqt, q_pe.data_ptr(), ldqp, c4.data_ptr(), c4b, c4r,
+            kv_scale.data_ptr(), scb, scr, k_r.data_ptr(), krb, krr, latent_scale, n_max, lengths.data_ptr(), scale,
+            lse.data_ptr(), _at(acc), acc_b, decay, out.data_ptr(), out_b, _at(dev_err), st),
             "mla_cache_weights_fp4kv")
     return out
 
@@ -704,23 +722,26 @@ def mla_cache_evict(planes: Sequence[torch.Tensor], acc: torch.Tensor, lengths: 
     (e.g. [c_kv, k_r], [c4, kv_scale, k_r]; add acc.unsqueeze(-1) to keep it in step).  Returns
     (new_lengths int32 [B], which may be given as lengths itself, and row_map int32 [B, keep]: the row
     that row i held before, -1 from new_lengths[b] on)."""
-    planes = list(planes)
-    if not 1 <= len(planes) <= _capi.MAX_PLANES:
+    n_planes = len(planes)
+    if not 1 <= n_planes <= _capi.MAX_PLANES:
         raise ValueError(f"need 1 to {_capi.MAX_PLANES} planes")
     if acc.dim() != 2:
         raise ValueError("acc must be [B, n_max]")
-    B, n_max = acc.shape
-    _shape(acc, (B, n_max), torch.float32, "acc")
+    B, n_max = lead = tuple(acc.shape)
+    acc_b = _weight_array(acc, lead, "acc")
     _i32(lengths, (B,), "lengths")
-    rows = (_capi.MLARows * _capi.MAX_PLANES)()
+    rows = _PLANES()
     for i, p in enumerate(planes):
-        if p.dim() != 3 or tuple(p.shape[:2]) != (B, n_max):
-            raise ValueError(f"plane {i} must be [B, n_max, width] = [{B}, {n_max}, .], got {list(p.shape)}")
-        if p.shape[2] > 1:
+        shape = p.shape
+        if len(shape) != 3 or shape[:2] != lead:
+            raise ValueError(f"plane {i} must be [B, n_max, width] = [{B}, {n_max}, .], got {list(shape)}")
+        bs, rs, one = p.stride()
+        if one != 1 and shape[2] > 1:
             _rows(p, f"plane {i}")
         es = p.element_size()
-        width = p.shape[2] * es
-        rows[i] = _capi.MLARows(p.data_ptr(), p.stride(0) * es, p.stride(1) * es if n_max > 1 else width, width)
+        width = shape[2] * es
+        r = rows[i]
+        r.base, r.bstride, r.rstride, r.row_bytes = p.data_ptr(), bs * es, rs * es if n_max > 1 else width, width
     if new_lengths is not None:
         _i32(new_lengths, (B,), "new_lengths")
     if row_map is not None:
@@ -733,9 +754,9 @@ def mla_cache_evict(planes: Sequence[torch.Tensor], acc: torch.Tensor, lengths: 
             new_lengths = torch.empty((B,), dtype=torch.int32, device=dev)
         if row_map is None:
             row_map = torch.empty((B, max(keep, 0)), dtype=torch.int32, device=dev)
-        check(_fn("mla_cache_evict")(B, n_max, rows, len(planes), _at(acc), _bstride(acc, n_max), _at(lengths),
-                                    int(keep), int(sink), int(recent), _at(new_lengths), _at(row_map),
-                                    _at(dev_err), st), "mla_cache_evict")
+        check(_fn("mla_cache_evict")(B, n_max, rows, n_planes, acc.data_ptr(), acc_b, lengths.data_ptr(), keep, sink,
+                                     recent, new_lengths.data_ptr(), row_map.data_ptr(), _at(dev_err), st),
+              "mla_cache_evict")
     return new_lengths, row_map
 
 
