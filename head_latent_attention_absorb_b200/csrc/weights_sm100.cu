@@ -98,29 +98,40 @@ __device__ __forceinline__ void for_each_pass(const Params& p, const Smem& sm, F
   });
 }
 
-// One lane's part of a tile of the 4-bit cache: key t, 32 features of every latent slab and half the rotary
-// row; and the tile's slabs written in the layout of the TMA boxes.
+// One lane's part of the 16 keys that a warp decodes of a tile.  Four lanes cover the 64 bytes of codes that a
+// key has in two slabs, so an instruction of 512 bytes looks up eight lines; lanes of the second slab are two
+// rows ahead, so that the eight lanes of a store phase hit distinct banks.
 struct KeyPart {
-  uint4 code[8], scale[2], rope[4];
+  uint4 code[4][2];   // [pair of slabs][keys 0..7, 8..15]
+  uint4 scale[2][2];  // all 32 scales of the two keys
+  uint4 rope[4];      // eight lanes cover a key's rotary row: keys lane / 8 + 4 i
 };
-__device__ __forceinline__ void load_part(const Params& p, int b, int t, int len, int half, KeyPart& k) {
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+struct KeySource {
+  const uint8_t *code, *scale, *rope;  // the lane's first key
+  int left, left_rope;                 // keys from that one on that are in the sequence
+};
+__device__ __forceinline__ int code_row(int lane) { return ((lane >> 2) + (lane & 2)) & 7; }
+__device__ __forceinline__ KeySource key_source(const Params& p, int b, int64_t first, int len, int lane) {
+  const int64_t t = first + code_row(lane), u = first + (lane >> 3);
+  return {p.kv.c4 + b * p.kv.c4_b + t * p.kv.c4_r + 16 * (lane & 3), p.kv.sc + b * p.kv.sc_b + t * p.kv.sc_r,
+          static_cast<const uint8_t*>(p.kv.k_r) + 2 * (b * p.kv.kr_b + u * p.kv.kr_r) + 16 * (lane & 7),
+          (int)(len - t), (int)(len - u)};
+}
+// Rows behind the sequence may hold anything, or not exist: they are zeros.
+__device__ __forceinline__ uint4 load_row(const uint8_t* src, bool present) {
+  return present ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0u, 0u, 0u, 0u);
+}
+__device__ __forceinline__ void load_codes(const Params& p, const KeySource& s, int pair, KeyPart& k) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) k.code[j] = zero;
+  for (int i = 0; i < 2; ++i) k.code[pair][i] = load_row(s.code + 8 * i * p.kv.c4_r + 64 * pair, 8 * i < s.left);
+}
+__device__ __forceinline__ void load_scales(const Params& p, const KeySource& s, int h, KeyPart& k) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) k.rope[j] = zero;
-  k.scale[0] = k.scale[1] = zero;
-  if (t >= len) return;  // rows behind the sequence may hold anything, or not exist
-  const uint4* c = reinterpret_cast<const uint4*>(p.kv.c4 + b * p.kv.c4_b + t * p.kv.c4_r) + half;
-  const uint4* s = reinterpret_cast<const uint4*>(p.kv.sc + b * p.kv.sc_b + t * p.kv.sc_r);
-  const uint4* r = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.kv.k_r) + b * p.kv.kr_b +
-                                                  t * p.kv.kr_r) + 4 * half;
+  for (int i = 0; i < 2; ++i) k.scale[i][h] = load_row(s.scale + 8 * i * p.kv.sc_r + 16 * h, 8 * i < s.left);
+}
+__device__ __forceinline__ void load_rope(const Params& p, const KeySource& s, KeyPart& k) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) k.code[j] = __ldg(c + 2 * j);
-  k.scale[0] = __ldg(s);
-  k.scale[1] = __ldg(s + 1);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) k.rope[j] = __ldg(r + j);
+  for (int i = 0; i < 4; ++i) k.rope[i] = load_row(s.rope + 8 * i * p.kv.kr_r, 4 * i < s.left_rope);
 }
 
 template <bool kFp4>
@@ -292,46 +303,61 @@ __global__ void __launch_bounds__(kFp4 ? kThreadsFp4 : kThreadsBf16, 1) weights_
     });
   } else if (kFp4 && warp >= kDecodeWarp0) {
     // ---------------------------------------------------------------- 4-bit keys to bf16 slabs
-    // Lane pairs own a key: each lane 32 of the 64 features of every slab, so a load instruction reads whole
-    // 32-byte sectors and the eight lanes of a store phase hit distinct banks.
-    const int row = 16 * (warp - kDecodeWarp0) + (lane >> 1), half = lane & 1;
-    const uint32_t dst_row = ring + row * 128;
+    // Each load of the next tile follows the last use of its registers, so a tile's time passes before it is
+    // needed.
+    const int row0 = 16 * (warp - kDecodeWarp0), row = code_row(lane), slab = (lane >> 1) & 1, half = lane & 1;
+    const uint32_t dst_codes = ring + (row0 + row) * 128, dst_rope = ring + (row0 + (lane >> 3)) * 128;
     uint32_t n = 0;
     KeyPart k;
     for_each_pass(p, sm, [&](int b, int len, int, int t0, int t1) {
-      load_part(p, b, t0 * kTile + row, len, half, k);
-      for (int t = t0; t < t1; ++t) {
+      KeySource s = key_source(p, b, (int64_t)t0 * kTile + row0, len, lane);
 #pragma unroll
-        for (int j = 0; j < kSlabs; ++j, ++n) {
-          const uint32_t st = n % kStages;
-          if (!__all_sync(0xffffffffu, wait(sm, sm.empty[st], ((n / kStages) & 1u) ^ 1u, p.err))) return false;
-          const uint32_t dst = dst_row + st * kSlabBytes;
-          if (j < kSlabs - 1) {
-            const uint32_t sw[8] = {k.scale[0].x, k.scale[0].y, k.scale[0].z, k.scale[0].w,
-                                    k.scale[1].x, k.scale[1].y, k.scale[1].z, k.scale[1].w};
-            const float2 s2 = unpack_f16x2(fp4::scales_to_f16(sw[j] >> (16 * half)));
+      for (int j = 0; j < 4; ++j) load_codes(p, s, j, k);
+      load_scales(p, s, 0, k);
+      load_scales(p, s, 1, k);
+      load_rope(p, s, k);
+      for (int t = t0; t < t1; ++t) {
+        s = key_source(p, b, (int64_t)(t + 1) * kTile + row0, t + 1 < t1 ? len : 0, lane);
+#pragma unroll
+        for (int j = 0; j < 4; ++j, n += 2) {
+          bool ok = true;
+          for (uint32_t m = n; m < n + 2; ++m) ok &= wait(sm, sm.empty[m % kStages], ((m / kStages) & 1u) ^ 1u, p.err);
+          if (!__all_sync(0xffffffffu, ok)) return false;
+          const uint32_t dst = dst_codes + (n + slab) % kStages * kSlabBytes;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint4 q = k.scale[i][j >> 1];
+            const uint32_t sw = (j & 1) ? (slab ? q.w : q.z) : (slab ? q.y : q.x);
+            const float2 s2 = unpack_f16x2(fp4::scales_to_f16(sw >> (16 * half)));
             const float s0 = s2.x * p.kv.latent_scale, s1 = s2.y * p.kv.latent_scale;
             const uint32_t scale[2] = {pack_bf16x2(s0, s0), pack_bf16x2(s1, s1)};
-            const uint32_t words[4] = {k.code[j].x, k.code[j].y, k.code[j].z, k.code[j].w};
+            const uint32_t words[4] = {k.code[j][i].x, k.code[j][i].y, k.code[j][i].z, k.code[j][i].w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int w = 0; w < 4; ++w) {
               uint32_t h[4];
-              fp4::codes_to_bf16(words[i], h);
+              fp4::codes_to_bf16(words[w], h);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) h[e] = fp4::mul_bf16x2(h[e], scale[i >> 1]);
-              st_shared_v4_b32(dst + (((4 * half + i) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
+              for (int e = 0; e < 4; ++e) h[e] = fp4::mul_bf16x2(h[e], scale[w >> 1]);
+              st_shared_v4_b32(dst + 1024 * i + (((4 * half + w) ^ row) << 4), h[0], h[1], h[2], h[3]);
             }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              st_shared_v4_b32(dst + (((4 * half + i) ^ (row & 7)) << 4), k.rope[i].x, k.rope[i].y, k.rope[i].z,
-                               k.rope[i].w);
-            if (t + 1 < t1) load_part(p, b, (t + 1) * kTile + row, len, half, k);
           }
+          load_codes(p, s, j, k);
+          if (j & 1) load_scales(p, s, j >> 1, k);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sm.full[st]));
+          if (lane < 2) mbar_arrive(smem_u32(&sm.full[(n + lane) % kStages]));
         }
+        const uint32_t st = n % kStages;
+        if (!__all_sync(0xffffffffu, wait(sm, sm.empty[st], ((n / kStages) & 1u) ^ 1u, p.err))) return false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          st_shared_v4_b32(dst_rope + st * kSlabBytes + 512 * i + (((lane & 7) ^ ((lane >> 3) + 4 * (i & 1))) << 4),
+                           k.rope[i].x, k.rope[i].y, k.rope[i].z, k.rope[i].w);
+        load_rope(p, s, k);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.full[st]));
+        ++n;
       }
       return true;
     });
