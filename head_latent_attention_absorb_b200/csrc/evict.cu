@@ -8,7 +8,8 @@
 // destinations before it, no row is read after it was written: the move needs no order and no copy.
 //
 // Two launches: the selection writes row_map (a cluster of eight CTAs per sequence, each with a slice of the
-// rows, or one CTA for a short sequence; counts, ranks and the list of moved rows cross through distributed shared memory), the move reads it.
+// rows, or one CTA for a short sequence; counts, ranks and the list of moved rows cross through distributed
+// shared memory), the move reads it.
 #include <math.h>
 
 #include "common.cuh"
@@ -18,12 +19,23 @@
 namespace mla {
 namespace {
 
-constexpr int kThreads = 512;   // of a CTA of the selection
+constexpr int kThreads = 1024;  // of a CTA of the selection
+constexpr int kWarps = kThreads / 32;
 constexpr int kCluster = 8;     // CTAs that share a sequence
-constexpr int kOneCta = 8192;     // rows that one CTA selects from by itself
+constexpr int kOneCta = 8192, kOneCtaFull = 32768;  // rows that one CTA selects from by itself
 constexpr int kSelectSmem = 220 * 1024;
-constexpr int kMaxRows = 400000;  // 4.5 bytes of a CTA's shared memory for kCluster rows
+constexpr int kMaxRows = 400000;  // a slice of them is counted in 16 bits
 constexpr int kWord = 32;       // rows of one word of the kept mask
+constexpr int kBatch = 4;       // keys, or words of the mask, that are read together
+// Digits of the radix selection, from the top.  One CTA takes 11, 11 and 10 bits: the first digit holds the sign,
+// the exponent and two bits of the fraction, which spreads weights of one size over enough counters that a warp's
+// additions seldom meet, and two digits mostly decide.  A cluster, which reads eight arrays of counts, takes 8 bits.
+template <int C>
+constexpr int kDigitBits = C == 1 ? 11 : 8;
+template <int C>
+constexpr int kBins = 1 << kDigitBits<C>;
+template <int C>
+constexpr int kPasses = (32 + kDigitBits<C> - 1) / kDigitBits<C>;
 
 // Order-preserving map of a float to 32 bits: NaN is the least, -0 equals +0.
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -47,42 +59,35 @@ __device__ __forceinline__ void st_cluster(int* p, uint32_t rank, int v) {
   asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(sm100::mapa(sm100::smem_u32(p), rank)), "r"(v) : "memory");
 }
 
+// Integers of the list of a slice of `per` words; the counts of the digits lie there before.  The moved rows are at
+// most half of all rows: they lie behind `keep` and fill holes before it.
+template <int C>
+__host__ __device__ constexpr int list_ints(int per) {
+  return per * kWord / 2 > kPasses<C> * kBins<C> ? per * kWord / 2 : kPasses<C> * kBins<C>;
+}
+
+struct Found {
+  int digit, rank;  // the digit that holds the threshold, and how many of its rows are to be taken
+  int rows, lower;  // the rows that have it, and those of them in the slices before this one
+};
 struct SelectSmem {
-  int hist[4][256];        // this CTA's counts, one array for each digit
-  int warp_sums[2][kThreads / 32];
-  int bin, rank;           // the digit found and what is still to be taken of its keys
-  int mine[2];             // this CTA's holes and moved rows
+  uint32_t sums[kPasses<kCluster> + 2][kWarps];
+  Found found[2];
+  int mine[2];  // this CTA's holes and moved rows
 };
 
-// Exclusive prefix sums of two values over the block's threads; total gets the sums.
-__device__ __forceinline__ int2 block_scan(int2 v, int (&warp_sums)[2][kThreads / 32], int2* total) {
+// Inclusive prefix sum over the block's threads; the array is written by this call alone.
+__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t (&warp_sums)[kWarps]) {
+  static_assert(kWarps == 32, "a lane has a warp's sum");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int2 x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y0 = __shfl_up_sync(0xffffffffu, x.x, o), y1 = __shfl_up_sync(0xffffffffu, x.y, o);
-    if (lane >= o) {
-      x.x += y0;
-      x.y += y1;
-    }
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
+  if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
-  if (lane == 31) {
-    warp_sums[0][warp] = x.x;
-    warp_sums[1][warp] = x.y;
-  }
-  __syncthreads();
-  int2 before = make_int2(0, 0), all = make_int2(0, 0);
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    const int s0 = warp_sums[0][w], s1 = warp_sums[1][w];
-    before.x += w < warp ? s0 : 0;
-    before.y += w < warp ? s1 : 0;
-    all.x += s0;
-    all.y += s1;
-  }
-  *total = all;
-  return make_int2(x.x - v.x + before.x, x.y - v.y + before.y);
+  return x + __reduce_add_sync(0xffffffffu, lane < warp ? warp_sums[lane] : 0u);
 }
 
 // Sum of the lower-ranked CTAs' value, once the cluster has met.
@@ -110,7 +115,7 @@ __device__ __forceinline__ void meet() {
 template <int C>
 __device__ __forceinline__ void select_rows(const EvictArgs& a, bool keys_in_smem) {
   __shared__ SelectSmem sm;
-  extern __shared__ int dyn[];
+  extern __shared__ __align__(16) int dyn[];
   sm100::griddep_launch_dependents();
   sm100::griddep_wait();
   const int b = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -133,86 +138,116 @@ __device__ __forceinline__ void select_rows(const EvictArgs& a, bool keys_in_sme
   const int r0 = min((int)rank * per * kWord, len), r1 = min(r0 + per * kWord, len);
   uint32_t* kept = reinterpret_cast<uint32_t*>(dyn);   // [per] kept rows of the slice
   uint32_t* tied = kept + per;                         // [per] rows at the threshold
-  int* holes_before = dyn + 2 * per;                   // [per]
-  int* moved_before = dyn + 3 * per;                   // [per]
-  int* list = dyn + 4 * per;                           // [per * 32] a part of the moved rows, in order
-  uint32_t* keys = reinterpret_cast<uint32_t*>(list) + per * kWord;  // [per * 32], where they fit
+  uint32_t* counts_before = tied + per;                // [per] holes and moved rows of the slice before each word
+  int* list = dyn + (3 * per + 3) / 4 * 4;             // a part of the moved rows, in order
+  int* hist = list;  // [kPasses][kBins] this CTA's counts of each digit, before the list is made
+  uint32_t* keys = reinterpret_cast<uint32_t*>(list) + list_ints<C>(per);  // [per * 32], where they fit
   const int lo = a.sink, hi = len - a.recent;          // rows that compete
   const int c0 = max(r0, lo), c1 = min(r1, hi);
   const int want = a.keep - a.sink - a.recent;
-  auto key = [&](int t) { return keys_in_smem ? keys[t - r0] : order_key(acc[t]); };
 
-  for (int i = tid; i < 4 * 256; i += kThreads) sm.hist[i >> 8][i & 255] = 0;
-  if (keys_in_smem) {
-#pragma unroll 8
-    for (int t = r0 + tid; t < r1; t += kThreads) keys[t - r0] = order_key(acc[t]);
-  }
+  for (int i = tid; i < kPasses<C> * kBins<C>; i += kThreads) hist[i] = 0;
   __syncthreads();
-  // radix select, eight bits a pass from the top: the want-th largest key
+  // radix select from the top: the want-th largest key, or as much of it as tells the kept rows from the others
   uint32_t prefix = 0u, mask = 0u;
   int left = want;  // keys equal to the prefix still to be taken
   int ties_before = 0;
-  for (int pass = 0; pass < 4 && want > 0; ++pass) {
-    const int shift = 24 - 8 * pass;
-#pragma unroll 4
-    for (int t = c0 + tid; t < c1; t += kThreads) {
-      const uint32_t k = key(t);
-      if ((k & mask) == prefix) atomicAdd(&sm.hist[pass][(k >> shift) & 255u], 1);
+  bool ties_all = true;  // every row at the threshold is kept
+  for (int pass = 0, bits = 32; bits > 0 && want > 0; ++pass) {
+    const int width = min(bits, kDigitBits<C>), shift = bits - width;
+    const uint32_t digit = (1u << width) - 1u;
+    int* count = hist + pass * kBins<C>;
+    for (int f = c0; f < c1; f += kBatch * kThreads) {
+      const int t0 = f + tid, some = (c1 - f + kThreads - 1) / kThreads;  // the block has keys in so many of the batch
+      uint32_t k[kBatch];
+      if (pass == 0 || !keys_in_smem) {
+        float v[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          if (i < some) v[i] = t0 + i * kThreads < c1 ? acc[t0 + i * kThreads] : 0.f;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          if (i < some) {
+            k[i] = order_key(v[i]);
+            if (keys_in_smem && t0 + i * kThreads < c1) keys[t0 + i * kThreads - r0] = k[i];
+          }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          if (i < some) k[i] = t0 + i * kThreads < c1 ? keys[t0 + i * kThreads - r0] : 0u;
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (i < some && t0 + i * kThreads < c1 && (k[i] & mask) == prefix) atomicAdd(&count[(k[i] >> shift) & digit], 1);
     }
     meet<C>();
-    if (tid < 256) {  // thread t sums digit 255 - t over the cluster, each CTA for itself
-      int n = 0, lower = 0;
+    // thread t sums its digits over the cluster, in descending order, each CTA for itself
+    constexpr int kOwn = kBins<C> > kThreads ? kBins<C> / kThreads : 1;
+    const int top = kBins<C> - 1 - kOwn * tid;
+    int n[kOwn] = {}, lower[kOwn] = {}, sum = 0;
+    if (top >= 0) {
 #pragma unroll
-      for (uint32_t r = 0; r < C; ++r) {
-        const int v = C == 1 ? sm.hist[pass][255 - tid] : ld_cluster(&sm.hist[pass][255 - tid], r);
-        n += v;
-        lower += r < rank ? v : 0;
-      }
-      // descending digits: inclusive prefix sums find the one that holds rank `left`
-      int x = n;
+      for (uint32_t r = 0; r < C; ++r)
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (lane == 31) sm.warp_sums[0][warp] = x;
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+        for (int i = 0; i < kOwn; ++i) {
+          const int v = C == 1 ? count[top - i] : ld_cluster(&count[top - i], r);
+          n[i] += v;
+          lower[i] += r < rank ? v : 0;
+          sum += v;
+        }
+    }
+    const int x = block_scan(sum, sm.sums[pass]);  // the prefix sums find the digit that holds rank `left`
+    int above = x - sum;
+    if (x >= left && above < left) {
 #pragma unroll
-      for (int w = 0; w < 7; ++w) x += w < warp ? sm.warp_sums[0][w] : 0;
-      if (x >= left && x - n < left) {
-        sm.bin = 255 - tid;
-        sm.rank = left - (x - n);
-        sm.mine[0] = lower;  // (in the last pass: rows at the threshold in the slices before this one)
+      for (int i = 0; i < kOwn; ++i) {
+        if (above < left && above + n[i] >= left) sm.found[pass & 1] = {top - i, left - above, n[i], lower[i]};
+        above += n[i];
       }
     }
     __syncthreads();
-    prefix |= (uint32_t)sm.bin << shift;
-    left = sm.rank;
-    ties_before = sm.mine[0];
-    mask |= 255u << shift;
-    __syncthreads();
+    const Found f = sm.found[pass & 1];
+    prefix |= (uint32_t)f.digit << shift;
+    mask |= digit << shift;
+    left = f.rank;
+    ties_before = f.lower;
+    ties_all = f.rows == f.rank;
+    bits = ties_all ? 0 : shift;
   }
 
   // kept and tied rows of the slice
-  for (int w = warp; w < per; w += kThreads / 32) {
-    const int t = r0 + w * kWord + lane;
-    const bool inside = t >= lo && t < hi && t < r1;
-    const uint32_t k = inside && want > 0 ? key(t) : 0u;
-    const uint32_t keep_w = __ballot_sync(0xffffffffu, inside ? want > 0 && k > prefix : t < r1);
-    const uint32_t tie_w = __ballot_sync(0xffffffffu, inside && want > 0 && k == prefix);
-    if (lane == 0) {
-      kept[w] = keep_w;
-      tied[w] = tie_w;
+  for (int wb = warp; wb < per; wb += kBatch * kWarps) {
+    const int some = (per - wb + kWarps - 1) / kWarps;
+    uint32_t k[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int t = r0 + (wb + i * kWarps) * kWord + lane;
+      k[i] = 0u;
+      if (i < some && t >= c0 && t < c1 && want > 0) k[i] = keys_in_smem ? keys[t - r0] : order_key(acc[t]);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (i >= some) break;
+      const int w = wb + i * kWarps, t = r0 + w * kWord + lane;
+      const bool inside = t >= lo && t < hi && t < r1;
+      const uint32_t keep_w = __ballot_sync(0xffffffffu, inside ? want > 0 && (k[i] & mask) > prefix : t < r1);
+      const uint32_t tie_w = __ballot_sync(0xffffffffu, inside && want > 0 && (k[i] & mask) == prefix);
+      if (lane == 0) {
+        kept[w] = keep_w;
+        tied[w] = tie_w;
+      }
     }
   }
   __syncthreads();
   // contiguous chunks of words for each thread, so that ranks follow from a scan over the threads
   const int chunk = (per + kThreads - 1) / kThreads;
   const int w0 = min(tid * chunk, per), w1 = min(w0 + chunk, per);
-  int ties = 0;
-  int2 total;
-  for (int w = w0; w < w1; ++w) ties += __popc(tied[w]);
-  int before = ties_before + block_scan(make_int2(ties, 0), sm.warp_sums, &total).x;
+  int before = 0;  // rows at the threshold before this thread's
+  if (!ties_all) {
+    uint32_t ties = 0;
+    for (int w = w0; w < w1; ++w) ties += __popc(tied[w]);
+    before = ties_before + (int)(block_scan(ties, sm.sums[kPasses<kCluster>]) - ties);
+  }
   auto below = [&](int w) {  // bits of the word whose row is below keep
     const int first = r0 + w * kWord;
     return first + kWord <= a.keep ? 0xffffffffu : first >= a.keep ? 0u : (1u << (a.keep - first)) - 1u;
@@ -221,10 +256,10 @@ __device__ __forceinline__ void select_rows(const EvictArgs& a, bool keys_in_sme
     const int n = r1 - (r0 + w * kWord);
     return n >= kWord ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
   };
-  int2 count = make_int2(0, 0);  // holes, moved rows
+  uint32_t count = 0u;  // holes, and 65536 times moved rows: a slice has at most 50000 rows
   for (int w = w0; w < w1; ++w) {
     const uint32_t tie = tied[w];
-    const int here = __popc(tie), take = max(0, min(here, left - before));
+    const int here = __popc(tie), take = ties_all ? here : max(0, min(here, left - before));
     before += here;
     uint32_t k = kept[w];
     if (take == here)
@@ -232,46 +267,60 @@ __device__ __forceinline__ void select_rows(const EvictArgs& a, bool keys_in_sme
     else if (take > 0)
       k |= tie & ((1u << nth_bit(tie, take)) - 1u);
     kept[w] = k;
-    holes_before[w] = count.x;
-    moved_before[w] = count.y;
-    count.x += __popc(~k & rows_of(w) & below(w));
-    count.y += __popc(k & ~below(w));
+    counts_before[w] = count;
+    count += __popc(~k & rows_of(w) & below(w)) + (__popc(k & ~below(w)) << 16);
   }
-  const int2 at = block_scan(count, sm.warp_sums, &total);
-  for (int w = w0; w < w1; ++w) {
-    holes_before[w] += at.x;
-    moved_before[w] += at.y;
-  }
-  if (tid == 0) {
-    sm.mine[0] = total.x;
-    sm.mine[1] = total.y;
+  const uint32_t upto = block_scan(count, sm.sums[kPasses<kCluster> + 1]);
+  for (int w = w0; w < w1; ++w) counts_before[w] += upto - count;
+  if (tid == kThreads - 1) {
+    sm.mine[0] = upto & 0xffffu;
+    sm.mine[1] = upto >> 16;
   }
   meet<C>();
   const int holes0 = before_me<C>(&sm.mine[0], rank), moved0 = before_me<C>(&sm.mine[1], rank);
-  // the moved rows in order, spread over the cluster (there are fewer than rows, so a slice's worth fits)
-  const int room = per * kWord;
-  for (int w = warp; w < per; w += kThreads / 32) {
-    const uint32_t k = kept[w] & ~below(w);
-    if ((k >> lane) & 1u) {
-      const int m = moved0 + moved_before[w] + __popc(k & ((1u << lane) - 1u)), row = r0 + w * kWord + lane;
-      if (C == 1)
-        list[m % room] = row;
-      else
-        st_cluster(&list[m % room], (uint32_t)(m / room) % C, row);
+  // the moved rows in order, dealt out over the cluster
+  for (int wb = warp; wb < per; wb += kBatch * kWarps) {
+    const int some = (per - wb + kWarps - 1) / kWarps;
+    uint32_t k[kBatch];
+    int m[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int w = wb + i * kWarps;
+      if (i >= some) break;
+      k[i] = kept[w] & ~below(w);
+      m[i] = moved0 + (int)(counts_before[w] >> 16) + __popc(k[i] & ((1u << lane) - 1u));
     }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (i < some && ((k[i] >> lane) & 1u)) {
+        const int row = r0 + (wb + i * kWarps) * kWord + lane;
+        if (C == 1)
+          list[m[i]] = row;
+        else
+          st_cluster(&list[(uint32_t)m[i] / C], (uint32_t)m[i] % C, row);
+      }
   }
   meet<C>();
   // hole j takes the j-th of them
-  for (int w = warp; w < per; w += kThreads / 32) {
-    const uint32_t in = rows_of(w) & below(w);
-    if (in == 0u) continue;
-    const uint32_t hole = ~kept[w] & in;
-    int src = r0 + w * kWord + lane;
-    if ((hole >> lane) & 1u) {
-      const int h = holes0 + holes_before[w] + __popc(hole & ((1u << lane) - 1u));
-      src = C == 1 ? list[h % room] : ld_cluster(&list[h % room], (uint32_t)(h / room) % C);
+  for (int wb = warp; wb < per; wb += kBatch * kWarps) {
+    const int some = (per - wb + kWarps - 1) / kWarps;
+    int h[kBatch], src[kBatch];
+    uint32_t in[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int w = wb + i * kWarps;
+      if (i >= some) break;
+      in[i] = rows_of(w) & below(w);
+      const uint32_t hole = ~kept[w] & in[i];
+      src[i] = r0 + w * kWord + lane;
+      h[i] = (hole >> lane) & 1u ? holes0 + (int)(counts_before[w] & 0xffffu) + __popc(hole & ((1u << lane) - 1u)) : -1;
     }
-    if ((in >> lane) & 1u) map[r0 + w * kWord + lane] = src;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (i < some && h[i] >= 0) src[i] = C == 1 ? list[h[i]] : ld_cluster(&list[(uint32_t)h[i] / C], (uint32_t)h[i] % C);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (i < some && ((in[i] >> lane) & 1u)) map[r0 + (wb + i * kWarps) * kWord + lane] = src[i];
   }
   if (rank == 0 && tid == 0) a.new_lengths[b] = a.keep;
   if (C > 1) meet<C>();  // no CTA leaves while another one may read its part of the list
@@ -350,11 +399,12 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a) {
     }
 }
 
-// Shared memory of a CTA of the selection: four words of masks and counts and a list entry for every row of a slice,
-// and the keys.
-size_t select_smem_bytes(int n_max, int ctas, bool keys) {
-  const size_t words = (n_max + kWord - 1) / kWord, per = (words + ctas - 1) / ctas;
-  return per * (16 + 4 * kWord * (keys ? 2 : 1));
+// Shared memory of a CTA of the selection: masks and counts for each word, the list (or, before it, the
+// counts of the digits) and the keys.
+template <int C>
+size_t select_smem_bytes(int n_max, bool keys) {
+  const size_t words = (n_max + kWord - 1) / kWord, per = (words + C - 1) / C;
+  return 16 * ((3 * per + 3) / 4) + 4 * ((size_t)list_ints<C>((int)per) + (keys ? per * kWord : 0));
 }
 
 }  // namespace
@@ -362,17 +412,19 @@ size_t select_smem_bytes(int n_max, int ctas, bool keys) {
 int evict_max_rows() { return kMaxRows; }
 
 cudaError_t evict_launch(const EvictArgs& a, cudaStream_t st) {
-  // One CTA for a sequence of up to kOneCta rows: a meeting of a cluster takes about a microsecond, a pass of one
-  // CTA over that many keys in shared memory less.
-  const bool one = a.n_max <= kOneCta;
-  const int ctas = one ? 1 : kCluster;
-  const bool keys = select_smem_bytes(a.n_max, ctas, true) <= kSelectSmem;
-  const size_t smem = select_smem_bytes(a.n_max, ctas, keys);
+  // One CTA for a sequence of up to kOneCta rows: the meetings of a cluster take longer than the passes of one CTA over
+  // the keys in its shared memory (8 sequences, one CTA / a cluster: 1024 rows 13 / 18 us, 4096 16 / 20, 8192 20 / 23,
+  // 16384 30 / 25).  As long as the keys fit, too, where clusters would not all run at once: two CTAs of this size share
+  // an SM (64 sequences: 4096 rows 19 / 66 us, 16384 51 / 93, 32768 110 / 150).
+  const bool one = a.n_max <= kOneCta || (a.n_max <= kOneCtaFull && a.B > 2 * sm_count() / kCluster);
+  const auto bytes = one ? select_smem_bytes<1> : select_smem_bytes<kCluster>;
+  const bool keys = bytes(a.n_max, true) <= kSelectSmem;
+  const size_t smem = bytes(a.n_max, keys);
   static int allowed_one[kMaxDevices], allowed_cluster[kMaxDevices];
   cudaError_t e = one ? allow_smem(reinterpret_cast<const void*>(evict_select_one), kSelectSmem, allowed_one)
                       : allow_smem(reinterpret_cast<const void*>(evict_select_cluster), kSelectSmem, allowed_cluster);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(one ? evict_select_one : evict_select_cluster, dim3(a.B * ctas), dim3(kThreads), smem, st, a, keys);
+  e = launch_pdl(one ? evict_select_one : evict_select_cluster, dim3(a.B * (one ? 1 : kCluster)), dim3(kThreads), smem, st, a, keys);
   if (e != cudaSuccess) return e;
   // the widest element that every plane's base, strides and rows are multiples of
   uintptr_t bits = 0;

@@ -208,6 +208,22 @@ def test_evict_long_sequences():
     assert run_evict([100000, 60001, 5], 100000, 40000, 4, 1024, widths=((8, torch.uint8),), seed=3) == 0
 
 
+@pytest.mark.parametrize("B,n_max", [(2, 8192), (2, 8193), (40, 8193), (40, 32768), (40, 32769), (2, 32769)])
+def test_evict_one_cta_and_cluster(B, n_max):
+    lengths = [n_max - 37 * b for b in range(B)]
+    assert run_evict(lengths, n_max, n_max // 2 + 1, 5, 333, widths=((4, torch.uint8),), seed=B + n_max) == 0
+
+
+@pytest.mark.parametrize("kind", ["equal", "two", "nan", "low_bits"])
+@pytest.mark.parametrize("keep,sink,recent", [(7000, 2500, 2600), (11999, 0, 0), (5000, 2000, 3000), (1, 0, 0)])
+def test_evict_ties_in_a_cluster(kind, keep, sink, recent):
+    n, g = 12000, torch.Generator().manual_seed(2)
+    acc = {"equal": torch.full((2, n), -0.3), "two": (torch.rand((2, n), generator=g) > 0.5).float(),
+           "nan": torch.where(torch.rand((2, n), generator=g) > 0.4, float("nan"), 1.0),
+           "low_bits": 1.0 + torch.randint(0, 40, (2, n), generator=g) * 2.0 ** -23}[kind]
+    assert run_evict([n, n - 1777], n, keep, sink, recent, acc=acc, widths=((16, torch.uint8),)) == 0
+
+
 def test_evict_repeats_in_a_graph():
     n, keep = 4000, 1500
     acc = torch.rand((3, n), device=DEV)
