@@ -134,6 +134,29 @@ __device__ __forceinline__ void load_rope(const Params& p, const KeySource& s, K
   for (int i = 0; i < 4; ++i) k.rope[i] = load_row(s.rope + 8 * i * p.kv.kr_r, 4 * i < s.left_rope);
 }
 
+// The sum of exp over a key's columns [0, cols) of the accumulator at `src`; kSelect: without those before `first`,
+// whose tokens do not see the key, and those whose -lse at `nl` (log2 units) is -infinity.
+template <bool kSelect>
+__device__ __forceinline__ float key_sum(uint32_t src, uint32_t nl, int cols, float scale_log2, int first) {
+  float w[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int c = 0; c < cols; c += 32) {
+    uint32_t s[32];
+    tmem_ld32(src + c, s);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      const float4 l4 = ld_shared_v4(nl + 4 * (c + i));
+      const float l[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = ex2f_approx(fmaf(__uint_as_float(s[i + e]), scale_log2, l[e]));
+        w[e] += kSelect && (c + i + e < first || l[e] == -INFINITY) ? 0.f : x;
+      }
+    }
+  }
+  return (w[0] + w[1]) + (w[2] + w[3]);
+}
+
 template <bool kFp4>
 __global__ void __launch_bounds__(kFp4 ? kThreadsFp4 : kThreadsBf16, 1) weights_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -263,41 +286,27 @@ __global__ void __launch_bounds__(kFp4 ? kThreadsFp4 : kThreadsBf16, 1) weights_
       const uint32_t nl = smem_u32(sm.neg_lse);
       for (int t = t0; t < t1 && !dead; ++t, ++tile) {
         const uint32_t buf = tile & 1u, src = tmem + ((uint32_t)(32 * warp) << 16) + buf * kRows;
+        const int key = t * kTile + 32 * warp + lane;
+        float* out = p.out + b * p.out_b + key;
+        float old = 0.f;  // on its way while the scores are made
+        if (key < len) {
+          if (g > 0)
+            old = *out;
+          else if (p.acc != nullptr && key < len - p.T)
+            old = p.acc[b * p.acc_b + key];
+        }
         dead = !__all_sync(0xffffffffu, wait(sm, sm.s_full[buf], (tile >> 1) & 1u, p.err));
         if (dead) break;
         tc_fence_after();
-        const int key = t * kTile + 32 * warp + lane;
         // some row of this tile is not seen by every token, or a query row gave no weight: select
         const bool select = dropped || (p.T > 1 && (t + 1) * kTile > len - p.T);
         const int first = max(0, key - (len - p.T)) * p.n_h - kRows * g;  // first query row that sees the key
-        float w[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int c = 0; c < cols; c += 32) {
-          uint32_t s[32];
-          tmem_ld32(src + c, s);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 l4 = ld_shared_v4(nl + 4 * (c + i));
-            const float l[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float x = ex2f_approx(fmaf(__uint_as_float(s[i + e]), p.scale_log2, l[e]));
-              w[e] += select && (c + i + e < first || l[e] == -INFINITY) ? 0.f : x;
-            }
-          }
-        }
+        const float sum = select ? key_sum<true>(src, nl, cols, p.scale_log2, first)
+                                 : key_sum<false>(src, nl, cols, p.scale_log2, first);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.s_empty[buf]));
-        if (key < len) {
-          float* out = p.out + b * p.out_b + key;
-          float sum = (w[0] + w[1]) + (w[2] + w[3]);
-          if (g > 0)
-            sum += *out;
-          else if (p.acc != nullptr && key < len - p.T)
-            sum = fmaf(p.decay, p.acc[b * p.acc_b + key], sum);
-          *out = sum;
-        }
+        if (key < len) *out = fmaf(g > 0 ? 1.f : p.decay, old, sum);
       }
       return true;
     });
