@@ -151,6 +151,16 @@ def _flag(dev_err: Optional[torch.Tensor]):
         raise TypeError("dev_err must be an int32 tensor")
 
 
+def _empty(like: torch.Tensor, shape: tuple) -> torch.Tensor:
+    """A contiguous tensor of like's type and device (torch.empty_strided takes half of torch.empty's time)."""
+    strides, n = [], 1
+    for w in reversed(shape):
+        strides.append(n)
+        n *= w
+    strides.reverse()
+    return torch.empty_strided(shape, strides, dtype=like.dtype, device=like.device)
+
+
 def _at(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -584,7 +594,7 @@ def mla_cache_read_fp4(dims, c4: torch.Tensor, kv_scale: torch.Tensor, n: int, f
     on, st = _launch_on(stream, dev)
     with on:
         if out is None:
-            out = torch.empty(shape, dtype=dtype, device=dev)
+            out = torch.empty_strided(shape, (n * d.d_c, d.d_c, 1), dtype=dtype, device=c4.device)
             strides = (n * d.d_c, d.d_c, 1)
         check(_fn("mla_cache_read_fp4")(
             d, code, B, n, _at(first), _at(counts), n_max, c4.data_ptr(), c4b, c4r, kv_scale.data_ptr(), scb, scr,
@@ -629,10 +639,10 @@ def mla_decode_absorb_fp4kv(dims, q_tilde: torch.Tensor, q_pe: torch.Tensor, c4:
     on, st = _launch_on(stream, dev)
     with on:
         if ctx is None:
-            ctx = torch.empty(q_tilde.shape, dtype=dtype, device=dev)
+            ctx = _empty(q_tilde, q_tilde.shape)
         if workspace is None:
             nbytes = max(_fp4kv_workspace(dev, d.n_h, d.d_c, d.d_r, dtype, B, T, n_max), 16)
-            workspace = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
+            workspace = c4.new_empty(nbytes)
         else:
             nbytes = workspace.numel() * workspace.element_size()
         check(_fn("mla_decode_absorb_fp4kv")(
@@ -751,9 +761,9 @@ def mla_cache_evict(planes: Sequence[torch.Tensor], acc: torch.Tensor, lengths: 
     on, st = _launch_on(stream, dev)
     with on:
         if new_lengths is None:
-            new_lengths = torch.empty((B,), dtype=torch.int32, device=dev)
+            new_lengths = lengths.new_empty(B)
         if row_map is None:
-            row_map = torch.empty((B, max(keep, 0)), dtype=torch.int32, device=dev)
+            row_map = _empty(lengths, (B, max(keep, 0)))
         check(_fn("mla_cache_evict")(B, n_max, rows, n_planes, acc.data_ptr(), acc_b, lengths.data_ptr(), keep, sink,
                                      recent, new_lengths.data_ptr(), row_map.data_ptr(), _at(dev_err), st),
               "mla_cache_evict")
