@@ -77,7 +77,11 @@ constexpr uint32_t kTmemCols = 512, kColO = 0, kColS = 256, kColQ = 384;  // sco
 // least 2^kRaise, and a probability that fp16's subnormals round (2^-25) is off by 2^-32 of the sum.
 constexpr float kRaise = 7.f, kRescale = 15.f;
 constexpr int kPlanRegs = 3;                     // items per lane that the chunk search holds (more than the pairs)
-constexpr int kSwitchTiles = 3;                  // what a second piece costs a CTA, in tiles
+constexpr int kJoin = 4;                         // partials that a warp of the join reads at once
+// What a second piece costs a pair, in tiles: the end of the pipeline, the result and the next query, some 13 us against
+// 2 us a tile.  (Measured with 3, 9 and 12: 60 sequences of 4096 rows 87, 82 and 81 us, 40 of 2048 49, 46 and 47,
+// 44 of 4096 72, 73 and 82.)
+constexpr int kSwitchTiles = 9;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -909,12 +913,12 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
   if (row >= p.B * p.R) return;  // (at most 65535 query groups of 128 rows)
   const int b = row / p.R, r = row - b * p.R, g = r / kRows, i = r % kRows;
   uint4* dst = reinterpret_cast<uint4*>(p.ctx + (int64_t)row * kDC + 256 * hf);
+  int4 e = p.table[b * p.groups + g];  // (on its way beside the length; a sequence without keys has left none)
   if (item_keys(p, b, g) == 0) {
     dst[lane] = make_uint4(0u, 0u, 0u, 0u);
     if (hf == 0 && lane == 0 && p.lse != nullptr) p.lse[row] = -INFINITY;
     return;
   }
-  int4 e = p.table[b * p.groups + g];
   if (e.z == 1) return;
   // a decode that gave up may have left no entry
   if ((unsigned)e.x >= 2u * p.pairs || e.y < 0 || e.z < 0 || e.z > p.pairs || e.y > p.pairs - e.z) e.z = 0;
@@ -926,17 +930,33 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
   const float ref = M == -INFINITY ? 0.f : M;
   float L = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   // lane l holds features 8 l .. 8 l + 7 of the half: two chunks of a rotated row
-#pragma unroll 4
-  for (int k = 0; k < e.z; ++k) {
-    const float2 ml = p.ws_ml[slot(k) * kRows + i];
-    const float4* src = reinterpret_cast<const float4*>(p.ws_o + ((4 * slot(k) + 2 * hf + (lane >> 4)) * stride + i) * 128);
-    const float4 a = src[(2 * lane + i) & 31], c = src[(2 * lane + 1 + i) & 31];
-    if (ml.y == 0.f) continue;  // the row saw none of this piece's keys
-    const float f = exp2f(ml.x - ref);
-    L = fmaf(f, ml.y, L);
-    const float v[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+  // The loads of kJoin pieces at once: with a branch on what was loaded between them they came one after the other,
+  // and a sequence of 32 pieces took 31 us instead of 24.  (Eight at once: 23, but 54 instead of 51 for 32 sequences
+  // of two or three pieces each, whose many warps no longer fit the SMs.)
+#pragma unroll 1
+  for (int k0 = 0; k0 < e.z; k0 += kJoin) {
+    float2 ml[kJoin];
+    float4 v[kJoin][2];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = fmaf(f, v[j], o[j]);
+    for (int u = 0; u < kJoin; ++u) {
+      ml[u] = make_float2(0.f, 0.f);
+      if (k0 + u < e.z) {
+        const int64_t s = slot(k0 + u);
+        ml[u] = p.ws_ml[s * kRows + i];
+        const float4* src = reinterpret_cast<const float4*>(p.ws_o + ((4 * s + 2 * hf + (lane >> 4)) * stride + i) * 128);
+        v[u][0] = src[(2 * lane + i) & 31];
+        v[u][1] = src[(2 * lane + 1 + i) & 31];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kJoin; ++u) {
+      if (ml[u].y == 0.f) continue;  // the row saw none of the piece's keys
+      const float f = exp2f(ml[u].x - ref);
+      L = fmaf(f, ml[u].y, L);
+      const float x[8] = {v[u][0].x, v[u][0].y, v[u][0].z, v[u][0].w, v[u][1].x, v[u][1].y, v[u][1].z, v[u][1].w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = fmaf(f, x[j], o[j]);
+    }
   }
   const float inv = (L == 0.f ? 0.f : 1.f / L) * p.kv.latent_scale;
   dst[lane] = make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv),
