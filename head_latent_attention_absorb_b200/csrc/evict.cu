@@ -334,24 +334,26 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
   select_rows<kCluster>(a, keys_in_smem);
 }
 
-// The rows that move: a CTA compacts 256 entries of row_map to those that do; a warp copies two rows at a time,
+// The rows that move: a CTA compacts kMoveEntries entries of row_map to those that do; a warp copies two rows at a time,
 // all planes' 16-byte (or smaller) elements numbered through, so that eight loads are under way per lane.
-constexpr int kMoveThreads = 256;
+// (Entries of a CTA 256, 128, 64, 32: 29, 25, 23, 24 us for 4 sequences cut from 32768 rows to 16384, 12.5, 12.4, 13.3,
+// 15.3 for 32 of 4096 rows that lose a few.)
+constexpr int kMoveThreads = 256, kMoveEntries = 128;
 template <typename V>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a) {
-  __shared__ int dst[kMoveThreads], src[kMoveThreads], warp_n[kMoveThreads / 32];
+  __shared__ int dst[kMoveEntries], src[kMoveEntries], warp_n[kMoveEntries / 32];
   sm100::griddep_launch_dependents();
   sm100::griddep_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.y;
-  const int i = blockIdx.x * kMoveThreads + tid;
-  const int from = i < a.keep ? a.row_map[(int64_t)b * a.keep + i] : -1;
+  const int i = blockIdx.x * kMoveEntries + tid;
+  const int from = tid < kMoveEntries && i < a.keep ? a.row_map[(int64_t)b * a.keep + i] : -1;
   const bool moves = from >= 0 && from != i && from < a.n_max;
   const uint32_t ballot = __ballot_sync(0xffffffffu, moves);
-  if (lane == 0) warp_n[warp] = __popc(ballot);
+  if (lane == 0 && warp < kMoveEntries / 32) warp_n[warp] = __popc(ballot);
   __syncthreads();
   int at = __popc(ballot & ((1u << lane) - 1u)), n = 0;
 #pragma unroll
-  for (int w = 0; w < kMoveThreads / 32; ++w) {
+  for (int w = 0; w < kMoveEntries / 32; ++w) {
     at += w < warp ? warp_n[w] : 0;
     n += warp_n[w];
   }
@@ -431,7 +433,7 @@ cudaError_t evict_launch(const EvictArgs& a, cudaStream_t st) {
   for (int p = 0; p < a.n_planes; ++p)
     bits |= reinterpret_cast<uintptr_t>(a.planes[p].base) | (uintptr_t)a.planes[p].bstride |
             (uintptr_t)a.planes[p].rstride | (uintptr_t)a.planes[p].row_bytes;
-  const dim3 grid((a.keep + kMoveThreads - 1) / kMoveThreads, a.B);
+  const dim3 grid((a.keep + kMoveEntries - 1) / kMoveEntries, a.B);
   if (bits % 16 == 0) return launch_pdl(evict_move_kernel<uint4>, grid, dim3(kMoveThreads), 0, st, a);
   if (bits % 4 == 0) return launch_pdl(evict_move_kernel<uint32_t>, grid, dim3(kMoveThreads), 0, st, a);
   return launch_pdl(evict_move_kernel<uint8_t>, grid, dim3(kMoveThreads), 0, st, a);

@@ -19,7 +19,10 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kAhead = 4;      // rows that a warp of the decode works on at once
-constexpr int kRowsSplit = 16;  // rows of a split while there are few of them
+// Rows of a split while there are few of them.  (4, 16 and 64: 9, 11 and 27 us for one sequence of 64 rows and 4 heads,
+// 18, 14 and 25 for 3 of 200 rows.)
+constexpr int kRowsSplit = 16;
+constexpr int kMaxSplits = 64;
 
 // The lane's blocks of latent row t of sequence b (kFp4: decoded; otherwise in the element type).
 template <typename T, int NB, bool kFp4>
@@ -94,6 +97,8 @@ template <typename T, int NB>
 __global__ void __launch_bounds__(32 * kWarps) decode_fp4_simt(Fp4DecodeArgs a, int n_splits, float* __restrict__ ws_o,
                                                                float2* __restrict__ ws_ml) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  sm100::griddep_launch_dependents();
+  sm100::griddep_wait();
   const int h = blockIdx.x * kWarps + warp;
   const int q = blockIdx.y, split = blockIdx.z;
   if (h >= a.n_h) return;
@@ -169,22 +174,42 @@ __global__ void __launch_bounds__(32 * kWarps) decode_fp4_simt(Fp4DecodeArgs a, 
     a.lse[row] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
+// One CTA per query row: the splits' factors once, then features with eight splits' loads under way.
 template <typename T>
 __global__ void __launch_bounds__(128) combine_fp4_simt(Fp4DecodeArgs a, int n_splits, const float* __restrict__ ws_o,
                                                         const float2* __restrict__ ws_ml) {
+  __shared__ float factor[kMaxSplits];
+  sm100::griddep_launch_dependents();
+  sm100::griddep_wait();
   const int64_t r = (int64_t)blockIdx.y * a.n_h + blockIdx.x, rows = (int64_t)a.B * a.T * a.n_h;
-  float M = -INFINITY, L = 0.f;
-  for (int s = 0; s < n_splits; ++s) M = fmaxf(M, ws_ml[s * rows + r].x);
-  for (int s = 0; s < n_splits; ++s) {
-    const float2 ml = ws_ml[s * rows + r];
-    if (ml.y != 0.f) L += ml.y * expf(ml.x - M);
+  const int lane = threadIdx.x & 31;
+  // every warp for itself: lane l has splits l and l + 32
+  float2 ml[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    ml[k] = lane + 32 * k < n_splits ? ws_ml[(lane + 32 * k) * rows + r] : make_float2(-INFINITY, 0.f);
+  const float M = warp_max(fmaxf(ml[0].x, ml[1].x));
+  float L = 0.f;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float f = ml[k].y != 0.f ? expf(ml[k].x - M) : 0.f;  // (0: the row saw none of the split's keys)
+    L = fmaf(f, ml[k].y, L);
+    if (threadIdx.x < 32) factor[lane + 32 * k] = f;
   }
+  L = warp_sum(L);
+  __syncthreads();
   const float inv = L == 0.f ? 0.f : 1.f / L;
   for (int c = threadIdx.x; c < a.d_c; c += blockDim.x) {
     float acc = 0.f;
-    for (int s = 0; s < n_splits; ++s) {
-      const float2 ml = ws_ml[s * rows + r];
-      if (ml.y != 0.f) acc = fmaf(expf(ml.x - M), ws_o[(s * rows + r) * a.d_c + c], acc);
+#pragma unroll 1
+    for (int s0 = 0; s0 < n_splits; s0 += 8) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (s0 + i < n_splits) v[i] = ws_o[((s0 + i) * rows + r) * a.d_c + c];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (s0 + i < n_splits && factor[s0 + i] != 0.f) acc = fmaf(factor[s0 + i], v[i], acc);
     }
     static_cast<T*>(a.ctx)[r * a.d_c + c] = from_f32<T>(acc * inv);
   }
@@ -228,7 +253,7 @@ int decode_fp4_simt_splits(int B, int n_max) {
   // for more of them, then enough (head group, query, split) blocks to cover it a few times over
   const int by_rows = (n_max + kRowsSplit - 1) / kRowsSplit, want = (4 * 148 + B - 1) / B;
   const int s = by_rows < want ? by_rows : want;
-  return s < 1 ? 1 : s > 64 ? 64 : s;
+  return s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s;
 }
 
 size_t decode_fp4_simt_workspace(int n_h, int d_c, int B, int n_max) {
@@ -241,14 +266,11 @@ cudaError_t decode_fp4_simt_launch(const Fp4DecodeArgs& a, void* ws, cudaStream_
   float* ws_o = static_cast<float*>(ws);
   float2* ws_ml = reinterpret_cast<float2*>(ws_o + (size_t)splits * q * a.n_h * a.d_c);
   const dim3 grid((a.n_h + kWarps - 1) / kWarps, q, splits);
-  if (a.d_c <= 512)
-    decode_fp4_simt<float, 1><<<grid, 32 * kWarps, 0, st>>>(a, splits, ws_o, ws_ml);
-  else
-    decode_fp4_simt<float, 2><<<grid, 32 * kWarps, 0, st>>>(a, splits, ws_o, ws_ml);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_pdl(a.d_c <= 512 ? decode_fp4_simt<float, 1> : decode_fp4_simt<float, 2>, grid,
+                                   dim3(32 * kWarps), 0, st, a, splits, ws_o, ws_ml);
   if (e != cudaSuccess || splits == 1) return e;
-  combine_fp4_simt<float><<<dim3(a.n_h, q), 128, 0, st>>>(a, splits, ws_o, ws_ml);
-  return cudaGetLastError();
+  return launch_pdl(combine_fp4_simt<float>, dim3(a.n_h, q), dim3(128), 0, st, a, splits, (const float*)ws_o,
+                    (const float2*)ws_ml);
 }
 
 cudaError_t weights_simt_launch(const WeightsArgs& a, cudaStream_t st) {
