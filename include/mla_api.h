@@ -387,7 +387,7 @@ mla_status mla_cache_append_at(mla_dims dims, mla_dtype dtype, int32_t B,
  *   counts     DEVICE int32 [B]: tokens of each sequence in [0, T], or NULL: T everywhere
  *   Device flag: counts[b] outside [0, T] sets MLA_ERR_LENGTH (the sequence writes nothing); a row outside
  *   [0, n_max) or a negative position sets MLA_ERR_INDEX (that token is not written).  Every other
- *   cache row is left as it was.  Asynchronous on `stream`.
+ *   cache row is left as it was.  B * T < 2^31.  Asynchronous on `stream`.
  */
 mla_status mla_cache_append_fp4(mla_dims dims, mla_dtype dtype, int32_t B, int32_t T,
                                 const void* kv_a, int64_t lda_b, int64_t lda, const float* gain, float eps,
@@ -427,7 +427,8 @@ size_t mla_decode_fp4kv_workspace_size(mla_dims dims, mla_dtype dtype, int32_t B
  *            get ctx = 0, lse = -inf.  Rows at and behind lengths[b] may hold anything.
  *   workspace  at least mla_decode_fp4kv_workspace_size() bytes, 16-byte aligned, no initialisation;
  *            calls that may overlap need one each
- *   B * T <= 65535.  Asynchronous on `stream`.
+ *   B * T <= 65535, and ceil(n_h T / 128) B ceil(n_max / 128) < 2^31.  Sequences may share one cache (batch
+ *   strides 0).  A bounded wait that runs out sets MLA_ERR_TIMEOUT.  Asynchronous on `stream`.
  */
 mla_status mla_decode_absorb_fp4kv(mla_dims dims, mla_dtype dtype, int32_t B, int32_t T,
                                    const void* q_tilde, int64_t ldqt, const void* q_pe, int64_t ldqp,
@@ -451,7 +452,8 @@ mla_status mla_decode_absorb_fp4kv(mla_dims dims, mla_dtype dtype, int32_t B, in
  *   decay    >= 0 and finite; 1 sums over all steps
  *   lengths  DEVICE int32 [B] in [T, n_max]; another length sets MLA_ERR_LENGTH and writes nothing
  *   Sums over heads and tokens are in fp32, in a fixed order.  Types and widths: MLA_BF16 with
- *   d_c = 512, d_r = 64, 1 <= n_h <= 128; MLA_F32 with n_h, d_c <= 1024, d_r <= 128.  B <= 65535.
+ *   d_c = 512, d_r = 64, 1 <= n_h <= 128; MLA_F32 with n_h, d_c <= 1024, d_r <= 128.  B * T <= 65535.
+ *   A bounded wait that runs out sets MLA_ERR_TIMEOUT.
  * mla_cache_weights_fp4kv reads the 4-bit cache instead.  Asynchronous on `stream`.
  */
 mla_status mla_cache_weights(mla_dims dims, mla_dtype dtype, int32_t B, int32_t T,

@@ -109,6 +109,31 @@ def test_evict_refuses(L, kw, want):
     assert _evict(L, **kw) == want, L.mla_last_error_message()
 
 
+def _read(L, **kw):
+    a = dict(dims=DS, dt=BF, B=2, n=16, n_max=16, c4=P, c4b=16 * 256, c4r=256, sc=P, scb=16 * 32, scr=32, ls=1.0, out=P,
+             outb=16 * 512, outr=512)
+    a.update(kw)
+    return L.mla_cache_read_fp4(a["dims"], a["dt"], a["B"], a["n"], 0, 0, a["n_max"], a["c4"], a["c4b"], a["c4r"], a["sc"],
+                                a["scb"], a["scr"], a["ls"], a["out"], a["outb"], a["outr"], 0, 0)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(B=0), INVALID), (dict(n=0), INVALID), (dict(n_max=0), INVALID), (dict(out=0), INVALID), (dict(c4=0), INVALID),
+    (dict(out=P + 8), INVALID), (dict(outr=504), INVALID), (dict(outr=516), INVALID), (dict(outb=15 * 512), INVALID),
+    (dict(c4r=264), INVALID), (dict(scr=16), INVALID), (dict(ls=3.0), INVALID), (dict(dims=TINY), UNSUPPORTED)])
+def test_read_refuses(L, kw, want):
+    assert _read(L, **kw) == want, L.mla_last_error_message()
+
+
+def test_sizes_that_pass_32_bits_are_refused(L):
+    assert _append(L, B=1 << 16, T=1 << 15, c4b=1 << 40, scb=1 << 40, krb=1 << 40) == UNSUPPORTED
+    assert _decode(L, B=65535, n_max=1 << 30, c4b=0, scb=0, krb=0) == UNSUPPORTED
+    assert _decode(L, B=32768, T=2, n_max=16) == UNSUPPORTED
+    assert _weights(L, B=65536, accb=16, outb=16) == UNSUPPORTED
+    assert _evict(L, B=65536) == UNSUPPORTED
+    assert _evict(L, n_max=400001, accb=400001, planes=((P, 1 << 40, 64, 64),)) == UNSUPPORTED
+
+
 def test_append_at_refuses_like_append(L):
     assert L.mla_cache_append_at(DS, BF, 2, P, 575, 0, 1e-6, 1e4, P, P, 16, P, 16 * 512, 512, P, 16 * 64, 64, 0, 0) == INVALID
 
