@@ -10,6 +10,11 @@
 // Two launches: the selection writes row_map (a cluster of eight CTAs per sequence, each with a slice of the
 // rows, or one CTA for a short sequence; counts, ranks and the list of moved rows cross through distributed
 // shared memory), the move reads it.
+//
+// Bound: the selection by latency, a chain of passes over keys in shared memory, scans and meetings (17 us for 4
+// sequences of up to 32768 rows, 12 for 32 of 4096, alone with cold caches); the move by its bytes, with
+// few warps when few rows move.  Both together, back to back: 4 sequences of 20000 to 32768 rows of 1152 bytes cut to
+// 16384 25 us (63 MB: 2.5 TB/s), 32 sequences of 4-bit rows that lose up to 256 of 4096 12.4 us.
 #include <math.h>
 
 #include "common.cuh"

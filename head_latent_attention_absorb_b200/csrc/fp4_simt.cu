@@ -7,6 +7,10 @@
 // One warp per (head, query, split) in the decode and per cached row in the weights; lane l owns the
 // 16-feature blocks l and l + 32 of a latent row, so a 4-bit row costs a lane one 8-byte load and
 // one scale per block.  They carry the fp32 element type for any dimensions.
+//
+// Bound: latency, at the few rows and heads that fp32 is used with: a row is a chain of loads, a sum across the warp
+// and an exponential, so a warp of the decode takes four rows at once and the splits are short.  3 sequences of 64 to
+// 193 rows and 4 heads: 11.7 us (168 with one row at a time in longer splits).
 #include <math.h>
 
 #include "common.cuh"

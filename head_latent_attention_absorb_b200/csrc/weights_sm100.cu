@@ -6,9 +6,13 @@
 // accumulator and up to 128 query rows its columns, so the sum over query rows is a sum within a thread and
 // nothing is exchanged.  Since lse is known there is no running maximum and no second pass.
 //
-// Bound: a bf16 cache by its bytes (1152 a row against 1152 n_h T / 8192 cycles of the tensor pipe at 128
-// heads), a 4-bit cache (416 bytes a row) by shared memory: a tile's MMAs read A and B there, 8 KB per 64
-// cycles, and the decoded tile is written there as well.
+// Bound: a bf16 cache by its bytes (1152 a row): B = 32, N = 4096, 128 heads 29.5 us, 151 MB at 5.1 TB/s (N = 16384:
+// 91 us, 6.6 TB/s); a tile takes 5500 cycles of the bytes' and 3850 of the MMAs' time.  A 4-bit cache (416 bytes a
+// row) by the decode beside the MMAs, some 6500 cycles a tile in which neither the tensor pipe nor the ALUs nor
+// shared memory is half busy: the slabs' proxy fences wait for the loads under way.  B = 8, up to 16384 rows 21 us,
+// B = 32, N = 16384 111 us.  8 us go before the first tile (launch, share of the work, the query rows) and 2 after
+// the last.  (A CTA pair that splits the query rows, with a ring of nine slabs, took 35 and 25 us instead of 29.5 and
+// 21: its start and end cost 4 us more.  Sixteen decode warps instead of eight: the same.)
 //
 // * One CTA per SM takes an equal share of the batch's 128-key tiles.  The query rows of its sequence (144 KB
 //   in nine 64-feature slabs) stay in shared memory; the keys pass through a ring of five 16 KB slabs.
@@ -39,7 +43,9 @@ constexpr int kRows = 128;                   // query rows per group: its column
 constexpr int kSlabs = (kDC + kDR) / 64;     // 64-feature slabs of a row
 constexpr int kSlabBytes = kTile * 128;      // 128 rows of 64 bf16 features
 constexpr int kStages = 5;
-constexpr int kGroupPiece = 4;               // tiles per piece when several groups pass over them
+// Tiles per piece when several groups of query rows pass over them.  (1, 4, 16: 52, 43 and 43 us for 4 sequences of 8192
+// bf16 rows with 8 tokens of 128 heads; a short piece keeps its keys in L2 between the groups.)
+constexpr int kGroupPiece = 4;
 constexpr int kQWarp = 6, kKeyWarp = 5, kMmaWarp = 4, kDecodeWarp0 = 7, kDecodeWarps = 8;
 constexpr int kThreadsBf16 = 32 * kDecodeWarp0, kThreadsFp4 = 32 * (kDecodeWarp0 + kDecodeWarps);
 constexpr uint32_t kTmemCols = 256;          // two accumulators of 128 columns
@@ -312,6 +318,8 @@ __global__ void __launch_bounds__(kFp4 ? kThreadsFp4 : kThreadsBf16, 1) weights_
     });
   } else if (kFp4 && warp >= kDecodeWarp0) {
     // ---------------------------------------------------------------- 4-bit keys to bf16 slabs
+    // (Every producer takes every use of every stage in order: a wait by parity that skipped uses of a stage could
+    // take an older phase for the one it needs.)
     // Each load of the next tile follows the last use of its registers, so a tile's time passes before it is
     // needed.
     const int row0 = 16 * (warp - kDecodeWarp0), row = code_row(lane), slab = (lane >> 1) & 1, half = lane & 1;
