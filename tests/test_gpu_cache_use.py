@@ -237,3 +237,40 @@ def test_evict_of_sequences_that_fit():
         new, row_map = api.mla_cache_evict([plane], acc, i32(lens), 50, sink=0, recent=0)
         assert new.tolist() == lens and torch.equal(plane, before)
         assert row_map[0].tolist() == [i if i < lens[0] else -1 for i in range(50)]
+
+
+@pytest.mark.parametrize("dtype,d_c,d_r", [(BF, 512, 64), (F32, 40, 6)])
+def test_append_at_writes_the_row_that_append_writes(dtype, d_c, d_r):
+    d, B, far, near = dims(4, d_c, d_r), 4, 4001, 8
+    x = torch.randn((B, d_c + d_r), device=DEV).to(dtype)
+    gain = torch.rand((d_c,), device=DEV) + 0.5
+    pos, rows = [4000, 3, 0, 1234], [5, 0, 7, 2]
+    a = torch.full((B, far, d_c + d_r), 3.0, dtype=dtype, device=DEV)
+    b = torch.full((B, near, d_c + d_r), 3.0, dtype=dtype, device=DEV)
+    api.mla_cache_append(d, x, i32(pos), a[..., :d_c], a[..., d_c:], gain=gain)
+    api.mla_cache_append(d, x, i32(pos), b[..., :d_c], b[..., d_c:], gain=gain, rows=i32(rows))
+    want = torch.full_like(b, 3.0)
+    for s in range(B):
+        want[s, rows[s]] = a[s, pos[s]]
+    assert torch.equal(b, want)
+    # a row behind the cache, before it, and a negative position: reported, nothing written
+    for p, r in (([1] * B, [0, 8, 1, 2]), ([1] * B, [0, -1, 1, 2]), ([1, -1, 1, 1], [0, 1, 1, 2])):
+        b.fill_(3.0)
+        err = i32([0])
+        api.mla_cache_append(d, x, i32(p), b[..., :d_c], b[..., d_c:], gain=gain, rows=i32(r), dev_err=err)
+        assert int(err) == 4 and bool((b[1] == 3.0).all()) and bool((b[0, 0] != 3.0).any())
+
+
+def test_caches_that_end_with_their_rows():
+    """The last sequence fills its cache to the end of the allocation, at lengths inside and at the end of a tile."""
+    for n in (1, 63, 64, 65, 127, 128, 129, 255, 256, 300):
+        c4, sc, kr = random_fp4(2, n, 512, n)
+        planes = (c4.to(DEV), sc.to(DEV), kr.to(DEV))
+        q, qp = queries(2, 1, 128, n)
+        lens = [n, n]
+        ctx, lse = decode(q[:, 0].to(DEV), qp[:, 0].to(DEV), planes, i32(lens))
+        check_decode(ctx, lse, reference(q, qp, values(c4, sc), kr, lens, 1, float(np.float32(SCALE))), BF)
+        w = weights(q[:, 0].to(DEV), qp[:, 0].to(DEV), planes, i32(lens), lse)
+        rows = api.mla_cache_read_fp4(dims(), *planes[:2], n)
+        v = api.mla_cache_weights(dims(), q[:, 0].to(DEV), qp[:, 0].to(DEV), rows, planes[2], i32(lens), SCALE, lse)
+        assert torch.equal(w, v)  # the same bf16 operands, in the same order
