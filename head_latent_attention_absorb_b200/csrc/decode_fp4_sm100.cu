@@ -929,11 +929,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
   if ((unsigned)e.x >= 2u * p.pairs || e.y < 0 || e.z < 0 || e.z > p.pairs || e.y > p.pairs - e.z) e.z = 0;
   const int stride = min(p.R, kRows);
   auto slot = [&](int k) { return (int64_t)(k == 0 ? e.x : 2 * (e.y + k)); };
-  float M = -INFINITY;
-  for (int k = lane; k < e.z; k += 32) M = fmaxf(M, p.ws_ml[slot(k) * kRows + i].x);
-  M = warp_max(M);
-  const float ref = M == -INFINITY ? 0.f : M;
-  float L = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  float M = -INFINITY, L = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   // lane l holds features 8 l .. 8 l + 7 of the half: two chunks of a rotated row
   // The loads of kJoin pieces at once: with a branch on what was loaded between them they came one after the other,
   // and a sequence of 32 pieces took 31 us instead of 24.  (Eight at once: 23, but 54 instead of 51 for 32 sequences
@@ -953,6 +949,18 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
         v[u][1] = src[(2 * lane + 1 + i) & 31];
       }
     }
+    float top = M;
+#pragma unroll
+    for (int u = 0; u < kJoin; ++u)
+      if (ml[u].y != 0.f) top = fmaxf(top, ml[u].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    if (k0 > 0) {
+      const float f = exp2f(M - ref);
+      L *= f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] *= f;
+    }
+    M = top;
 #pragma unroll
     for (int u = 0; u < kJoin; ++u) {
       if (ml[u].y == 0.f) continue;  // the row saw none of the piece's keys
