@@ -70,7 +70,7 @@ struct Params {
 };
 
 struct Smem {
-  uint64_t full[kStages], empty[kStages], q_full, q_empty, s_full[2], s_empty[2], drain;
+  uint64_t full[kStages], empty[kStages], q_full[kSlabs], q_empty, s_full[2], s_empty[2], drain;
   alignas(16) float neg_lse[kRows];  // -lse in log2 units, -inf for absent and dropped rows
   int dropped[4];        // some present row of the quarter has no softmax
   uint32_t tmem_base;
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kFp4 ? kThreadsFp4 : kThreadsBf16, 1) weights_
       mbar_init(smem_u32(&sm.full[s]), kFp4 ? kDecodeWarps : 1);
       mbar_init(smem_u32(&sm.empty[s]), 1);
     }
-    mbar_init(smem_u32(&sm.q_full), 1);
+    for (int j = 0; j < kSlabs; ++j) mbar_init(smem_u32(&sm.q_full[j]), 1);
     mbar_init(smem_u32(&sm.q_empty), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sm.s_full[i]), 1);
@@ -206,14 +206,19 @@ __global__ void __launch_bounds__(kFp4 ? kThreadsFp4 : kThreadsBf16, 1) weights_
       uint32_t pass = 0;
       for_each_pass(p, sm, [&](int b, int, int g, int, int) {
         if (!wait(sm, sm.q_empty, (pass & 1u) ^ 1u, p.err)) return false;
-        const uint32_t bar = smem_u32(&sm.q_full);
-        mbar_arrive_expect_tx(bar, kSlabs * kSlabBytes);
-        for (int j = 0; j < kSlabs - 1; ++j) tma_load_3d(q_addr + j * kSlabBytes, &p.tm_q, bar, 64 * j, kRows * g, b, pol);
-        tma_load_3d(q_addr + (kSlabs - 1) * kSlabBytes, &p.tm_qp, bar, 0, kRows * g, b, pol);
+        for (int j = 0; j < kSlabs; ++j) {
+          const uint32_t bar = smem_u32(&sm.q_full[j]), dst = q_addr + j * kSlabBytes;
+          mbar_arrive_expect_tx(bar, kSlabBytes);
+          if (j < kSlabs - 1)
+            tma_load_3d(dst, &p.tm_q, bar, 64 * j, kRows * g, b, pol);
+          else
+            tma_load_3d(dst, &p.tm_qp, bar, 0, kRows * g, b, pol);
+        }
         ++pass;
         return true;
       });
-      if (pass > 0) mbar_wait(smem_u32(&sm.q_full), (pass - 1) & 1u, &sm.never, kWaitLimitNs);
+      for (int j = 0; j < kSlabs && pass > 0; ++j)
+        mbar_wait(smem_u32(&sm.q_full[j]), (pass - 1) & 1u, &sm.never, kWaitLimitNs);
     }
     __syncwarp();
   } else if (!kFp4 && warp == kKeyWarp) {
@@ -246,13 +251,13 @@ __global__ void __launch_bounds__(kFp4 ? kThreadsFp4 : kThreadsBf16, 1) weights_
       for_each_pass(p, sm, [&](int, int, int g, int t0, int t1) {
         const int cols = (min(R - kRows * g, kRows) + 31) & ~31;  // zero rows pad to the readers' 32 columns
         const uint32_t idesc = idesc_bf16_f32(kTile, cols, 0, 0);
-        if (!wait(sm, sm.q_full, pass & 1u, p.err)) return false;
         for (int t = t0; t < t1; ++t, ++tile) {
           const uint32_t buf = tile & 1u;
           if (!wait(sm, sm.s_empty[buf], ((tile >> 1) & 1u) ^ 1u, p.err)) return false;
           tc_fence_after();
           for (int j = 0; j < kSlabs; ++j, ++n) {
             const uint32_t st = n % kStages;
+            if (t == t0 && !wait(sm, sm.q_full[j], pass & 1u, p.err)) return false;
             if (!wait(sm, sm.full[st], (n / kStages) & 1u, p.err)) return false;
             tc_fence_after();
             const uint32_t a = ring + st * kSlabBytes, q = q_addr + j * kSlabBytes;
