@@ -5,11 +5,11 @@
 //
 // Bound: the tensor pipe.  A cached row costs 2 R (2 d_c + d_r) operations against 416 bytes: at R = 128
 // 669 a byte, far right of the GPU's ridge.  Measured (one call, replayed in a graph): B = 32, N = 4096, 128 heads
-// 51 us, 712 TFLOP/s; B = 8, 1024 to 65536 rows 84 us; 32 query rows (16 heads, 2 tokens), B = 32, up to 8191 rows
-// 56 us, a quarter of each MMA's rows in use; B = 1, N = 1000 18.5 us.  A tile of 128 keys takes a pair 4000 cycles, 2190
+// 51 us, 716 TFLOP/s; B = 8, 1024 to 65536 rows 84 us; 32 query rows (16 heads, 2 tokens), B = 32, up to 8191 rows
+// 55 us, a quarter of each MMA's rows in use; B = 1, N = 1000 18.2 us.  A tile of 128 keys takes a pair 4000 cycles, 2190
 // of them in the MMAs: the loop from a released buffer over the decode of its next keys, the scores and the softmax
-// to the values crosses between the CTAs four times.  Some 18 us of a call lie outside its tiles: work split and
-// query (8), the end of the pipeline and the partials (6), the join (4).
+// to the values crosses between the CTAs four times.  Some 17 us of a call lie outside its tiles: work split and
+// query (8), the end of the pipeline and the partials (6), the join (3).
 //
 // Why this split.  The fp32 context of 128 rows x 512 features fills TMEM, so no SM can hold it beside
 // scores.  Every MMA therefore spans a CTA pair (cta_group::2, M = 128): each CTA holds 64 of the rows with their

@@ -6,12 +6,12 @@
 // accumulator and up to 128 query rows its columns, so the sum over query rows is a sum within a thread and
 // nothing is exchanged.  Since lse is known there is no running maximum and no second pass.
 //
-// Bound: a bf16 cache by its bytes (1152 a row): B = 32, N = 4096, 128 heads 29.5 us, 151 MB at 5.1 TB/s (N = 16384:
+// Bound: a bf16 cache by its bytes (1152 a row): B = 32, N = 4096, 128 heads 29.1 us, 151 MB at 5.2 TB/s (N = 16384:
 // 91 us, 6.6 TB/s); a tile takes 5500 cycles of the bytes' and 3850 of the MMAs' time.  A 4-bit cache (416 bytes a
 // row) by the decode beside the MMAs, some 6500 cycles a tile in which neither the tensor pipe nor the ALUs nor
 // shared memory is half busy: the slabs' proxy fences wait for the loads under way.  B = 8, up to 16384 rows 21 us,
-// B = 32, N = 16384 111 us.  8 us go before the first tile (launch, share of the work, the query rows) and 2 after
-// the last.  (A CTA pair that splits the query rows, with a ring of nine slabs, took 35 and 25 us instead of 29.5 and
+// B = 32, N = 16384 111 us.  7 us go before the first tile (launch, share of the work, the first slabs) and 2 after
+// the last.  (A CTA pair that splits the query rows, with a ring of nine slabs, took 35 and 25 us instead of 29 and
 // 21: its start and end cost 4 us more.  Sixteen decode warps instead of eight: the same.)
 //
 // * One CTA per SM takes an equal share of the batch's 128-key tiles.  The query rows of its sequence (144 KB
