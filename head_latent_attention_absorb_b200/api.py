@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import struct
 from typing import Optional, Sequence
 
 import torch
@@ -77,6 +78,8 @@ def _fast_dims(x: Sequence[int]) -> MLADims:
 
 
 _PLANES = _capi.MLARows * _capi.MAX_PLANES
+# fills an array of planes in one call: base, strides, row bytes and the struct's padding
+_PACK_PLANES = [struct.Struct("@" + "Pqqi4x" * n).pack_into for n in range(_capi.MAX_PLANES + 1)]
 _DIMS: dict = {}
 _FN: dict = {}
 
@@ -639,7 +642,7 @@ def mla_decode_absorb_fp4kv(dims, q_tilde: torch.Tensor, q_pe: torch.Tensor, c4:
     on, st = _launch_on(stream, dev)
     with on:
         if ctx is None:
-            ctx = _empty(q_tilde, q_tilde.shape)
+            ctx = torch.empty_like(q_tilde) if q_tilde.is_contiguous() else _empty(q_tilde, q_tilde.shape)
         if workspace is None:
             nbytes = max(_fp4kv_workspace(dev, d.n_h, d.d_c, d.d_r, dtype, B, T, n_max), 16)
             workspace = c4.new_empty(nbytes)
@@ -740,7 +743,7 @@ def mla_cache_evict(planes: Sequence[torch.Tensor], acc: torch.Tensor, lengths: 
     B, n_max = lead = tuple(acc.shape)
     acc_b = _weight_array(acc, lead, "acc")
     _i32(lengths, (B,), "lengths")
-    rows = _PLANES()
+    rows, fields = _PLANES(), []
     for i, p in enumerate(planes):
         shape = p.shape
         if len(shape) != 3 or shape[:2] != lead:
@@ -750,8 +753,8 @@ def mla_cache_evict(planes: Sequence[torch.Tensor], acc: torch.Tensor, lengths: 
             _rows(p, f"plane {i}")
         es = p.element_size()
         width = shape[2] * es
-        r = rows[i]
-        r.base, r.bstride, r.rstride, r.row_bytes = p.data_ptr(), bs * es, rs * es if n_max > 1 else width, width
+        fields += (p.data_ptr(), bs * es, rs * es if n_max > 1 else width, width)
+    _PACK_PLANES[n_planes](rows, 0, *fields)
     if new_lengths is not None:
         _i32(new_lengths, (B,), "new_lengths")
     if row_map is not None:
@@ -763,7 +766,8 @@ def mla_cache_evict(planes: Sequence[torch.Tensor], acc: torch.Tensor, lengths: 
         if new_lengths is None:
             new_lengths = lengths.new_empty(B)
         if row_map is None:
-            row_map = _empty(lengths, (B, max(keep, 0)))
+            wide = max(keep, 0)
+            row_map = torch.empty_strided((B, wide), (wide, 1), dtype=torch.int32, device=lengths.device)
         check(_fn("mla_cache_evict")(B, n_max, rows, n_planes, acc.data_ptr(), acc_b, lengths.data_ptr(), keep, sink,
                                      recent, new_lengths.data_ptr(), row_map.data_ptr(), _at(dev_err), st),
               "mla_cache_evict")
