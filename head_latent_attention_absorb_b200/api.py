@@ -753,7 +753,7 @@ def mla_cache_evict(planes: Sequence[torch.Tensor], acc: torch.Tensor, lengths: 
             _rows(p, f"plane {i}")
         es = p.element_size()
         width = shape[2] * es
-        fields += (p.data_ptr(), bs * es, rs * es if n_max > 1 else width, width)
+        fields += (p.data_ptr(), bs * es, rs * es if n_max > 1 else width, min(width, 0x7fffffff))  # (so wide a row is refused)
     _PACK_PLANES[n_planes](rows, 0, *fields)
     if new_lengths is not None:
         _i32(new_lengths, (B,), "new_lengths")

@@ -727,13 +727,16 @@ mla_status mla_cache_evict(int32_t B, int32_t n_max, const mla_rows* planes, int
     return fail(MLA_ERR_INVALID_ARG, "sink and recent must be >= 0 with a sum of at most keep");
   if (acc_bstride < n_max && B > 1) return fail(MLA_ERR_INVALID_ARG, "acc batch stride smaller than n_max");
   mla::EvictArgs a;
+  int64_t row_bytes = 0;
   for (int p = 0; p < n_planes; ++p) {
     const mla_rows& r = planes[p];
     if (!r.base) return fail(MLA_ERR_INVALID_ARG, "plane %d: NULL pointer", p);
     if (r.row_bytes <= 0 || r.rstride < r.row_bytes || (B > 1 && r.bstride < (n_max - 1) * r.rstride + r.row_bytes))
       return fail(MLA_ERR_INVALID_ARG, "plane %d: rows overlap (row_bytes, rstride or bstride too small)", p);
     a.planes[p] = r;
+    row_bytes += r.row_bytes;
   }
+  if (row_bytes > 1 << 30) return fail(MLA_ERR_UNSUPPORTED, "a row of all planes must not exceed 2^30 bytes");
   a.B = B; a.n_max = n_max; a.n_planes = n_planes; a.keep = keep; a.sink = sink; a.recent = recent;
   a.acc = acc; a.acc_b = acc_bstride; a.lengths = lengths; a.new_lengths = new_lengths; a.row_map = row_map;
   a.err = dev_err;

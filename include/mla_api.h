@@ -495,7 +495,7 @@ typedef struct {
  *   keep        1 <= keep <= n_max; sink, recent >= 0, sink + recent <= keep
  *   new_lengths DEVICE int32 [B]: min(lengths[b], keep); may be lengths itself
  *   row_map     DEVICE int32 [B, keep]: the row that row i held before, -1 for i >= new_lengths[b]
- *   n_max <= 400000, B <= 65535.  Planes must not overlap.  Asynchronous on `stream`.
+ *   n_max <= 400000, B <= 65535, at most 2^30 bytes a row of all planes.  Planes must not overlap.  Asynchronous on `stream`.
  */
 mla_status mla_cache_evict(int32_t B, int32_t n_max, const mla_rows* planes, int32_t n_planes,
                            const float* acc, int64_t acc_bstride, const int32_t* lengths,

@@ -132,6 +132,8 @@ def test_sizes_that_pass_32_bits_are_refused(L):
     assert _weights(L, B=65536, accb=16, outb=16) == UNSUPPORTED
     assert _evict(L, B=65536) == UNSUPPORTED
     assert _evict(L, n_max=400001, accb=400001, planes=((P, 1 << 40, 64, 64),)) == UNSUPPORTED
+    assert _evict(L, planes=((P, 1 << 40, 1 << 31, (1 << 31) - 1),)) == UNSUPPORTED
+    assert _evict(L, planes=((P, 1 << 40, 1 << 30, 1 << 30), (P, 1 << 40, 16, 16))) == UNSUPPORTED
 
 
 def test_append_at_refuses_like_append(L):
