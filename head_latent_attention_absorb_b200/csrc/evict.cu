@@ -27,7 +27,8 @@ namespace {
 constexpr int kThreads = 1024;  // of a CTA of the selection
 constexpr int kWarps = kThreads / 32;
 constexpr int kCluster = 8;     // CTAs that share a sequence
-constexpr int kOneCta = 8192, kOneCtaFull = 32768;  // rows that one CTA selects from by itself
+// Rows that one CTA selects from by itself: always; as far as its shared memory goes; for each sequence of the batch.
+constexpr int kOneCta = 8192, kOneCtaFull = 32768, kOneCtaPer = 1024;
 constexpr int kSelectSmem = 220 * 1024;
 constexpr int kMaxRows = 400000;  // a slice of them is counted in 16 bits
 constexpr int kWord = 32;       // rows of one word of the kept mask
@@ -419,11 +420,13 @@ size_t select_smem_bytes(int n_max, bool keys) {
 int evict_max_rows() { return kMaxRows; }
 
 cudaError_t evict_launch(const EvictArgs& a, cudaStream_t st) {
-  // One CTA for a sequence of up to kOneCta rows: the meetings of a cluster take longer than the passes of one CTA over
-  // the keys in its shared memory (8 sequences, one CTA / a cluster: 1024 rows 13 / 18 us, 4096 16 / 20, 8192 20 / 23,
-  // 16384 30 / 25).  As long as the keys fit, too, where clusters would not all run at once: two CTAs of this size share
-  // an SM (64 sequences: 4096 rows 19 / 66 us, 16384 51 / 93, 32768 110 / 150).
-  const bool one = a.n_max <= kOneCta || (a.n_max <= kOneCtaFull && a.B > 2 * sm_count() / kCluster);
+  // One CTA for a short sequence, a cluster for a long one: the meetings of a cluster take longer than one CTA's passes
+  // over some thousand keys in its shared memory, and a cluster's CTAs share the SMs with those of the other sequences.
+  // The border moves up with their number.  One CTA / a cluster, us a call:
+  //    8 sequences of 1024 rows 13 / 18, 4096 16 / 20, 8192 20 / 23, 16384 30 / 25
+  //   16 of 8192 19 / 30, 16384 32 / 36, 24000 43 / 39;   26 of 16384 36 / 43, 24000 50 / 50, 32768 65 / 59
+  //   37 of 24000 57 / 70, 32768 76 / 84;   64 of 4096 19 / 66, 16384 51 / 93, 32768 110 / 150
+  const bool one = a.n_max <= kOneCta || (a.n_max <= kOneCtaFull && a.n_max / kOneCtaPer <= a.B);
   const auto bytes = one ? select_smem_bytes<1> : select_smem_bytes<kCluster>;
   const bool keys = bytes(a.n_max, true) <= kSelectSmem;
   const size_t smem = bytes(a.n_max, keys);

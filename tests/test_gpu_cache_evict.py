@@ -208,7 +208,7 @@ def test_evict_long_sequences():
     assert run_evict([100000, 60001, 5], 100000, 40000, 4, 1024, widths=((8, torch.uint8),), seed=3) == 0
 
 
-@pytest.mark.parametrize("B,n_max", [(2, 8192), (2, 8193), (40, 8193), (40, 32768), (40, 32769), (2, 32769)])
+@pytest.mark.parametrize("B,n_max", [(2, 8192), (2, 8193), (40, 8193), (40, 32768), (40, 32769), (2, 32769), (12, 12288), (12, 13312)])
 def test_evict_one_cta_and_cluster(B, n_max):
     lengths = [n_max - 37 * b for b in range(B)]
     assert run_evict(lengths, n_max, n_max // 2 + 1, 5, 333, widths=((4, torch.uint8),), seed=B + n_max) == 0
