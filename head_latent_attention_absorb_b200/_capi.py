@@ -87,6 +87,8 @@ SIGNATURES = {
                                         c_i32, c_vp, c_f32, c_vp, c_vp, c_i64, c_f32, c_vp, c_i64, c_vp, c_vp]),
     "mla_cache_evict": (c_i32, [c_i32, c_i32, ctypes.POINTER(MLARows), c_i32, c_vp, c_i64, c_vp, c_i32, c_i32,
                                 c_i32, c_vp, c_vp, c_vp, c_vp]),
+    "mla_cache_evict_at": (c_i32, [c_i32, c_i32, ctypes.POINTER(MLARows), c_i32, c_vp, c_i64, c_vp, c_i32, c_i32,
+                                   c_i32, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp]),
     "mla_check_topk": (c_i32, [c_i32, c_vp, c_i32, c_vp, c_i32, c_vp, c_vp]),
     "mla_prefill_sparse_workspace_size": (c_sz, [MLADims, c_i32, c_i32, c_i32]),
     "mla_prefill_sparse": (c_i32, [MLADims, c_i32, c_i32, c_i32, c_vp, c_vp, c_i64, c_vp, c_i64, c_vp,

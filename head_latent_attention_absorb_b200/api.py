@@ -728,13 +728,17 @@ def mla_cache_weights_fp4kv(dims, q_tilde: torch.Tensor, q_pe: torch.Tensor, c4:
 
 def mla_cache_evict(planes: Sequence[torch.Tensor], acc: torch.Tensor, lengths: torch.Tensor, keep: int,
                     sink: int = 0, recent: int = 0, new_lengths: Optional[torch.Tensor] = None,
-                    row_map: Optional[torch.Tensor] = None, dev_err: Optional[torch.Tensor] = None, stream=None):
-    """Keep `keep` rows of every sequence that holds more: the first `sink`, the last `recent`, and the
+                    row_map: Optional[torch.Tensor] = None, dev_err: Optional[torch.Tensor] = None, stream=None,
+                    positions: Optional[torch.Tensor] = None):
+    """Keep `keep` rows of every sequence that holds more: the first `sink`, the `recent` newest, and the
     heaviest of the rest by acc (float32 [B, n_max]); kept rows behind `keep` move, in place, into the rows
     before it that go.  planes: 1 to 4 tensors [B, n_max, width] of any type whose rows move together
-    (e.g. [c_kv, k_r], [c4, kv_scale, k_r]; add acc.unsqueeze(-1) to keep it in step).  Returns
-    (new_lengths int32 [B], which may be given as lengths itself, and row_map int32 [B, keep]: the row
-    that row i held before, -1 from new_lengths[b] on)."""
+    (e.g. [c_kv, k_r], [c4, kv_scale, k_r]; add acc.unsqueeze(-1) to keep it in step).
+    positions: int32 [B, n_max], the position of the token that each row holds; it moves with the rows, and
+    the newest are those of largest position.  Without it the last `recent` rows count as the newest, which
+    is right only while rows stand in order of age: an eviction ends that order, so a cache that is cut more
+    than once needs positions.  Returns (new_lengths int32 [B], which may be given as lengths itself, and
+    row_map int32 [B, keep]: the row that row i held before, -1 from new_lengths[b] on)."""
     n_planes = len(planes)
     if not 1 <= n_planes <= _capi.MAX_PLANES:
         raise ValueError(f"need 1 to {_capi.MAX_PLANES} planes")
@@ -742,6 +746,10 @@ def mla_cache_evict(planes: Sequence[torch.Tensor], acc: torch.Tensor, lengths: 
         raise ValueError("acc must be [B, n_max]")
     B, n_max = lead = tuple(acc.shape)
     acc_b = _weight_array(acc, lead, "acc")
+    pos_b = n_max
+    if positions is not None:
+        strides = _shape(positions, lead, torch.int32, "positions")
+        pos_b = strides[0] if B > 1 else n_max
     _i32(lengths, (B,), "lengths")
     rows, fields = _PLANES(), []
     for i, p in enumerate(planes):
@@ -760,7 +768,7 @@ def mla_cache_evict(planes: Sequence[torch.Tensor], acc: torch.Tensor, lengths: 
     if row_map is not None:
         _i32(row_map, (B, keep), "row_map")
     _flag(dev_err)
-    dev = _on_device(acc, lengths, new_lengths, row_map, dev_err, *planes)
+    dev = _on_device(acc, lengths, new_lengths, row_map, dev_err, positions, *planes)
     on, st = _launch_on(stream, dev)
     with on:
         if new_lengths is None:
@@ -768,9 +776,14 @@ def mla_cache_evict(planes: Sequence[torch.Tensor], acc: torch.Tensor, lengths: 
         if row_map is None:
             wide = max(keep, 0)
             row_map = torch.empty_strided((B, wide), (wide, 1), dtype=torch.int32, device=lengths.device)
-        check(_fn("mla_cache_evict")(B, n_max, rows, n_planes, acc.data_ptr(), acc_b, lengths.data_ptr(), keep, sink,
-                                     recent, new_lengths.data_ptr(), row_map.data_ptr(), _at(dev_err), st),
-              "mla_cache_evict")
+        if positions is None:
+            check(_fn("mla_cache_evict")(B, n_max, rows, n_planes, acc.data_ptr(), acc_b, lengths.data_ptr(), keep, sink,
+                                         recent, new_lengths.data_ptr(), row_map.data_ptr(), _at(dev_err), st),
+                  "mla_cache_evict")
+        else:
+            check(_fn("mla_cache_evict_at")(B, n_max, rows, n_planes, acc.data_ptr(), acc_b, lengths.data_ptr(), keep,
+                                            sink, recent, positions.data_ptr(), pos_b, new_lengths.data_ptr(),
+                                            row_map.data_ptr(), _at(dev_err), st), "mla_cache_evict_at")
     return new_lengths, row_map
 
 

@@ -153,6 +153,7 @@ struct EvictArgs {
   mla_rows planes[MLA_MAX_PLANES];
   const float* acc; int64_t acc_b;
   const int32_t* lengths;
+  int32_t* positions; int64_t pos_b;  // nullptr: the rows stand in order of age
   int32_t* new_lengths;
   int32_t* row_map;
   int32_t* err;

@@ -1,11 +1,17 @@
 // Eviction from a cache by accumulated attention weight.
 //
-// Per sequence with L > keep rows: kept are the first `sink` rows, the last `recent` rows, and the
+// Per sequence with L > keep rows: kept are the first `sink` rows, the `recent` newest rows, and the
 // keep - sink - recent rows of largest accumulated weight among the rest (ties: the lower row; NaN
 // counts as the least).  Attention does not depend on the order of the rows (the rotary key carries
 // each row's position), so nothing is shifted: the kept rows behind `keep` move into the holes before
 // it, j-th hole from j-th row.  That moves the fewest bytes, and since sources lie at or behind `keep` and
 // destinations before it, no row is read after it was written: the move needs no order and no copy.
+//
+// Which rows are the newest: without positions the last ones, which holds while rows stand in order of age.  The move
+// itself ends that order (the newest rows go into holes anywhere), so a cache that is cut again brings its rows'
+// positions, which move along.  The newest are then found by a radix selection of their own, over (position, row),
+// whose keys are all distinct, and enter the selection by weight with a key above every weight's.  The sinks need no
+// positions: the first `sink` rows are always kept and never move.
 //
 // Two launches: the selection writes row_map (a cluster of eight CTAs per sequence, each with a slice of the
 // rows, or one CTA for a short sequence; counts, ranks and the list of moved rows cross through distributed
@@ -14,7 +20,8 @@
 // Bound: the selection by latency, a chain of passes over keys in shared memory, scans and meetings (17 us for 4
 // sequences of up to 32768 rows, 12 for 32 of 4096, alone with cold caches); the move by its bytes, with
 // few warps when few rows move.  Both together, back to back: 4 sequences of 20000 to 32768 rows of 1152 bytes cut to
-// 16384 25 us (63 MB: 2.5 TB/s), 32 sequences of 4-bit rows that lose up to 256 of 4096 12.4 us.
+// 16384 25 us (63 MB: 2.5 TB/s), 32 sequences of 4-bit rows that lose up to 256 of 4096 12.6 us.  With positions 38 and
+// 21 us: one pass for the bits in which positions differ and mostly two for the newest rows.
 #include <math.h>
 
 #include "common.cuh"
@@ -50,6 +57,13 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
+// Rows in order of age as one number; of equal positions the higher row is the newer one.
+constexpr int kRowBits = 19;  // of a row's number
+static_assert(kMaxRows < 1 << kRowBits, "a row's number is the low part of the key");
+__device__ __forceinline__ uint64_t age_key(int32_t position, int row) {
+  return (uint64_t)((uint32_t)position ^ 0x80000000u) << 32 | (uint32_t)row;
+}
+
 // Position of the n-th (from 0) set bit of m.
 __device__ __forceinline__ int nth_bit(uint32_t m, int n) {
   for (; n > 0; --n) m &= m - 1;
@@ -80,6 +94,7 @@ struct SelectSmem {
   uint32_t sums[kPasses<kCluster> + 2][kWarps];
   Found found[2];
   int mine[2];  // this CTA's holes and moved rows
+  int differ;   // bits in which the positions of this CTA's rows differ
 };
 
 // Inclusive prefix sum over the block's threads; the array is written by this call alone.
@@ -117,8 +132,84 @@ __device__ __forceinline__ void meet() {
     sm100::cluster_sync();
 }
 
-// C CTAs (a cluster) per sequence; CTA r has the r-th slice of its rows (whole words of the mask).
+// Clears the counts of an earlier pass, after a later pass's meeting: by then every CTA has read them.
 template <int C>
+__device__ __forceinline__ void clear_counts(int* hist, int pass) {
+  if (pass < 0) return;
+  for (int i = threadIdx.x; i < kBins<C>; i += kThreads) hist[pass % kPasses<C> * kBins<C> + i] = 0;
+}
+
+// The digit that holds the `left`-th largest of the keys counted in the cluster's `count`; every thread of every CTA.
+template <int C>
+__device__ __forceinline__ Found find_digit(const int* count, int left, uint32_t rank, uint32_t (&sums)[kWarps], Found& found) {
+  // thread t sums its digits over the cluster, in descending order, each CTA for itself
+  constexpr int kOwn = kBins<C> > kThreads ? kBins<C> / kThreads : 1;
+  const int top = kBins<C> - 1 - kOwn * (int)threadIdx.x;
+  int n[kOwn] = {}, lower[kOwn] = {}, sum = 0;
+  if (top >= 0) {
+#pragma unroll
+    for (uint32_t r = 0; r < C; ++r)
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) {
+        const int v = C == 1 ? count[top - i] : ld_cluster(&count[top - i], r);
+        n[i] += v;
+        lower[i] += r < rank ? v : 0;
+        sum += v;
+      }
+  }
+  const int x = block_scan(sum, sums);  // the prefix sums find the digit that holds rank `left`
+  int above = x - sum;
+  if (x >= left && above < left) {
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      if (above < left && above + n[i] >= left) found = {top - i, left - above, n[i], lower[i]};
+      above += n[i];
+    }
+  }
+  __syncthreads();
+  return found;
+}
+
+// The age_key of the `recent`-th newest of the sequence's rows from lo on, of which this CTA has [c0, c1); 1 <= recent <=
+// their number.  `pass` counts the passes, which take turns with the kPasses arrays of counts; the last one's is left as
+// it is, since other CTAs may be reading it.
+template <int C>
+__device__ __forceinline__ uint64_t newest_from(const int32_t* positions, int lo, int c0, int c1, int recent, uint32_t rank,
+                                                int* hist, SelectSmem& sm, int& pass) {
+  const int tid = threadIdx.x;
+  const int32_t some = positions[lo];
+  uint32_t differ = 0u;
+  for (int t = c0 + tid; t < c1; t += kThreads) differ |= (uint32_t)(positions[t] ^ some);
+  differ = __reduce_or_sync(0xffffffffu, differ);
+  if ((tid & 31) == 0) atomicOr(&sm.differ, (int)differ);
+  meet<C>();
+  for (uint32_t r = 0; r < C; ++r) differ |= (uint32_t)(C == 1 ? sm.differ : ld_cluster(&sm.differ, r));
+  // from the highest bit in which positions differ; the bits between a position and a row's number are zeros
+  int bits = differ != 0u ? 64 - __clz(differ) : kRowBits, left = recent;
+  uint64_t mask = bits < 64 ? ~uint64_t(0) << bits : 0u, prefix = age_key(some, 0) & mask;
+  for (bool found = false; !found && bits > 0; ++pass) {
+    const int width = min(bits > 32 ? bits - 32 : bits, kDigitBits<C>), shift = bits - width;
+    const uint32_t digit = (1u << width) - 1u;
+    int* count = hist + pass % kPasses<C> * kBins<C>;
+    for (int t = c0 + tid; t < c1; t += kThreads) {
+      const uint64_t key = age_key(positions[t], t);
+      if ((key & mask) == prefix) atomicAdd(&count[(uint32_t)(key >> shift) & digit], 1);
+    }
+    meet<C>();
+    clear_counts<C>(hist, pass - 1);
+    const Found f = find_digit<C>(count, left, rank, sm.sums[pass % kPasses<C>], sm.found[pass & 1]);
+    prefix |= (uint64_t)f.digit << shift;
+    mask |= (uint64_t)digit << shift;
+    left = f.rank;
+    found = f.rows == f.rank;
+    bits = shift > kRowBits && shift <= 32 ? kRowBits : shift;
+  }
+  return prefix;  // (its lower bits are zeros)
+}
+
+// C CTAs (a cluster) per sequence; CTA r has the r-th slice of its rows (whole words of the mask).  kAged: the newest
+// rows by position.
+template <int C, bool kAged>
 __device__ __forceinline__ void select_rows(const EvictArgs& a, bool keys_in_smem) {
   __shared__ SelectSmem sm;
   extern __shared__ __align__(16) int dyn[];
@@ -148,25 +239,35 @@ __device__ __forceinline__ void select_rows(const EvictArgs& a, bool keys_in_sme
   int* list = dyn + (3 * per + 3) / 4 * 4;             // a part of the moved rows, in order
   int* hist = list;  // [kPasses][kBins] this CTA's counts of each digit, before the list is made
   uint32_t* keys = reinterpret_cast<uint32_t*>(list) + list_ints<C>(per);  // [per * 32], where they fit
-  const int lo = a.sink, hi = len - a.recent;          // rows that compete
+  // rows that compete, and how many of them stay (kAged: the newest compete too, with the largest key)
+  const int lo = a.sink, hi = kAged ? len : len - a.recent;
   const int c0 = max(r0, lo), c1 = min(r1, hi);
-  const int want = a.keep - a.sink - a.recent;
+  const int want = a.keep - a.sink - (kAged ? 0 : a.recent);
 
   for (int i = tid; i < kPasses<C> * kBins<C>; i += kThreads) hist[i] = 0;
+  if (kAged && tid == 0) sm.differ = 0;
   __syncthreads();
+  const int32_t* positions = kAged ? a.positions + b * a.pos_b : nullptr;
+  uint64_t newest = 0u;
+  int pass = 0;
+  if constexpr (kAged) newest = newest_from<C>(positions, lo, c0, c1, a.recent, rank, hist, sm, pass);
+  auto row_key = [&](int t, float weight) {
+    if (kAged && age_key(positions[t], t) >= newest) return 0xffffffffu;  // (above that of +infinity)
+    return order_key(weight);
+  };
   // radix select from the top: the want-th largest key, or as much of it as tells the kept rows from the others
   uint32_t prefix = 0u, mask = 0u;
   int left = want;  // keys equal to the prefix still to be taken
   int ties_before = 0;
   bool ties_all = true;  // every row at the threshold is kept
-  for (int pass = 0, bits = 32; bits > 0 && want > 0; ++pass) {
+  for (int bits = 32; bits > 0 && want > 0; ++pass) {
     const int width = min(bits, kDigitBits<C>), shift = bits - width;
     const uint32_t digit = (1u << width) - 1u;
-    int* count = hist + pass * kBins<C>;
+    int* count = hist + (kAged ? pass % kPasses<C> : pass) * kBins<C>;
     for (int f = c0; f < c1; f += kBatch * kThreads) {
       const int t0 = f + tid, some = (c1 - f + kThreads - 1) / kThreads;  // the block has keys in so many of the batch
       uint32_t k[kBatch];
-      if (pass == 0 || !keys_in_smem) {
+      if (bits == 32 || !keys_in_smem) {
         float v[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
@@ -174,7 +275,7 @@ __device__ __forceinline__ void select_rows(const EvictArgs& a, bool keys_in_sme
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
           if (i < some) {
-            k[i] = order_key(v[i]);
+            k[i] = kAged && t0 + i * kThreads >= c1 ? 0u : row_key(t0 + i * kThreads, v[i]);
             if (keys_in_smem && t0 + i * kThreads < c1) keys[t0 + i * kThreads - r0] = k[i];
           }
       } else {
@@ -187,32 +288,8 @@ __device__ __forceinline__ void select_rows(const EvictArgs& a, bool keys_in_sme
         if (i < some && t0 + i * kThreads < c1 && (k[i] & mask) == prefix) atomicAdd(&count[(k[i] >> shift) & digit], 1);
     }
     meet<C>();
-    // thread t sums its digits over the cluster, in descending order, each CTA for itself
-    constexpr int kOwn = kBins<C> > kThreads ? kBins<C> / kThreads : 1;
-    const int top = kBins<C> - 1 - kOwn * tid;
-    int n[kOwn] = {}, lower[kOwn] = {}, sum = 0;
-    if (top >= 0) {
-#pragma unroll
-      for (uint32_t r = 0; r < C; ++r)
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i) {
-          const int v = C == 1 ? count[top - i] : ld_cluster(&count[top - i], r);
-          n[i] += v;
-          lower[i] += r < rank ? v : 0;
-          sum += v;
-        }
-    }
-    const int x = block_scan(sum, sm.sums[pass]);  // the prefix sums find the digit that holds rank `left`
-    int above = x - sum;
-    if (x >= left && above < left) {
-#pragma unroll
-      for (int i = 0; i < kOwn; ++i) {
-        if (above < left && above + n[i] >= left) sm.found[pass & 1] = {top - i, left - above, n[i], lower[i]};
-        above += n[i];
-      }
-    }
-    __syncthreads();
-    const Found f = sm.found[pass & 1];
+    if (kAged) clear_counts<C>(hist, pass - 1);
+    const Found f = find_digit<C>(count, left, rank, sm.sums[kAged ? pass % kPasses<C> : pass], sm.found[pass & 1]);
     prefix |= (uint32_t)f.digit << shift;
     mask |= digit << shift;
     left = f.rank;
@@ -229,7 +306,7 @@ __device__ __forceinline__ void select_rows(const EvictArgs& a, bool keys_in_sme
     for (int i = 0; i < kBatch; ++i) {
       const int t = r0 + (wb + i * kWarps) * kWord + lane;
       k[i] = 0u;
-      if (i < some && t >= c0 && t < c1 && want > 0) k[i] = keys_in_smem ? keys[t - r0] : order_key(acc[t]);
+      if (i < some && t >= c0 && t < c1 && want > 0) k[i] = keys_in_smem ? keys[t - r0] : row_key(t, acc[t]);
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
@@ -332,12 +409,14 @@ __device__ __forceinline__ void select_rows(const EvictArgs& a, bool keys_in_sme
   if (C > 1) meet<C>();  // no CTA leaves while another one may read its part of the list
 }
 
+template <bool kAged>
 __global__ void __launch_bounds__(kThreads) evict_select_one(EvictArgs a, bool keys_in_smem) {
-  select_rows<1>(a, keys_in_smem);
+  select_rows<1, kAged>(a, keys_in_smem);
 }
+template <bool kAged>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     evict_select_cluster(EvictArgs a, bool keys_in_smem) {
-  select_rows<kCluster>(a, keys_in_smem);
+  select_rows<kCluster, kAged>(a, keys_in_smem);
 }
 
 // The rows that move: a CTA compacts kMoveEntries entries of row_map to those that do; a warp copies two rows at a time,
@@ -345,7 +424,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
 // (Entries of a CTA 256, 128, 64, 32: 29, 25, 23, 24 us for 4 sequences cut from 32768 rows to 16384, 12.5, 12.4, 13.3,
 // 15.3 for 32 of 4096 rows that lose a few.)
 constexpr int kMoveThreads = 256, kMoveEntries = 128;
-template <typename V>
+template <typename V, bool kPositions>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a) {
   __shared__ int dst[kMoveEntries], src[kMoveEntries], warp_n[kMoveEntries / 32];
   sm100::griddep_launch_dependents();
@@ -366,6 +445,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a) {
   if (moves) {
     dst[at] = i;
     src[at] = from;
+    if constexpr (kPositions) a.positions[b * a.pos_b + i] = a.positions[b * a.pos_b + from];
   }
   __syncthreads();
   int first[MLA_MAX_PLANES + 1];  // elements of the planes before each one
@@ -407,6 +487,12 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a) {
     }
 }
 
+template <typename V>
+cudaError_t move_launch(const EvictArgs& a, dim3 grid, cudaStream_t st) {
+  return launch_pdl(a.positions != nullptr ? evict_move_kernel<V, true> : evict_move_kernel<V, false>, grid, dim3(kMoveThreads), 0,
+                    st, a);
+}
+
 // Shared memory of a CTA of the selection: masks and counts for each word, the list (or, before it, the
 // counts of the digits) and the keys.
 template <int C>
@@ -430,11 +516,13 @@ cudaError_t evict_launch(const EvictArgs& a, cudaStream_t st) {
   const auto bytes = one ? select_smem_bytes<1> : select_smem_bytes<kCluster>;
   const bool keys = bytes(a.n_max, true) <= kSelectSmem;
   const size_t smem = bytes(a.n_max, keys);
-  static int allowed_one[kMaxDevices], allowed_cluster[kMaxDevices];
-  cudaError_t e = one ? allow_smem(reinterpret_cast<const void*>(evict_select_one), kSelectSmem, allowed_one)
-                      : allow_smem(reinterpret_cast<const void*>(evict_select_cluster), kSelectSmem, allowed_cluster);
+  const bool aged = a.positions != nullptr && a.recent > 0;
+  const auto kernel = one ? aged ? evict_select_one<true> : evict_select_one<false>
+                          : aged ? evict_select_cluster<true> : evict_select_cluster<false>;
+  static int allowed[4][kMaxDevices];
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), kSelectSmem, allowed[2 * one + aged]);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(one ? evict_select_one : evict_select_cluster, dim3(a.B * (one ? 1 : kCluster)), dim3(kThreads), smem, st, a, keys);
+  e = launch_pdl(kernel, dim3(a.B * (one ? 1 : kCluster)), dim3(kThreads), smem, st, a, keys);
   if (e != cudaSuccess) return e;
   // the widest element that every plane's base, strides and rows are multiples of
   uintptr_t bits = 0;
@@ -442,9 +530,9 @@ cudaError_t evict_launch(const EvictArgs& a, cudaStream_t st) {
     bits |= reinterpret_cast<uintptr_t>(a.planes[p].base) | (uintptr_t)a.planes[p].bstride |
             (uintptr_t)a.planes[p].rstride | (uintptr_t)a.planes[p].row_bytes;
   const dim3 grid((a.keep + kMoveEntries - 1) / kMoveEntries, a.B);
-  if (bits % 16 == 0) return launch_pdl(evict_move_kernel<uint4>, grid, dim3(kMoveThreads), 0, st, a);
-  if (bits % 4 == 0) return launch_pdl(evict_move_kernel<uint32_t>, grid, dim3(kMoveThreads), 0, st, a);
-  return launch_pdl(evict_move_kernel<uint8_t>, grid, dim3(kMoveThreads), 0, st, a);
+  if (bits % 16 == 0) return move_launch<uint4>(a, grid, st);
+  if (bits % 4 == 0) return move_launch<uint32_t>(a, grid, st);
+  return move_launch<uint8_t>(a, grid, st);
 }
 
 }  // namespace mla

@@ -711,9 +711,10 @@ mla_status mla_cache_weights_fp4kv(mla_dims dims, mla_dtype dtype, int32_t B, in
   return cuda_status(e, "mla_cache_weights_fp4kv launch");
 }
 
-mla_status mla_cache_evict(int32_t B, int32_t n_max, const mla_rows* planes, int32_t n_planes, const float* acc,
-                           int64_t acc_bstride, const int32_t* lengths, int32_t keep, int32_t sink, int32_t recent,
-                           int32_t* new_lengths, int32_t* row_map, int32_t* dev_err, void* stream) {
+mla_status mla_cache_evict_at(int32_t B, int32_t n_max, const mla_rows* planes, int32_t n_planes, const float* acc,
+                              int64_t acc_bstride, const int32_t* lengths, int32_t keep, int32_t sink, int32_t recent,
+                              int32_t* positions, int64_t pos_bstride, int32_t* new_lengths, int32_t* row_map,
+                              int32_t* dev_err, void* stream) {
   g_msg[0] = 0;
   if (B <= 0 || n_max <= 0) return fail(MLA_ERR_INVALID_ARG, "B and n_max must be positive");
   if (B > 65535) return fail(MLA_ERR_UNSUPPORTED, "B must not exceed 65535");
@@ -726,6 +727,8 @@ mla_status mla_cache_evict(int32_t B, int32_t n_max, const mla_rows* planes, int
   if (sink < 0 || recent < 0 || (int64_t)sink + recent > keep)
     return fail(MLA_ERR_INVALID_ARG, "sink and recent must be >= 0 with a sum of at most keep");
   if (acc_bstride < n_max && B > 1) return fail(MLA_ERR_INVALID_ARG, "acc batch stride smaller than n_max");
+  if (positions && pos_bstride < n_max && B > 1)
+    return fail(MLA_ERR_INVALID_ARG, "positions batch stride smaller than n_max");
   mla::EvictArgs a;
   int64_t row_bytes = 0;
   for (int p = 0; p < n_planes; ++p) {
@@ -739,8 +742,16 @@ mla_status mla_cache_evict(int32_t B, int32_t n_max, const mla_rows* planes, int
   if (row_bytes > 1 << 30) return fail(MLA_ERR_UNSUPPORTED, "a row of all planes must not exceed 2^30 bytes");
   a.B = B; a.n_max = n_max; a.n_planes = n_planes; a.keep = keep; a.sink = sink; a.recent = recent;
   a.acc = acc; a.acc_b = acc_bstride; a.lengths = lengths; a.new_lengths = new_lengths; a.row_map = row_map;
+  a.positions = positions; a.pos_b = pos_bstride;
   a.err = dev_err;
   return cuda_status(mla::evict_launch(a, static_cast<cudaStream_t>(stream)), "mla_cache_evict launch");
+}
+
+mla_status mla_cache_evict(int32_t B, int32_t n_max, const mla_rows* planes, int32_t n_planes, const float* acc,
+                           int64_t acc_bstride, const int32_t* lengths, int32_t keep, int32_t sink, int32_t recent,
+                           int32_t* new_lengths, int32_t* row_map, int32_t* dev_err, void* stream) {
+  return mla_cache_evict_at(B, n_max, planes, n_planes, acc, acc_bstride, lengths, keep, sink, recent, nullptr, 0,
+                            new_lengths, row_map, dev_err, stream);
 }
 
 mla_status mla_check_topk(int32_t B, const int32_t* topk_idx, int32_t topk, const int32_t* lengths, int32_t n_max,

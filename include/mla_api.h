@@ -487,6 +487,9 @@ typedef struct {
  * least).  The kept rows at and behind `keep` move into the rows before it that go, in ascending order each; all
  * other rows stay where they are.  Attention does not depend on the order of the rows; the next token
  * of the sequence goes to row new_lengths[b] (mla_cache_append_at, mla_cache_append_fp4).
+ * The last rows are the newest tokens only while rows stand in order of age, as appends leave them.  The move
+ * itself ends that order: a cache that is cut again needs mla_cache_evict_at, or its newest tokens lose their
+ * protection.  (The first `sink` rows are always kept and never move.)
  *   planes      HOST array of 1 .. MLA_MAX_PLANES row arrays that move together (c_kv and k_r; c8, kv_scale
  *               and k_r; c4, kv_scale and k_r; acc itself as 4-byte rows, to keep it in step)
  *   acc         float, element (b, t) at acc[b*acc_bstride + t] (mla_cache_weights)
@@ -501,6 +504,21 @@ mla_status mla_cache_evict(int32_t B, int32_t n_max, const mla_rows* planes, int
                            const float* acc, int64_t acc_bstride, const int32_t* lengths,
                            int32_t keep, int32_t sink, int32_t recent, int32_t* new_lengths, int32_t* row_map,
                            int32_t* dev_err, void* stream);
+
+/*
+ * mla_cache_evict_at - mla_cache_evict with the position of each row given apart from its row, for any number
+ * of evictions of one cache: kept are the first `sink` rows, of the rows behind them the `recent` rows of
+ * largest position (of equal positions the higher row), and of the rest the rows of largest acc.
+ *   positions   DEVICE int32, element (b, t) at positions[b*pos_bstride + t]: the position of the token in row t
+ *               (what mla_cache_append_at and mla_cache_append_fp4 got with it), for t < lengths[b]; moved
+ *               with the rows, in place, beside the planes.  NULL: mla_cache_evict
+ *   Other arguments as in mla_cache_evict.  Asynchronous on `stream`.
+ */
+mla_status mla_cache_evict_at(int32_t B, int32_t n_max, const mla_rows* planes, int32_t n_planes,
+                              const float* acc, int64_t acc_bstride, const int32_t* lengths,
+                              int32_t keep, int32_t sink, int32_t recent, int32_t* positions,
+                              int64_t pos_bstride, int32_t* new_lengths, int32_t* row_map,
+                              int32_t* dev_err, void* stream);
 
 /*
  * mla_check_topk - opt-in validation of a top-k index array before a sparse decode.  The pages'

@@ -70,13 +70,17 @@ def token_weights(q_tilde, q_pe, c_kv, k_r, scale: float, lse):
     return w
 
 
-def evict_map(acc, length: int, keep: int, sink: int, recent: int):
-    """The rows that rows 0 .. min(length, keep) - 1 held before the eviction."""
+def evict_map(acc, length: int, keep: int, sink: int, recent: int, positions=None):
+    """The rows that rows 0 .. min(length, keep) - 1 held before the eviction.  positions: of each row's token
+    (None: rows in order of age)."""
     if length <= keep:
         return list(range(length))
     w = [float(v) for v in acc[:length]]
-    rank = sorted(range(sink, length - recent), key=lambda t: (np.isnan(w[t]), -w[t] if w[t] == w[t] else 0.0, t))
-    held = set(range(sink)) | set(range(length - recent, length)) | set(rank[:keep - sink - recent])
+    age = range(length) if positions is None else [int(p) for p in positions[:length]]
+    by_age = sorted(range(sink, length), key=lambda t: (age[t], t))
+    newest, rest = by_age[len(by_age) - recent:], by_age[:len(by_age) - recent]
+    rank = sorted(rest, key=lambda t: (np.isnan(w[t]), -w[t] if w[t] == w[t] else 0.0, t))
+    held = set(range(sink)) | set(newest) | set(rank[:keep - sink - recent])
     late = [t for t in range(keep, length) if t in held]
     holes = [i for i in range(keep) if i not in held]
     assert len(late) == len(holes)
