@@ -340,7 +340,9 @@ __device__ __forceinline__ PartSource part_source(const Args& p, int b, int len,
           p.kv.sc + b * p.kv.sc_b + t * p.kv.sc_r + 16 * region + 2 * (lane & 7), 4 * p.kv.c4_r, 4 * p.kv.sc_r,
           (int)(len - t)};
 }
-// Loads the source's keys; those of the other half of the features, too, lie `half` halves away.
+// Loads the source's keys; those of the other half of the features, too, lie `half` halves away.  (Plain loads: the append
+// or eviction before this kernel may still be writing rows when it starts, so the cache is not read-only for the kernel's
+// lifetime, as a load through the non-coherent path requires.)
 template <int G>
 __device__ __forceinline__ void load_part(const PartSource& s, int half, Part<G>& k) {
 #pragma unroll
@@ -348,8 +350,8 @@ __device__ __forceinline__ void load_part(const PartSource& s, int half, Part<G>
     k.code[i] = make_uint4(0u, 0u, 0u, 0u);
     k.scale[i] = 0u;
     if (4 * i < s.left) {  // rows behind the sequence may hold anything, or not exist
-      k.code[i] = __ldg(reinterpret_cast<const uint4*>(s.code + i * s.code4 + 128 * half));
-      k.scale[i] = __ldg(reinterpret_cast<const uint16_t*>(s.scale + i * s.scale4 + 16 * half));
+      k.code[i] = *reinterpret_cast<const uint4*>(s.code + i * s.code4 + 128 * half);
+      k.scale[i] = *reinterpret_cast<const uint16_t*>(s.scale + i * s.scale4 + 16 * half);
     }
   }
 }
@@ -384,7 +386,7 @@ __device__ __forceinline__ void store_part(const Part<G>& k, uint32_t dst, int j
 __device__ __forceinline__ void load_rope(const uint8_t*& src, int64_t rows4, int left, uint4 (&k)[16]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i)
-    k[i] = 4 * i < left ? __ldg(reinterpret_cast<const uint4*>(src + i * rows4)) : make_uint4(0u, 0u, 0u, 0u);
+    k[i] = 4 * i < left ? *reinterpret_cast<const uint4*>(src + i * rows4) : make_uint4(0u, 0u, 0u, 0u);
   src += kTile / 4 * rows4;
 }
 __device__ __forceinline__ void store_rope(const uint4 (&k)[16], uint32_t dst, int lane) {

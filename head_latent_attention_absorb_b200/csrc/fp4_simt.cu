@@ -98,8 +98,7 @@ __device__ __forceinline__ float score(const QueryArgs& a, const Query<T, NB>& q
 }
 
 template <typename T, int NB>
-__global__ void __launch_bounds__(32 * kWarps) decode_fp4_simt(Fp4DecodeArgs a, int n_splits, float* __restrict__ ws_o,
-                                                               float2* __restrict__ ws_ml) {
+__global__ void __launch_bounds__(32 * kWarps) decode_fp4_simt(Fp4DecodeArgs a, int n_splits, float* ws_o, float2* ws_ml) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   sm100::griddep_launch_dependents();
   sm100::griddep_wait();
@@ -178,10 +177,10 @@ __global__ void __launch_bounds__(32 * kWarps) decode_fp4_simt(Fp4DecodeArgs a, 
     a.lse[row] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
-// One CTA per query row: the splits' factors once, then features with eight splits' loads under way.
+// One CTA per query row: the splits' factors once, then features with eight splits' loads under way.  (The partials are
+// not __restrict__: the decode writes them while this kernel may have started, so they are not read-only for its lifetime.)
 template <typename T>
-__global__ void __launch_bounds__(128) combine_fp4_simt(Fp4DecodeArgs a, int n_splits, const float* __restrict__ ws_o,
-                                                        const float2* __restrict__ ws_ml) {
+__global__ void __launch_bounds__(128) combine_fp4_simt(Fp4DecodeArgs a, int n_splits, const float* ws_o, const float2* ws_ml) {
   __shared__ float factor[kMaxSplits];
   sm100::griddep_launch_dependents();
   sm100::griddep_wait();

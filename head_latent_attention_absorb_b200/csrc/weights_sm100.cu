@@ -123,9 +123,10 @@ __device__ __forceinline__ KeySource key_source(const Params& p, int b, int64_t 
           static_cast<const uint8_t*>(p.kv.k_r) + 2 * (b * p.kv.kr_b + u * p.kv.kr_r) + 16 * (lane & 7),
           (int)(len - t), (int)(len - u)};
 }
-// Rows behind the sequence may hold anything, or not exist: they are zeros.
+// Rows behind the sequence may hold anything, or not exist: they are zeros.  (Plain loads: the kernel before this one may
+// still be writing the cache when this one starts, which a load through the non-coherent path does not allow.)
 __device__ __forceinline__ uint4 load_row(const uint8_t* src, bool present) {
-  return present ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0u, 0u, 0u, 0u);
+  return present ? *reinterpret_cast<const uint4*>(src) : make_uint4(0u, 0u, 0u, 0u);
 }
 __device__ __forceinline__ void load_codes(const Params& p, const KeySource& s, int pair, KeyPart& k) {
 #pragma unroll
