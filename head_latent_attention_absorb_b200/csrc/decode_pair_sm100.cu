@@ -790,13 +790,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // first 24 score K-steps); both lane halves hold every head of this CTA
       if (nseg > 0 && !wait_or_fail(smem_u32(&sm.q_empty), (nseg - 1) & 1u)) break;
       {
+        // (plain loads: the projection before this kernel may still be writing the query when it starts)
         const uint4* qt = reinterpret_cast<const uint4*>(p.q_tilde + ((int64_t)b * kNH + h) * p.ldqt + 192 * wsub);
 #pragma unroll
         for (int cc = 0; cc < 3; ++cc) {
           uint32_t r[32];
 #pragma unroll
           for (int v = 0; v < 8; ++v) {
-            const uint4 u = __ldg(qt + 8 * cc + v);
+            const uint4 u = qt[8 * cc + v];
             r[4 * v] = u.x; r[4 * v + 1] = u.y; r[4 * v + 2] = u.z; r[4 * v + 3] = u.w;
           }
           tmem_st32(tmem + lane_off + kColQ + 96 * wsub + 32 * cc, r);

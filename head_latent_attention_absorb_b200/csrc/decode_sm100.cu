@@ -1134,6 +1134,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       } else {
+        // (plain loads: the projection before this kernel may still be writing the query when it starts)
         const __nv_bfloat16* qt = p.q_tilde + ((int64_t)b * kNH + h) * p.ldqt + 256 * rank;
         const __nv_bfloat16* qp = p.q_pe + ((int64_t)b * kNH + h) * p.ldqp + 32 * rank;
 #pragma unroll
@@ -1142,7 +1143,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           uint32_t r[32];
 #pragma unroll
           for (int v = 0; v < 8; ++v) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(qt + c * 64) + v);
+            const uint4 u = reinterpret_cast<const uint4*>(qt + c * 64)[v];
             r[4 * v] = u.x; r[4 * v + 1] = u.y; r[4 * v + 2] = u.z; r[4 * v + 3] = u.w;
           }
           tmem_st32(tQ + c * 32, r);
@@ -1151,7 +1152,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           uint32_t r16[16];
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(qp) + v);
+            const uint4 u = reinterpret_cast<const uint4*>(qp)[v];
             r16[4 * v] = u.x; r16[4 * v + 1] = u.y; r16[4 * v + 2] = u.z; r16[4 * v + 3] = u.w;
           }
           tmem_st16(tQ + 128, r16);
