@@ -132,6 +132,7 @@ struct Piece {
   int b, g, len;         // its sequence, group of query rows, and the sequence's length
   int begin, n;          // first tile, tiles
   int slot, c0, pieces;  // where its partial goes; first pair and number of the item's pieces
+  int hiding;            // its first tile, from `begin` on, with a key that the group's first row does not see
 };
 
 struct Smem {
@@ -229,6 +230,7 @@ __device__ __noinline__ void next_piece(const Args& p, int c, Plan& s, Piece& r)
   r.b = p.groups == 1 ? r.item : r.item / p.groups;
   r.g = r.item - r.b * p.groups;
   r.len = p.lengths[r.b];
+  r.hiding = p.T == 1 ? 0x7fffffff : (r.len - p.T + (kRows * r.g) / p.n_h + 1) / kTile - r.begin;
 }
 
 // One warp: the share of pair c and its first piece.
@@ -360,6 +362,14 @@ __device__ __forceinline__ void next_tile(PartSource& s) {
   s.scale += kTile / 4 * s.scale4;
   s.left -= kTile;
 }
+// A key that some query rows do not see gets the probability 0 from them, but 0 times a NaN value is NaN.  So in tiles with
+// such keys (Piece::hiding) NaN scales count as 0, and the rotary row of their key is NaN instead, which makes the key's
+// scores NaN for the rows that do see it.
+template <int G>
+__device__ __forceinline__ void drop_nan(Part<G>& k) {
+#pragma unroll
+  for (int i = 0; i < G; ++i) k.scale[i] &= ~(((((k.scale[i] & 0x7f7fu) + 0x0101u) & 0x8080u) >> 7) * 0xffu);
+}
 // Decodes into the region at `dst`, keys 4 G j on.
 template <int G>
 __device__ __forceinline__ void store_part(const Part<G>& k, uint32_t dst, int j, int lane) {
@@ -394,8 +404,18 @@ __device__ __forceinline__ void store_rope(const uint4 (&k)[16], uint32_t dst, i
 #pragma unroll
   for (int i = 0; i < 16; ++i)
     st_shared_v4_b32(dst + 512 * i + (((lane & 7) ^ (lane >> 3) ^ (4 * (i & 1))) << 4), k[i].x, k[i].y, k[i].z, k[i].w);
-  fence_proxy_async_smem();
-  __syncwarp();
+}
+// The rotary chunks of keys with a NaN among their scales, of which a lane looks at four, become NaN; `t`, `left` as above.
+__device__ __noinline__ void mark_nan(const Args& p, int b, int t, int left, uint32_t dst, int lane) {
+  const uint8_t* src = p.kv.sc + b * p.kv.sc_b + t * p.kv.sc_r + 4 * (lane & 7);
+  dst += (lane >> 3) * 128;
+#pragma unroll 1
+  for (int i = 0; i < 16 && 4 * i < left; ++i) {
+    const uint32_t s = *reinterpret_cast<const uint32_t*>(src + 4 * i * p.kv.sc_r);
+    if (((s & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u)
+      st_shared_v4_b32(dst + 512 * i + (((lane & 7) ^ (lane >> 3) ^ (4 * (i & 1))) << 4), 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u,
+                       0x7fc07fc0u);
+  }
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -736,6 +756,10 @@ __device__ __noinline__ bool key_role(Smem& sm, const Piece& w, uint32_t it0, ui
     if (!wait_warp(sm, sm.x_empty[xb], ((it / kXBufs) & 1u) ^ 1u, p.err)) return false;
     // (the first use of the third buffer: the query has left it)
     if (t == 2 && !wait_warp(sm, sm.q_placed, parity, p.err)) return false;
+    if ((int)t >= w.hiding) {
+      drop_nan(x);
+      drop_nan(y);
+    }
     store_part(x, base + xb * kRegion, j, lane);
     if (lane == 0) arrive_even(sm.x_full[xb], rank);
     next_tile(src);
@@ -761,6 +785,7 @@ __device__ __noinline__ bool value_role(Smem& sm, const Piece& w, uint32_t it0) 
   for (uint32_t t = 0; t < n; ++t) {
     const uint32_t it = it0 + t;
     if (!wait_warp(sm, sm.s_full[it & 1u], (it >> 1) & 1u, p.err)) return false;
+    if ((int)t >= w.hiding) drop_nan(v);
     store_part(v, base + (rank == 0 ? kYOff + it % kYBufs * kRegion : it % kXBufs * kRegion), j, lane);
     if (lane == 0) arrive_even(sm.v_full[it & 1u], rank);
     next_tile(src);
@@ -784,6 +809,9 @@ __device__ __noinline__ bool rope_role(Smem& sm, const Piece& w, uint32_t it0) {
   for (uint32_t t = 0; t < n; ++t) {
     if (!wait_warp(sm, sm.rope_empty, ((it0 + t) & 1u) ^ 1u, p.err)) return false;
     store_rope(k, base + kRopeOff, lane);
+    if ((int)t >= w.hiding) mark_nan(p, w.b, keys + (int)t * kTile + (lane >> 3), left, base + kRopeOff, lane);
+    fence_proxy_async_smem();
+    __syncwarp();
     if (lane == 0) arrive_even(sm.rope_full, rank);
     left -= kTile;
     load_rope(src, 8 * p.kv.kr_r, left, k);

@@ -424,7 +424,8 @@ size_t mla_decode_fp4kv_workspace_size(mla_dims dims, mla_dtype dtype, int32_t B
  *   z_t = scale * (q_tilde . c[t, :] + q_pe . k_r[t, :])
  *   q_tilde, q_pe, ctx_out, lse_out  query rows (b * T + s) * n_h + h, as in mla_decode_absorb_multi
  *   lengths  DEVICE int32 [B] in [T, n_max]; another length sets MLA_ERR_LENGTH and the sequence's tokens
- *            get ctx = 0, lse = -inf.  Rows at and behind lengths[b] may hold anything.
+ *            get ctx = 0, lse = -inf.  Rows at and behind lengths[b] may hold anything, and a row that holds NaN makes
+ *            NaN only the tokens that see it.
  *   workspace  at least mla_decode_fp4kv_workspace_size() bytes, 16-byte aligned, no initialisation;
  *            calls that may overlap need one each
  *   B * T <= 65535, and ceil(n_h T / 128) B ceil(n_max / 128) < 2^31.  Sequences may share one cache (batch
