@@ -384,7 +384,8 @@ mla_status mla_cache_append_at(mla_dims dims, mla_dtype dtype, int32_t B,
  *   kv_a       element (b, i, j) at kv_a[b*lda_b + i*lda + j]; j < d_c latent, then d_r rotary
  *   positions  DEVICE int32 [B]: position of each sequence's first new token
  *   rows       DEVICE int32 [B]: cache row of it, or NULL: rows = positions
- *   counts     DEVICE int32 [B]: tokens of each sequence in [0, T], or NULL: T everywhere
+ *   counts     DEVICE int32 [B]: tokens of each sequence in [0, T], or NULL: T everywhere; of a sequence's
+ *              rows of kv_a only the first counts[b] are read, and always the first one
  *   Device flag: counts[b] outside [0, T] sets MLA_ERR_LENGTH (the sequence writes nothing); a row outside
  *   [0, n_max) or a negative position sets MLA_ERR_INDEX (that token is not written).  Every other
  *   cache row is left as it was.  B * T < 2^31.  Asynchronous on `stream`.
