@@ -7,6 +7,8 @@
 #include <stdint.h>
 #include <stdlib.h>
 
+#include <atomic>
+
 #include "mla_api.h"
 
 namespace mla {
@@ -166,21 +168,29 @@ inline int current_device() {
   cudaGetDevice(&dev);
   return dev >= 0 && dev < kMaxDevices ? dev : 0;
 }
+// What is looked up once per device, in static storage (0: not yet).  Any thread may look it up, and all find the same, so
+// the accesses need no order.
+struct PerDevice {
+  std::atomic<int> value[kMaxDevices];
+  int get(int dev) const { return value[dev].load(std::memory_order_relaxed); }
+  void set(int dev, int v) { value[dev].store(v, std::memory_order_relaxed); }
+};
 inline int sm_count() {
-  static int cache[kMaxDevices] = {};
+  static PerDevice cache;
   const int dev = current_device();
-  if (cache[dev] == 0) {
-    int n = 0;
-    cache[dev] = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0 ? n : 148;
+  int n = cache.get(dev);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
+    cache.set(dev, n);
   }
-  return cache[dev];
+  return n;
 }
 // Raises a kernel's dynamic shared memory limit, once per device; `allowed` is the kernel's own record.
-inline cudaError_t allow_smem(const void* kernel, int bytes, int (&allowed)[kMaxDevices]) {
+inline cudaError_t allow_smem(const void* kernel, int bytes, PerDevice& allowed) {
   const int dev = current_device();
-  if (allowed[dev] >= bytes) return cudaSuccess;
+  if (allowed.get(dev) >= bytes) return cudaSuccess;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) allowed[dev] = bytes;
+  if (e == cudaSuccess) allowed.set(dev, bytes);
   return e;
 }
 

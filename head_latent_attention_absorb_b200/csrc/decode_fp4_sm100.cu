@@ -1021,9 +1021,9 @@ int shape_pairs(int pairs, int n_h, int B, int T, int n_max) {
 }
 // Pairs that are resident at once (a GPC with an odd number of SMs leaves one over): one wave.  Per device.
 int resident_pairs() {
-  static int cache[kMaxDevices] = {};
+  static PerDevice cache;
   const int dev = current_device();
-  if (cache[dev] > 0) return cache[dev];
+  if (cache.get(dev) > 0) return cache.get(dev);
   int pairs = max_pairs(), active = 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs);
@@ -1032,7 +1032,7 @@ int resident_pairs() {
   if (cudaOccupancyMaxActiveClusters(&active, decode_kernel, &cfg) == cudaSuccess && active > 0 && active < pairs)
     pairs = active;
   cudaGetLastError();  // a failed query leaves no sticky state
-  cache[dev] = pairs;
+  cache.set(dev, pairs);
   return pairs;
 }
 size_t table_bytes(int n_h, int B, int T) { return (size_t)B * (((size_t)n_h * T + kRows - 1) / kRows) * sizeof(int4); }
@@ -1057,7 +1057,7 @@ cudaError_t decode_fp4_tc_launch(const Fp4DecodeArgs& a, void* ws, cudaStream_t 
   p.groups = (p.R + kRows - 1) / kRows;
   if (!query_map(&params.tm_q, a.q_tilde, kDC, p.R, a.B, a.ldqt) || !query_map(&params.tm_qp, a.q_pe, kDR, p.R, a.B, a.ldqp))
     return cudaErrorInvalidValue;
-  static int allowed[kMaxDevices];
+  static PerDevice allowed;
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(decode_kernel), kSmemBytes, allowed);
   if (e != cudaSuccess) return e;
   p.pairs = shape_pairs(resident_pairs(), a.n_h, a.B, a.T, a.n_max);

@@ -1832,10 +1832,11 @@ struct Wave {
   bool one_wave;
 };
 Wave grid_wave() {
-  static Wave cache[64] = {};
+  static PerDevice cache;  // 2 clusters + one_wave
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev >= 0 && dev < 64 && cache[dev].clusters > 0) return cache[dev];
+  const bool known = dev >= 0 && dev < kMaxDevices;
+  if (const int c = known ? cache.get(dev) : 0) return {c / 2, c % 2 != 0};
   const int upper = max_clusters();
   Wave w{upper, false};
   if (cudaFuncSetAttribute(decode_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes()) ==
@@ -1851,7 +1852,7 @@ Wave grid_wave() {
     }
   }
   cudaGetLastError();  // a failed query leaves no sticky state
-  if (dev >= 0 && dev < 64) cache[dev] = w;
+  if (known) cache.set(dev, 2 * w.clusters + w.one_wave);
   return w;
 }
 

@@ -519,7 +519,7 @@ cudaError_t evict_launch(const EvictArgs& a, cudaStream_t st) {
   const bool aged = a.positions != nullptr && a.recent > 0;
   const auto kernel = one ? aged ? evict_select_one<true> : evict_select_one<false>
                           : aged ? evict_select_cluster<true> : evict_select_cluster<false>;
-  static int allowed[4][kMaxDevices];
+  static PerDevice allowed[4];
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), kSelectSmem, allowed[2 * one + aged]);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kernel, dim3(a.B * (one ? 1 : kCluster)), dim3(kThreads), smem, st, a, keys);

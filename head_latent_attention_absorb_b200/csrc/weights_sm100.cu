@@ -407,7 +407,7 @@ bool make_cache_map(CUtensorMap* m, const void* base, int width, int n_max, int 
 
 template <bool kFp4>
 cudaError_t launch(const Params& p, int grid, cudaStream_t st) {
-  static int allowed[kMaxDevices];
+  static PerDevice allowed;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(weights_kernel<kFp4>), kSmemBytes, allowed);
   if (e != cudaSuccess) return e;
   return launch_pdl(weights_kernel<kFp4>, dim3(grid), dim3(kFp4 ? kThreadsFp4 : kThreadsBf16), kSmemBytes, st, p);
