@@ -328,6 +328,8 @@ mla_status mla_prefill_naive(mla_dims dims, mla_dtype dtype, int32_t B, int32_t 
  *   k_r        pair i of k_r[b*kr_bstride + p_b*kr_rstride + :] = (y[2i] + j y[2i+1]) exp(j p_b base^(-2i/d_r)),
  *              y = kv_a[b, d_c:d_c+d_r]: interleaved pairs, base = rope_base (10000 in DeepSeek-V3)
  *   Every other cache row is left as it was.  d_r must be even; eps >= 0; rope_base > 0.
+ *   Types and widths: MLA_BF16 with d_c = 512, d_r = 64 and 1 <= n_h <= 128; MLA_F32 with n_h, d_c <= 1024,
+ *   d_r <= 128.  The heads do not enter, and d_h and d_v are not read: a rank appends with its own heads' dims.
  *   Device flag: a position outside [0, n_max) sets MLA_ERR_INDEX and that sequence writes nothing.
  * Asynchronous on `stream`.
  */
