@@ -1,4 +1,4 @@
-// CUDA-core kernels of the 4-bit decode and of the attention-weight pass, generic in the dimensions.
+// CUDA-core kernels of the 4-bit decode and of the attention-weight pass in fp32, generic in the dimensions.
 //
 //   decode   z[h,t] = scale (q~_h . c_t + q_pe,h . k^R_t), softmax over t <= length - T + s,
 //            ctx_h = sum_t p c_t, lse = log sum exp z      (split over the rows, merged by a second pass)
@@ -6,7 +6,7 @@
 //
 // One warp per (head, query, split) in the decode and per cached row in the weights; lane l owns the
 // 16-feature blocks l and l + 32 of a latent row, so a 4-bit row costs a lane one 8-byte load and
-// one scale per block.  They carry the fp32 element type for any dimensions.
+// one scale per block.
 //
 // Bound: latency, at the few rows and heads that fp32 is used with: a row is a chain of loads, a sum across the warp
 // and an exponential, so a warp of the decode takes four rows at once and the splits are short.  3 sequences of 64 to
@@ -28,8 +28,8 @@ constexpr int kAhead = 4;      // rows that a warp of the decode works on at onc
 constexpr int kRowsSplit = 16;
 constexpr int kMaxSplits = 64;
 
-// The lane's blocks of latent row t of sequence b (kFp4: decoded; otherwise in the element type).
-template <typename T, int NB, bool kFp4>
+// The lane's blocks of latent row t of sequence b (kFp4: decoded; otherwise as it is).
+template <int NB, bool kFp4>
 __device__ __forceinline__ void load_row(const QueryArgs& a, int b, int t, int lane, float (&c)[NB][16]) {
   const int blocks = (a.d_c + fp4::kBlock - 1) / fp4::kBlock;
 #pragma unroll
@@ -55,36 +55,36 @@ __device__ __forceinline__ void load_row(const QueryArgs& a, int b, int t, int l
         }
       }
     } else {
-      const T* src = static_cast<const T*>(a.kv.c_kv) + b * a.kv.ckv_b + t * a.kv.ckv_r + 16 * blk;
+      const float* src = static_cast<const float*>(a.kv.c_kv) + b * a.kv.ckv_b + t * a.kv.ckv_r + 16 * blk;
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        if (16 * blk + i < a.d_c) c[k][i] = to_f32(src[i]);
+        if (16 * blk + i < a.d_c) c[k][i] = src[i];
     }
   }
 }
 
 // A lane's features of query row r.
-template <typename T, int NB>
+template <int NB>
 struct Query {
   float c[NB][16], pe[4];  // d_r <= 128
   __device__ __forceinline__ void load(const QueryArgs& a, int64_t r, int lane) {
-    const T* q = static_cast<const T*>(a.q_tilde) + r * a.ldqt;
-    const T* qp = static_cast<const T*>(a.q_pe) + r * a.ldqp;
+    const float* q = static_cast<const float*>(a.q_tilde) + r * a.ldqt;
+    const float* qp = static_cast<const float*>(a.q_pe) + r * a.ldqp;
 #pragma unroll
     for (int k = 0; k < NB; ++k)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int f = 16 * (lane + 32 * k) + i;
-        c[k][i] = f < a.d_c ? to_f32(q[f]) : 0.f;
+        c[k][i] = f < a.d_c ? q[f] : 0.f;
       }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) pe[i] = lane + 32 * i < a.d_r ? to_f32(qp[lane + 32 * i]) : 0.f;
+    for (int i = 0; i < 4; ++i) pe[i] = lane + 32 * i < a.d_r ? qp[lane + 32 * i] : 0.f;
   }
 };
 
 // scale (q~ . c_t + q_pe . k^R_t), summed over the warp.  (load_row leaves zeros past d_c.)
-template <typename T, int NB>
-__device__ __forceinline__ float score(const QueryArgs& a, const Query<T, NB>& q, const T* k_row, int lane,
+template <int NB>
+__device__ __forceinline__ float score(const QueryArgs& a, const Query<NB>& q, const float* k_row, int lane,
                                        const float (&c)[NB][16]) {
   float dot = 0.f;
 #pragma unroll
@@ -93,11 +93,11 @@ __device__ __forceinline__ float score(const QueryArgs& a, const Query<T, NB>& q
     for (int i = 0; i < 16; ++i) dot = fmaf(q.c[k][i], c[k][i], dot);
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (lane + 32 * i < a.d_r) dot = fmaf(q.pe[i], to_f32(k_row[lane + 32 * i]), dot);
+    if (lane + 32 * i < a.d_r) dot = fmaf(q.pe[i], k_row[lane + 32 * i], dot);
   return warp_sum(dot) * a.scale;
 }
 
-template <typename T, int NB>
+template <int NB>
 __global__ void __launch_bounds__(32 * kWarps) decode_fp4_simt(Fp4DecodeArgs a, int n_splits, float* ws_o, float2* ws_ml) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   sm100::griddep_launch_dependents();
@@ -118,18 +118,18 @@ __global__ void __launch_bounds__(32 * kWarps) decode_fp4_simt(Fp4DecodeArgs a, 
   for (int k = 0; k < NB; ++k)
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[k][i] = 0.f;
-  Query<T, NB> query;
+  Query<NB> query;
   query.load(a, r, lane);
   float m = -INFINITY, l = 0.f;
   // four rows at a time: their loads and sums overlap, and the running maximum is settled once
   for (int t = t0; t < t1; t += kAhead) {
     float c[kAhead][NB][16], z[kAhead];
 #pragma unroll
-    for (int e = 0; e < kAhead; ++e) load_row<T, NB, true>(a, b, min(t + e, t1 - 1), lane, c[e]);
+    for (int e = 0; e < kAhead; ++e) load_row<NB, true>(a, b, min(t + e, t1 - 1), lane, c[e]);
 #pragma unroll
     for (int e = 0; e < kAhead; ++e) {
       const int row = min(t + e, t1 - 1);
-      z[e] = score<T, NB>(a, query, static_cast<const T*>(a.kv.k_r) + b * a.kv.kr_b + row * a.kv.kr_r, lane, c[e]);
+      z[e] = score<NB>(a, query, static_cast<const float*>(a.kv.k_r) + b * a.kv.kr_b + row * a.kv.kr_r, lane, c[e]);
     }
     float m_new = m;
 #pragma unroll
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(32 * kWarps) decode_fp4_simt(Fp4DecodeArgs a, 
       const int f = 16 * (lane + 32 * k) + i;
       if (f >= a.d_c) continue;
       if (whole)
-        static_cast<T*>(a.ctx)[row * a.d_c + f] = from_f32<T>(acc[k][i] * inv);
+        static_cast<float*>(a.ctx)[row * a.d_c + f] = acc[k][i] * inv;
       else
         ws_o[row * a.d_c + f] = acc[k][i];
     }
@@ -179,7 +179,6 @@ __global__ void __launch_bounds__(32 * kWarps) decode_fp4_simt(Fp4DecodeArgs a, 
 
 // One CTA per query row: the splits' factors once, then features with eight splits' loads under way.  (The partials are
 // not __restrict__: the decode writes them while this kernel may have started, so they are not read-only for its lifetime.)
-template <typename T>
 __global__ void __launch_bounds__(128) combine_fp4_simt(Fp4DecodeArgs a, int n_splits, const float* ws_o, const float2* ws_ml) {
   __shared__ float factor[kMaxSplits];
   sm100::griddep_launch_dependents();
@@ -214,12 +213,12 @@ __global__ void __launch_bounds__(128) combine_fp4_simt(Fp4DecodeArgs a, int n_s
       for (int i = 0; i < 8; ++i)
         if (s0 + i < n_splits && factor[s0 + i] != 0.f) acc = fmaf(factor[s0 + i], v[i], acc);
     }
-    static_cast<T*>(a.ctx)[r * a.d_c + c] = from_f32<T>(acc * inv);
+    static_cast<float*>(a.ctx)[r * a.d_c + c] = acc * inv;
   }
   if (a.lse != nullptr && threadIdx.x == 0) a.lse[r] = L == 0.f ? -INFINITY : M + logf(L);
 }
 
-template <typename T, int NB, bool kFp4>
+template <int NB, bool kFp4>
 __global__ void __launch_bounds__(32 * kWarps) weights_simt(WeightsArgs a) {
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5), b = blockIdx.y;
@@ -230,17 +229,17 @@ __global__ void __launch_bounds__(32 * kWarps) weights_simt(WeightsArgs a) {
   }
   if (t >= len) return;
   float c[NB][16];
-  load_row<T, NB, kFp4>(a, b, t, lane, c);
-  const T* k_row = static_cast<const T*>(a.kv.k_r) + b * a.kv.kr_b + t * a.kv.kr_r;
+  load_row<NB, kFp4>(a, b, t, lane, c);
+  const float* k_row = static_cast<const float*>(a.kv.k_r) + b * a.kv.kr_b + t * a.kv.kr_r;
   float w = 0.f;
   // new token s sees rows t <= len - T + s
   for (int s = max(0, t - (len - a.T)); s < a.T; ++s)
     for (int h = 0; h < a.n_h; ++h) {
       const int64_t r = ((int64_t)b * a.T + s) * a.n_h + h;
       const float lse = a.lse[r];
-      Query<T, NB> query;
+      Query<NB> query;
       query.load(a, r, lane);
-      const float z = score<T, NB>(a, query, k_row, lane, c);
+      const float z = score<NB>(a, query, k_row, lane, c);
       if (lse != -INFINITY) w += expf(z - lse);  // a row without a softmax gave no weight
     }
   if (lane != 0) return;
@@ -269,10 +268,10 @@ cudaError_t decode_fp4_simt_launch(const Fp4DecodeArgs& a, void* ws, cudaStream_
   float* ws_o = static_cast<float*>(ws);
   float2* ws_ml = reinterpret_cast<float2*>(ws_o + (size_t)splits * q * a.n_h * a.d_c);
   const dim3 grid((a.n_h + kWarps - 1) / kWarps, q, splits);
-  const cudaError_t e = launch_pdl(a.d_c <= 512 ? decode_fp4_simt<float, 1> : decode_fp4_simt<float, 2>, grid,
+  const cudaError_t e = launch_pdl(a.d_c <= 512 ? decode_fp4_simt<1> : decode_fp4_simt<2>, grid,
                                    dim3(32 * kWarps), 0, st, a, splits, ws_o, ws_ml);
   if (e != cudaSuccess || splits == 1) return e;
-  return launch_pdl(combine_fp4_simt<float>, dim3(a.n_h, q), dim3(128), 0, st, a, splits, (const float*)ws_o,
+  return launch_pdl(combine_fp4_simt, dim3(a.n_h, q), dim3(128), 0, st, a, splits, (const float*)ws_o,
                     (const float2*)ws_ml);
 }
 
@@ -280,11 +279,10 @@ cudaError_t weights_simt_launch(const WeightsArgs& a, cudaStream_t st) {
   const dim3 grid((a.n_max + kWarps - 1) / kWarps, a.B);
   const bool fp4 = a.kv.c4 != nullptr;
   if (a.d_c <= 512)
-    (fp4 ? weights_simt<float, 1, true> : weights_simt<float, 1, false>)<<<grid, 32 * kWarps, 0, st>>>(a);
+    (fp4 ? weights_simt<1, true> : weights_simt<1, false>)<<<grid, 32 * kWarps, 0, st>>>(a);
   else
-    (fp4 ? weights_simt<float, 2, true> : weights_simt<float, 2, false>)<<<grid, 32 * kWarps, 0, st>>>(a);
+    (fp4 ? weights_simt<2, true> : weights_simt<2, false>)<<<grid, 32 * kWarps, 0, st>>>(a);
   return cudaGetLastError();
 }
-
 
 }  // namespace mla
