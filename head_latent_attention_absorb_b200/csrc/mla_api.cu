@@ -89,12 +89,16 @@ mla_status check_fp4(const mla_dims& d, mla_dtype dt, const void* c4, int64_t c4
   return MLA_OK;
 }
 
+// Cached rows that the 4-bit decode and the attention weights count in 32 bits, rounded up to tiles and splits
+constexpr int32_t kMaxCacheRows = INT32_MAX - 1023;
+
 // Query rows and rotary rows of the 4-bit decode and of the attention weights
 mla_status check_queries(const mla_dims& d, mla_dtype dt, int32_t B, int32_t T, const void* q_tilde, int64_t ldqt,
                          const void* q_pe, int64_t ldqp, const void* k_r, int64_t kr_b, int64_t kr_r, int32_t n_max,
                          const int32_t* lengths, float scale) {
   if (B <= 0 || T < 1 || n_max <= 0 || T > n_max) return fail(MLA_ERR_INVALID_ARG, "need B > 0 and 1 <= T <= n_max");
   if ((int64_t)B * T > 65535) return fail(MLA_ERR_UNSUPPORTED, "B * T must not exceed 65535");
+  if (n_max > kMaxCacheRows) return fail(MLA_ERR_UNSUPPORTED, "n_max must not exceed %d", kMaxCacheRows);
   if (!q_tilde || !q_pe || !k_r || !lengths) return fail(MLA_ERR_INVALID_ARG, "NULL pointer");
   if (ldqt < d.d_c || ldqp < d.d_r) return fail(MLA_ERR_INVALID_ARG, "query row stride too small");
   if (kr_r < d.d_r || kr_b < 0) return fail(MLA_ERR_INVALID_ARG, "cache stride too small");
@@ -623,7 +627,9 @@ mla_status mla_cache_read_fp4(mla_dims dims, mla_dtype dtype, int32_t B, int32_t
 }
 
 size_t mla_decode_fp4kv_workspace_size(mla_dims dims, mla_dtype dtype, int32_t B, int32_t T, int32_t n_max) {
-  if (check_cache_dims(dims, dtype, true) != MLA_OK || B <= 0 || T < 1 || n_max < T || (int64_t)B * T > 65535) return 0;
+  if (check_cache_dims(dims, dtype, true) != MLA_OK || B <= 0 || T < 1 || n_max < T || n_max > kMaxCacheRows ||
+      (int64_t)B * T > 65535)
+    return 0;
   return dtype == MLA_BF16 ? mla::decode_fp4_tc_workspace(dims.n_h, B, T, n_max)
                            : mla::decode_fp4_simt_workspace(dims.n_h, dims.d_c, B * T, n_max);
 }

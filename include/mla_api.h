@@ -431,7 +431,7 @@ size_t mla_decode_fp4kv_workspace_size(mla_dims dims, mla_dtype dtype, int32_t B
  *            NaN only the tokens that see it.
  *   workspace  at least mla_decode_fp4kv_workspace_size() bytes, 16-byte aligned, no initialisation;
  *            calls that may overlap need one each
- *   B * T <= 65535, and ceil(n_h T / 128) B ceil(n_max / 128) < 2^31.  Sequences may share one cache (batch
+ *   B * T <= 65535, n_max <= 2^31 - 1024, and ceil(n_h T / 128) B ceil(n_max / 128) < 2^31.  Sequences may share one cache (batch
  *   strides 0).  A bounded wait that runs out sets MLA_ERR_TIMEOUT.  Asynchronous on `stream`.
  */
 mla_status mla_decode_absorb_fp4kv(mla_dims dims, mla_dtype dtype, int32_t B, int32_t T,
@@ -456,7 +456,8 @@ mla_status mla_decode_absorb_fp4kv(mla_dims dims, mla_dtype dtype, int32_t B, in
  *   decay    >= 0 and finite; 1 sums over all steps
  *   lengths  DEVICE int32 [B] in [T, n_max]; another length sets MLA_ERR_LENGTH and writes nothing
  *   Sums over heads and tokens are in fp32, in a fixed order.  Types and widths: MLA_BF16 with
- *   d_c = 512, d_r = 64, 1 <= n_h <= 128; MLA_F32 with n_h, d_c <= 1024, d_r <= 128.  B * T <= 65535.
+ *   d_c = 512, d_r = 64, 1 <= n_h <= 128; MLA_F32 with n_h, d_c <= 1024, d_r <= 128.  B * T <= 65535,
+ *   n_max <= 2^31 - 1024.
  *   A bounded wait that runs out sets MLA_ERR_TIMEOUT.
  * mla_cache_weights_fp4kv reads the 4-bit cache instead.  Asynchronous on `stream`.
  */
