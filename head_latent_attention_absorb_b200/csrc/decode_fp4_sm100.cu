@@ -5,8 +5,8 @@
 //
 // Bound: the tensor pipe.  A cached row costs 2 R (2 d_c + d_r) operations against 416 bytes: at R = 128
 // 669 a byte, far right of the GPU's ridge.  Measured (one call, replayed in a graph): B = 32, N = 4096, 128 heads
-// 51 us, 716 TFLOP/s; B = 8, 1024 to 65536 rows 84 us; 32 query rows (16 heads, 2 tokens), B = 32, up to 8191 rows
-// 55 us, a quarter of each MMA's rows in use; B = 1, N = 1000 18.2 us.  A tile of 128 keys takes a pair 4000 cycles, 2190
+// 51.7 us, 706 TFLOP/s; B = 8, 1024 to 65536 rows 85 us; 32 query rows (16 heads, 2 tokens), B = 32, up to 8191 rows
+// 56 us, a quarter of each MMA's rows in use; B = 1, N = 1000 18.4 us.  A tile of 128 keys takes a pair 4000 cycles, 2190
 // of them in the MMAs: the loop from a released buffer over the decode of its next keys, the scores and the softmax
 // to the values crosses between the CTAs four times.  Some 17 us of a call lie outside its tiles: work split and
 // query (8), the end of the pipeline and the partials (6), the join (3).

@@ -8,10 +8,11 @@
 //
 // One warp per token: lane l owns blocks l and l + 32, so the block maximum never leaves the lane, and
 // only the sum of squares crosses the warp (five shuffles).  A token is 1152 bytes read and 416 written in bf16,
-// but a prompt is bound by the instructions and latencies of the quantisation: 13,300 tokens take 16.5 us and
-// their read-back 9.4 us (each alone, cold caches; 39 and 31 % of the issue slots, 1.3 and 1.9 TB/s), together 19 us
-// back to back.  The next token's row is on its way while one is quantised.  32 single tokens: 4.7 us with the
-// read-back, latency.
+// but a prompt is bound by the instructions and latencies of the quantisation: 11,551 tokens in a batch of four prompts
+// padded to 4095 take 16.0 us and their read-back, with its zeros, 9.2 us (each alone, cold caches; 39 and 31 % of the
+// issue slots, 1.1 and 2.2 TB/s), together 18.7 us back to back.  The next token's row is on its way while one is
+// quantised.  32 single tokens: 4.9 us with the read-back, latency.  fp32 rows, loaded and stored element by element:
+// 2000 tokens of 640 features 7.9 us, their read-back 10.3.
 //
 // A 4-bit code is a step of up to a third of its value, so a value next to a rounding border has to
 // fall on the side that the formula puts it on.  The fp32 pass carries a relative error below
@@ -194,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 8 : 4) append_fp4_kernel(c
   }
   // the next token's row and indices are on their way while a token is worked on.  Rows of padding are not read: a
   // padded batch would pay for them, and there may be no memory there.  (A sequence's first row is there, and does not
-  // wait for the count: 32 single tokens 4.8 us instead of 5.0.)
+  // wait for the count: 32 single tokens 4.9 us instead of 5.1.)
   struct Token {
     Raw<T> raw[NB];
     const T* row;

@@ -494,7 +494,8 @@ typedef struct {
  * of the sequence goes to row new_lengths[b] (mla_cache_append_at, mla_cache_append_fp4).
  * The last rows are the newest tokens only while rows stand in order of age, as appends leave them.  The move
  * itself ends that order: a cache that is cut again needs mla_cache_evict_at, or its newest tokens lose their
- * protection.  (The first `sink` rows are always kept and never move.)
+ * protection.  (The first `sink` rows are always kept and never move.)  Several new tokens of a sequence have to be its
+ * last rows for their decode and their weights: evict before they are appended or after both.
  *   planes      HOST array of 1 .. MLA_MAX_PLANES row arrays that move together (c_kv and k_r; c8, kv_scale
  *               and k_r; c4, kv_scale and k_r; acc itself as 4-byte rows, to keep it in step)
  *   acc         float, element (b, t) at acc[b*acc_bstride + t] (mla_cache_weights)
