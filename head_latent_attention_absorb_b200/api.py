@@ -482,11 +482,22 @@ def mla_cache_append(dims, kv_a: torch.Tensor, positions: torch.Tensor, c_kv: to
                                      _ptr(c_kv), c_kv.stride(0), c_kv.stride(1), _ptr(k_r), k_r.stride(0),
                                      k_r.stride(1), _ptr(dev_err), _stream(stream)), "mla_cache_append")
         return
+    dtype = kv_a.dtype
+    if kv_a.shape[1] < d.d_c + d.d_r:
+        raise ValueError("kv_a must be [B, d_c + d_r]")
+    c = _shape(c_kv, (B, n_max, d.d_c), dtype, "c_kv")
+    k = _shape(k_r, (B, n_max, d.d_r), dtype, "k_r")
+    _i32(positions, (B,), "positions")
     _i32(rows, (B,), "rows")
-    check(lib().mla_cache_append_at(d, _dt(kv_a), B, _ptr(kv_a), kv_a.stride(0), _ptr(gain), float(eps),
-                                    float(rope_base), _ptr(positions), _ptr(rows), n_max,
-                                    _ptr(c_kv), c_kv.stride(0), c_kv.stride(1), _ptr(k_r), k_r.stride(0),
-                                    k_r.stride(1), _ptr(dev_err), _stream(stream)), "mla_cache_append_at")
+    if gain is not None:
+        _shape(gain, (d.d_c,), torch.float32, "gain")
+    _flag(dev_err)
+    on, st = _launch_on(stream, _on_device(kv_a, positions, rows, c_kv, k_r, gain, dev_err))
+    with on:
+        check(_fn("mla_cache_append_at")(
+            d, _dtc(dtype), B, kv_a.data_ptr(), kv_a.stride(0), _at(gain), eps, rope_base, positions.data_ptr(),
+            rows.data_ptr(), n_max, c_kv.data_ptr(), c[0], c[1], k_r.data_ptr(), k[0], k[1], _at(dev_err), st),
+            "mla_cache_append_at")
 
 
 def mla_check_topk(topk_idx: torch.Tensor, n_max: int, lengths: Optional[torch.Tensor] = None,

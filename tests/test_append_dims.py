@@ -1,8 +1,9 @@
 """Which dimensions mla_cache_append and mla_cache_append_at take: the heads do not enter, so a rank's share of them will do."""
 
 import pytest
+import torch
 
-from head_latent_attention_absorb_b200 import _capi
+from head_latent_attention_absorb_b200 import _capi, api
 from head_latent_attention_absorb_b200.build import build
 
 P = 0x10000  # an aligned non-NULL address; no call below passes validation
@@ -37,3 +38,22 @@ def test_dimensions(L, at, dims, dt, want):
     status = call(L, at, dims, dt)
     assert status in (INVALID, UNSUPPORTED)
     assert want in L.mla_last_error_message().decode(), L.mla_last_error_message()
+
+
+def _append_at(**kw):
+    a = dict(x=torch.zeros((2, 80)), pos=torch.zeros(2, dtype=torch.int32), c=torch.zeros((2, 16, 64)), k=torch.zeros((2, 16, 16)),
+             rows=torch.zeros(2, dtype=torch.int32), gain=None, err=None)
+    a.update(kw)
+    api.mla_cache_append((4, 64, 16, 32, 32), a["x"], a["pos"], a["c"], a["k"], gain=a["gain"], rows=a["rows"], dev_err=a["err"])
+
+
+@pytest.mark.parametrize("kw,kind,match", [
+    (dict(pos=torch.zeros(1, dtype=torch.int32)), TypeError, "positions"), (dict(rows=torch.zeros(1, dtype=torch.int32)), TypeError, "rows"),
+    (dict(x=torch.zeros((2, 79))), ValueError, "kv_a"), (dict(x=torch.zeros((1, 80))), ValueError, "kv_a"),
+    (dict(c=torch.zeros((2, 16, 48))), ValueError, "c_kv"), (dict(c=torch.zeros((2, 16, 64), dtype=torch.bfloat16)), TypeError, "c_kv"),
+    (dict(k=torch.zeros((2, 15, 16))), ValueError, "k_r"), (dict(k=torch.zeros((1, 16, 16))), ValueError, "k_r"),
+    (dict(k=torch.zeros((2, 16, 16), dtype=torch.bfloat16)), TypeError, "k_r"), (dict(gain=torch.ones(63)), ValueError, "gain"),
+    (dict(err=torch.zeros(1)), TypeError, "dev_err"), (dict(), ValueError, "CUDA tensor")])
+def test_binding_refuses_what_would_leave_its_arrays(kw, kind, match):
+    with pytest.raises(kind, match=match):
+        _append_at(**kw)

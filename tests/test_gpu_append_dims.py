@@ -23,3 +23,17 @@ def test_rows_do_not_depend_on_the_heads(dtype, d_c, d_r, heads):
     for n_h in heads:
         for d_h in (0, 128):
             assert torch.equal(rows(n_h, d_h), want)
+
+
+def test_rows_apart_from_positions_on_another_stream():
+    x = torch.randn((3, 576), device="cuda").to(torch.bfloat16)
+    pos, at = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([9000, 7, 3], [1, 0, 5]))
+    want = torch.zeros((3, 8, 576), dtype=torch.bfloat16, device="cuda")
+    api.mla_cache_append((16, 512, 64, 128, 128), x, pos, want[..., :512], want[..., 512:], rows=at)
+    st = torch.cuda.Stream()
+    for stream in (st, st.cuda_stream):
+        got = torch.zeros_like(want)
+        torch.cuda.synchronize()
+        api.mla_cache_append((16, 512, 64, 128, 128), x, pos, got[..., :512], got[..., 512:], rows=at, stream=stream)
+        st.synchronize()
+        assert torch.equal(got, want) and bool((want[1, 0] != 0).any())
