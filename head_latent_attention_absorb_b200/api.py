@@ -648,6 +648,8 @@ def mla_decode_absorb_fp4kv(dims, q_tilde: torch.Tensor, q_pe: torch.Tensor, c4:
         _shape(lse, q_tilde.shape[:-1], torch.float32, "lse")
         if not lse.is_contiguous():
             raise ValueError("ctx and lse must be contiguous")
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     _flag(dev_err)
     dev = _on_device(q_tilde, q_pe, c4, kv_scale, k_r, lengths, ctx, lse, workspace, dev_err)
     on, st = _launch_on(stream, dev)
